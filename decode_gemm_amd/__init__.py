@@ -23,7 +23,8 @@ __all__ = [
     "expand_direct", "split_count", "run_pipeline_noalloc", "noalloc_scratch_bytes", "bundle_write", "bundle_open",
     "bundle_items", "bundle_plans", "load_bundle", "variant_by_name",
     "DERR_BADCODE", "DERR_CHUNKLEN", "DERR_RAWINDEX", "STATUS", "Proj", "MlpLayer", "proj", "mlp_layers", "mlp_stack_workspace",
-    "mlp_stack_forward",
+    "mlp_stack_forward", "F32", "BF16", "fp8_quantize", "fp8_swiglu", "fp8_gemm", "fp8_gemm_workspace", "sample",
+    "sample_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libuw.so")
@@ -33,6 +34,8 @@ STATUS = {0: "UW_OK", 1: "UW_EINVAL", 2: "UW_ESHAPE", 3: "UW_EFORMAT", 4: "UW_ER
 OK, EINVAL, ESHAPE, EFORMAT, ERANGE, ENOSPACE, EHIP, EUNSUPPORTED, EINTERNAL = range(9)
 W_BF16, W_EXP, W_IDX, W_DIRECT = 0, 1, 2, 3
 PIPE_FULL, PIPE_EXP, PIPE_TRANSCODE, PIPE_DIRECT, PIPE_EXPAND = 0, 1, 2, 3, 4
+F32, BF16 = 0, 1
+FP8_GROUP = 128
 PIPELINE_NAMES = {0: "full", 1: "exp", 2: "transcode", 3: "direct", 4: "expand"}
 DERR_BADCODE, DERR_CHUNKLEN, DERR_RAWINDEX = 1, 2, 4
 
@@ -109,6 +112,25 @@ class TuneArgs(ctypes.Structure):
         ("variant_mask", ctypes.c_int32), ("d_scrub", ctypes.c_void_p), ("scrub_bytes", ctypes.c_size_t),
         ("rot", ctypes.POINTER(Proj)), ("n_rot", ctypes.c_int32), ("trials", ctypes.c_int32),
         ("tune_split", ctypes.c_int32),
+    ]
+
+
+class Fp8GemmArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("d_x", ctypes.c_void_p),
+        ("ldx", ctypes.c_int64), ("d_sx", ctypes.c_void_p), ("ldsx", ctypes.c_int64), ("d_w", ctypes.c_void_p),
+        ("ldw", ctypes.c_int64), ("d_sw", ctypes.c_void_p), ("ldsw", ctypes.c_int64), ("d_y", ctypes.c_void_p),
+        ("ldy", ctypes.c_int64), ("y_type", ctypes.c_int32), ("d_ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
+    ]
+
+
+class SampleArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("V", ctypes.c_int64), ("d_logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+        ("type", ctypes.c_int32), ("d_u", ctypes.c_void_p), ("d_temperature", ctypes.c_void_p),
+        ("d_top_k", ctypes.c_void_p), ("d_top_p", ctypes.c_void_p), ("d_min_p", ctypes.c_void_p),
+        ("d_token", ctypes.c_void_p), ("d_prob", ctypes.c_void_p), ("d_ws", ctypes.c_void_p),
+        ("ws_bytes", ctypes.c_size_t),
     ]
 
 
@@ -197,6 +219,12 @@ def _load():
         "uw_stream_cu_count": ([P, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
         "uw_stream_read": ([P, ctypes.c_size_t, P, P], ctypes.c_int),
         "uw_expand_direct": ([H, P, P, P], ctypes.c_int),
+        "uw_fp8_quantize": ([P, i32, i64, i64, i64, i32, P, i64, P, i64, P], ctypes.c_int),
+        "uw_fp8_swiglu": ([P, i64, P, i64, i64, i64, P, i64, P, i64, P], ctypes.c_int),
+        "uw_fp8_gemm": ([ctypes.POINTER(Fp8GemmArgs), P], ctypes.c_int),
+        "uw_fp8_gemm_workspace": ([i64, i64, i64], sz),
+        "uw_sample": ([ctypes.POINTER(SampleArgs), P], ctypes.c_int),
+        "uw_sample_workspace": ([i64, i64], sz),
     }
     for name, (args, res) in sigs.items():
         f = getattr(L, name)
@@ -380,6 +408,77 @@ def autotune(h: Header, d_blob, d_x, d_y, Ms, d_direct=None, d_ws=None, ws_bytes
 
 def swiglu(d_g, d_u, d_h, n: int, stream=None) -> None:
     _check(lib.uw_swiglu(_ptr(d_g), _ptr(d_u), n, _ptr(d_h), _stream(stream)))
+
+
+def _type(t, given):
+    """uw_type of a tensor's elements (bf16 also carried as 16-bit integers); a raw address needs it given."""
+    if given is not None:
+        return given
+    name = str(getattr(t, "dtype", ""))
+    if name == "torch.float32":
+        return F32
+    if name in ("torch.bfloat16", "torch.int16", "torch.uint16"):
+        return BF16
+    raise ValueError(f"type must be given for {name or 'a raw address'}: F32 or BF16")
+
+
+def _launch(t, call, stream):
+    """call(stream) with the device of t current and, without a stream, that device's current one."""
+    if t is None or isinstance(t, int) or not t.is_cuda:
+        return _check(call(_stream(stream)))
+    import torch
+
+    if t.device.index == torch.cuda.current_device():
+        return _check(call(_stream(stream)))
+    with torch.cuda.device(t.device):
+        return _check(call(_stream(stream)))
+
+
+def fp8_quantize(d_x, d_q, d_s, M: int, K: int, block_rows: int = 1, x_type: int | None = None, ldx: int | None = None,
+                 ldq: int | None = None, lds: int | None = None, stream=None) -> None:
+    """uw_fp8_quantize: e4m3 codes and fp32 scales of X [M][K], one scale per 128 values of a row
+    (block_rows 1, scales [ceil(K / 128)][lds]) or per 128 x 128 block (block_rows 128, scales
+    [ceil(M / 128)][lds]). x_type follows a tensor's dtype unless given."""
+    st = lds if lds is not None else M if block_rows == 1 else (K + 127) // 128
+    _launch(d_x, lambda s: lib.uw_fp8_quantize(_ptr(d_x), _type(d_x, x_type), M, K, K if ldx is None else ldx, block_rows,
+                                               _ptr(d_q), K if ldq is None else ldq, _ptr(d_s), st, s), stream)
+
+
+def fp8_swiglu(d_g, d_u, d_q, d_s, M: int, K: int, ldg: int | None = None, ldu: int | None = None,
+               ldq: int | None = None, lds: int | None = None, stream=None) -> None:
+    """uw_fp8_swiglu: silu(g) * u of fp32 g and u, as e4m3 codes and row scales."""
+    _launch(d_g, lambda s: lib.uw_fp8_swiglu(_ptr(d_g), K if ldg is None else ldg, _ptr(d_u), K if ldu is None else ldu, M,
+                                             K, _ptr(d_q), K if ldq is None else ldq, _ptr(d_s),
+                                             M if lds is None else lds, s), stream)
+
+
+def fp8_gemm_workspace(M: int, N: int, K: int) -> int:
+    return lib.uw_fp8_gemm_workspace(M, N, K)
+
+
+def fp8_gemm(d_x, d_sx, d_w, d_sw, d_y, M: int, N: int, K: int, ldx: int | None = None, ldsx: int | None = None,
+             ldw: int | None = None, ldsw: int | None = None, ldy: int | None = None, y_type: int | None = None,
+             d_ws=None, ws_bytes: int = 0, stream=None) -> None:
+    """uw_fp8_gemm: Y [M][N] (fp32 or bf16, by the dtype of d_y unless y_type is given) from codes and
+    scales of X and W. d_ws: fp8_gemm_workspace(M, N, K) bytes; without it K is never cut."""
+    a = Fp8GemmArgs(M, N, K, _ptr(d_x), K if ldx is None else ldx, _ptr(d_sx), M if ldsx is None else ldsx, _ptr(d_w),
+                    K if ldw is None else ldw, _ptr(d_sw), (K + 127) // 128 if ldsw is None else ldsw, _ptr(d_y),
+                    N if ldy is None else ldy, _type(d_y, y_type), _ptr(d_ws), ws_bytes)
+    _launch(d_x, lambda s: lib.uw_fp8_gemm(ctypes.byref(a), s), stream)
+
+
+def sample_workspace(M: int, V: int) -> int:
+    return lib.uw_sample_workspace(M, V)
+
+
+def sample(d_logits, d_u, d_token, M: int, V: int, ld: int | None = None, type: int | None = None, d_temperature=None,
+           d_top_k=None, d_top_p=None, d_min_p=None, d_prob=None, d_ws=None, ws_bytes: int = 0, stream=None) -> None:
+    """uw_sample: one token (int32) per row of logits [M][V] (fp32 or bf16, by dtype unless type is
+    given) for the uniform numbers d_u [M]; settings are device arrays of M or None. d_prob (optional)
+    receives the drawn token's probability. d_ws: sample_workspace(M, V) bytes."""
+    a = SampleArgs(M, V, _ptr(d_logits), V if ld is None else ld, _type(d_logits, type), _ptr(d_u), _ptr(d_temperature),
+                   _ptr(d_top_k), _ptr(d_top_p), _ptr(d_min_p), _ptr(d_token), _ptr(d_prob), _ptr(d_ws), ws_bytes)
+    _launch(d_logits, lambda s: lib.uw_sample(ctypes.byref(a), s), stream)
 
 
 def proj(h: Header, d_blob, pipeline: int = PIPE_DIRECT, d_direct=None, variant: int = -1, split_k: int = 0) -> Proj:

@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libuw.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
-HIP_SOURCES = ["uw_decode.hip", "uw_gemm.hip", "uw_runtime.hip"]
+HIP_SOURCES = ["uw_decode.hip", "uw_gemm.hip", "uw_runtime.hip", "uw_fp8.hip", "uw_fp8_gemm.hip", "uw_sample.hip"]
 HOST_SOURCES = ["uw_host.cpp", "uw_bundle.cpp"]
 # Packed fp32 VALU forms are kept out of the generated code.
 HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang",

@@ -1,0 +1,302 @@
+// The 8-bit block-scaled path: quantizers to e4m3 codes with one fp32 scale per 128 values of
+// a row or per 128 x 128 block, and the activation between the MLP projections that ends in
+// such codes. (The matrix product that reads them is in uw_fp8_gemm.hip.)
+#include <hip/hip_runtime.h>
+
+#include <cfloat>
+
+#include "uw_internal.h"
+#include "uw_recon.h"
+
+namespace uw {
+
+namespace {
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+constexpr int kG = UW_FP8_GROUP;
+constexpr float kTop = 448.0f;  // largest e4m3 value
+
+// 8 consecutive values of a row, from k on; values at and past K read as 0.
+__device__ __forceinline__ void load8(const uint16_t* p, int64_t k, int64_t K, float (&v)[8])
+{
+    if (k + 8 <= K) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p + k);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = k + i < K ? __uint_as_float(static_cast<uint32_t>(p[k + i]) << 16) : 0.f;
+    }
+}
+
+__device__ __forceinline__ void load8(const float* p, int64_t k, int64_t K, float (&v)[8])
+{
+    if (k + 8 <= K) {
+        const floatx4 a = *reinterpret_cast<const floatx4*>(p + k), b = *reinterpret_cast<const floatx4*>(p + k + 4);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = k + i < K ? p[k + i] : 0.f;
+    }
+}
+
+// Largest |v| among the finite values (0 if there is none): NaN and infinities are passed over,
+// so one of them does not change what the other values of its group become.
+__device__ __forceinline__ float amax8(const float (&v)[8])
+{
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float t = fabsf(v[i]);
+        a = fmaxf(a, t <= FLT_MAX ? t : 0.f);
+    }
+    return a;
+}
+
+// Maximum over the 16 lanes of a DPP row (rotations by 8, 4, 2 and 1 within the row).
+__device__ __forceinline__ float row_max16(float a)
+{
+#define UW_ROW_MAX(ctrl) \
+    a = fmaxf(a, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(a), ctrl, 0xF, 0xF, false)))
+    UW_ROW_MAX(0x128);
+    UW_ROW_MAX(0x124);
+    UW_ROW_MAX(0x122);
+    UW_ROW_MAX(0x121);
+#undef UW_ROW_MAX
+    return a;
+}
+
+__device__ __forceinline__ float scale_of(float a) { return a == 0.f ? 1.f : fmaxf(a / kTop, FLT_MIN); }
+
+// Eight codes of v / s. The quotient is the correctly rounded one: r = 1 / s is, and one
+// residual step (x - y s, exact in an fma) corrects y = x r by the last bit where it is off
+// (s >= 2^-126 keeps r finite; only where the residual itself is below the smallest normal
+// number may the quotient's last fp32 bit stay off). Three operations instead of a division's
+// ten. The one rounding to fewer bits is the conversion's, to nearest even.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s, float r)
+{
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float q = v[i] * r;
+        const float e = __builtin_fmaf(-q, s, v[i]);
+        const float t = __builtin_amdgcn_fmed3f(__builtin_fmaf(e, r, q), -kTop, kTop);
+        y[i] = fabsf(v[i]) <= FLT_MAX ? t : __uint_as_float(0x7FC00000u);
+    }
+    uint2 o;
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    o.x = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
+    o.y = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], w, true);
+    return o;
+}
+
+// Codes k .. k+7 of a row (those before K).
+__device__ __forceinline__ void store8(uint8_t* q, int64_t k, int64_t K, const uint2& c)
+{
+    if (k + 8 <= K) {
+        *reinterpret_cast<uint2*>(q + k) = c;
+    } else {
+        for (int i = 0; i < 8; i++)
+            if (k + i < K) q[k + i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+    }
+}
+
+struct QuantArgs {
+    const void* x;   // values (gate for the activation)
+    const float* u;  // up (activation only)
+    int64_t ldx, ldu, M, K;
+    uint8_t* q;
+    float* s;
+    int64_t ldq, lds;
+    uint32_t tiles_k;  // workgroups along K
+};
+
+template <class T>
+struct LoadX {
+    __device__ static void row(const QuantArgs& a, int64_t m, int64_t k, float (&v)[8])
+    {
+        load8(static_cast<const T*>(a.x) + m * a.ldx, k, a.K, v);
+    }
+};
+
+struct LoadSwiglu {
+    __device__ static void row(const QuantArgs& a, int64_t m, int64_t k, float (&v)[8])
+    {
+        float g[8], u[8];
+        load8(static_cast<const float*>(a.x) + m * a.ldx, k, a.K, g);
+        load8(a.u + m * a.ldu, k, a.K, u);
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = silu_mul(g[i], u[i]);
+    }
+};
+
+// Row groups: 16 lanes hold one group's 128 values, eight each, so the group's maximum is a
+// DPP row reduction and nothing passes through LDS. A workgroup of 256 threads covers ROWS rows
+// x (16 / ROWS) x STEP groups.
+template <class Load, int ROWS, int STEP>
+__global__ void __launch_bounds__(256) quantize_rows(QuantArgs a)
+{
+    constexpr int GC = 16 / ROWS;  // groups side by side
+    const uint32_t tk = blockIdx.x % a.tiles_k, tm = blockIdx.x / a.tiles_k;
+    const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
+    const int64_t m = static_cast<int64_t>(tm) * ROWS + sub % ROWS;
+    if (m >= a.M) return;
+    const int64_t g0 = static_cast<int64_t>(tk) * (GC * STEP) + sub / ROWS;
+    const int64_t G = (a.K + kG - 1) / kG;
+    float v[STEP][8];
+#pragma unroll
+    for (int t = 0; t < STEP; t++) {
+        const int64_t g = g0 + t * GC;
+        if (g < G) Load::row(a, m, g * kG + 8 * l, v[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < STEP; t++) {
+        const int64_t g = g0 + t * GC;
+        if (g >= G) break;
+        const float s = scale_of(row_max16(amax8(v[t])));
+        store8(a.q + m * a.ldq, g * kG + 8 * l, a.K, codes8(v[t], s, 1.0f / s));
+        if (l == 0) a.s[g * a.lds + m] = s;
+    }
+}
+
+// 128 x 128 blocks, one workgroup each: the block stays in registers (64 values per thread)
+// between the maximum, joined over the waves in LDS, and the codes.
+template <class T>
+__global__ void __launch_bounds__(256) quantize_blocks(QuantArgs a)
+{
+    __shared__ float part[4];
+    const uint32_t g = blockIdx.x % a.tiles_k;
+    const int64_t nb = blockIdx.x / a.tiles_k;
+    const int64_t m0 = nb * kG + (threadIdx.x >> 4), k = static_cast<int64_t>(g) * kG + 8 * (threadIdx.x & 15);
+    float v[8][8];
+    float top = 0.f;
+#pragma unroll
+    for (int t = 0; t < 8; t++) {
+        const int64_t m = m0 + 16 * t;
+        if (m < a.M) {
+            LoadX<T>::row(a, m, k, v[t]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[t][i] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 8; t++) top = fmaxf(top, amax8(v[t]));
+    top = row_max16(top);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+    __syncthreads();
+    const float s = scale_of(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
+    const float r = 1.0f / s;
+#pragma unroll
+    for (int t = 0; t < 8; t++) {
+        const int64_t m = m0 + 16 * t;
+        if (m < a.M) store8(a.q + m * a.ldq, k, a.K, codes8(v[t], s, r));
+    }
+    if (threadIdx.x == 0) a.s[nb * a.lds + g] = s;
+}
+
+// Checks that the two quantizers share.
+uw_status check_quant(int64_t M, int64_t K, const void* q, int64_t ldq, const void* s, int64_t lds, int64_t lds_least)
+{
+    if (!q || !s) return fail(UW_EINVAL, "NULL device pointer");
+    if (!aligned(q, 16) || !aligned(s, 4)) return fail(UW_EINVAL, "codes must be 16-byte aligned, scales 4-byte aligned");
+    if (ldq < K || ldq % 16) return fail(UW_EINVAL, "ldq must be >= K and a multiple of 16");
+    if (lds < lds_least) return fail(UW_EINVAL, "lds too small");
+    (void)M;
+    return UW_OK;
+}
+
+template <class Load>
+uw_status launch_rows(QuantArgs& a, hipStream_t s)
+{
+    const int64_t G = (a.K + kG - 1) / kG;
+    const int64_t rows = a.M < 16 ? 1 : 16, wide = a.M < 16 ? 16 : 4;
+    const int64_t tk = (G + wide - 1) / wide, tm = (a.M + rows - 1) / rows;
+    if (tk > INT32_MAX || tm > INT32_MAX / tk) return fail(UW_EUNSUPPORTED, "too many groups for one launch");
+    a.tiles_k = static_cast<uint32_t>(tk);
+    const dim3 grid(static_cast<uint32_t>(tk * tm));
+    if (a.M < 16)
+        hipLaunchKernelGGL((quantize_rows<Load, 1, 1>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((quantize_rows<Load, 16, 4>), grid, dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? UW_OK : fail(UW_EHIP, "quantize launch failed: %s", hipGetErrorString(e));
+}
+
+template <class T>
+uw_status launch_blocks(QuantArgs& a, hipStream_t s)
+{
+    const int64_t G = (a.K + kG - 1) / kG, nb = (a.M + kG - 1) / kG;
+    if (G > INT32_MAX || nb > INT32_MAX / G) return fail(UW_EUNSUPPORTED, "too many blocks for one launch");
+    a.tiles_k = static_cast<uint32_t>(G);
+    hipLaunchKernelGGL(quantize_blocks<T>, dim3(static_cast<uint32_t>(G * nb)), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? UW_OK : fail(UW_EHIP, "quantize launch failed: %s", hipGetErrorString(e));
+}
+
+}  // namespace
+
+}  // namespace uw
+
+using namespace uw;
+
+uw_status uw_fp8_quantize(const void* d_x, int32_t x_type, int64_t M, int64_t K, int64_t ldx, int32_t block_rows,
+                          uint8_t* d_q, int64_t ldq, float* d_s, int64_t lds, void* stream)
+{
+    clear_error();
+    if (M < 0 || K < 1) return fail(UW_ESHAPE, "bad shape %lld x %lld", (long long)M, (long long)K);
+    if (x_type != UW_F32 && x_type != UW_BF16) return fail(UW_EINVAL, "bad x_type %d", x_type);
+    if (block_rows != 1 && block_rows != kG) return fail(UW_EINVAL, "block_rows must be 1 or %d", kG);
+    if (M == 0) return UW_OK;
+    if (!d_x || !aligned(d_x, 16)) return fail(UW_EINVAL, "d_x must be 16-byte aligned and not NULL");
+    if (ldx < K || ldx % (x_type == UW_BF16 ? 8 : 4)) return fail(UW_EINVAL, "ldx must be >= K and keep rows 16-byte aligned");
+    uw_status st = check_quant(M, K, d_q, ldq, d_s, lds, block_rows == 1 ? M : (K + kG - 1) / kG);
+    if (st != UW_OK) return st;
+    QuantArgs a{};
+    a.x = d_x;
+    a.ldx = ldx;
+    a.M = M;
+    a.K = K;
+    a.q = d_q;
+    a.ldq = ldq;
+    a.s = d_s;
+    a.lds = lds;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (block_rows == 1) return x_type == UW_BF16 ? launch_rows<LoadX<uint16_t>>(a, s) : launch_rows<LoadX<float>>(a, s);
+    return x_type == UW_BF16 ? launch_blocks<uint16_t>(a, s) : launch_blocks<float>(a, s);
+}
+
+uw_status uw_fp8_swiglu(const float* d_g, int64_t ldg, const float* d_u, int64_t ldu, int64_t M, int64_t K,
+                        uint8_t* d_q, int64_t ldq, float* d_s, int64_t lds, void* stream)
+{
+    clear_error();
+    if (M < 0 || K < 1) return fail(UW_ESHAPE, "bad shape %lld x %lld", (long long)M, (long long)K);
+    if (M == 0) return UW_OK;
+    if (!d_g || !d_u || !aligned(d_g, 16) || !aligned(d_u, 16)) return fail(UW_EINVAL, "d_g and d_u must be 16-byte aligned and not NULL");
+    if (ldg < K || ldu < K || ldg % 4 || ldu % 4) return fail(UW_EINVAL, "ldg and ldu must be >= K and multiples of 4");
+    uw_status st = check_quant(M, K, d_q, ldq, d_s, lds, M);
+    if (st != UW_OK) return st;
+    QuantArgs a{};
+    a.x = d_g;
+    a.ldx = ldg;
+    a.u = d_u;
+    a.ldu = ldu;
+    a.M = M;
+    a.K = K;
+    a.q = d_q;
+    a.ldq = ldq;
+    a.s = d_s;
+    a.lds = lds;
+    return launch_rows<LoadSwiglu>(a, static_cast<hipStream_t>(stream));
+}

@@ -462,6 +462,130 @@ int uw_variant_by_name(const char* name);
 uw_status uw_swiglu(const float* d_g, const float* d_u, int64_t n, uint16_t* d_h, void* stream);
 
 /*
+ * The 8-bit path: projections that may lose bits, beside the lossless planes above. Values
+ * are OCP e4m3 codes (1 sign, 4 exponent, 3 mantissa bits, largest 448, no infinities, NaN =
+ * 0x7F / 0xFF) with one fp32 scale per group of UW_FP8_GROUP values along K: a code q of a
+ * group with scale s stands for q * s. G = ceil(K / 128) groups; the last may be short.
+ *   rows    (activations) a group is 128 values of one row; scales are group-major,
+ *           s[g * lds + m], lds >= M: the scales that a GEMM step reads for its rows adjacent
+ *   blocks  (weights) a group is a 128 x 128 block, the last ones short in either direction;
+ *           scales s[(n / 128) * lds + g], lds >= G
+ * Code rows start ldq (ldx, ldw) bytes apart, a multiple of 16 and at least K; K is any
+ * positive number. The ld - K bytes behind a row are neither written nor used, so they may
+ * hold anything (a NaN code too), but the last row's too have to be readable up to the
+ * next multiple of 16.
+ *
+ * uw_fp8_quantize (device). Codes and scales of X [M][K] (x_type UW_BF16 or UW_F32, ldx
+ * elements between rows, 16-byte aligned rows: ldx a multiple of 8 for bf16, 4 for fp32)
+ * with groups of block_rows x 128 values, block_rows 1 (rows) or 128 (blocks). Per group,
+ * with a = the largest |x| among its finite values: s = max(a / 448, 2^-126), or 1 where
+ * a = 0, and code = e4m3(x / s) rounded to nearest even and held at +-448. A value that is
+ * NaN or infinite gets the NaN code and leaves its group's other values as they are.
+ *
+ * uw_fp8_swiglu (device). The activation of uw_swiglu, ending in codes: h = silu(g) * u in
+ * fp32 (not rounded to bf16 on the way), quantized as rows. g and u fp32 [M][K] with leading
+ * dimensions ldg and ldu (multiples of 4), so that both can be halves of one product with the
+ * gate and up weights stacked. d_g, d_u, d_q and d_s must not overlap.
+ *
+ * Errors: UW_ESHAPE (M < 0, K < 1), UW_EINVAL (NULL or misaligned pointers: 16 bytes, scales
+ * 4; a leading dimension too small or not the multiple named; an unknown type or block_rows),
+ * UW_EUNSUPPORTED (more than 2^31 - 1 workgroups), UW_EHIP. M = 0 is a no-op.
+ */
+#define UW_FP8_GROUP 128
+typedef enum { UW_F32 = 0, UW_BF16 = 1 } uw_type;
+
+uw_status uw_fp8_quantize(const void* d_x, int32_t x_type, int64_t M, int64_t K, int64_t ldx, int32_t block_rows,
+                          uint8_t* d_q, int64_t ldq, float* d_s, int64_t lds, void* stream);
+uw_status uw_fp8_swiglu(const float* d_g, int64_t ldg, const float* d_u, int64_t ldu, int64_t M, int64_t K,
+                        uint8_t* d_q, int64_t ldq, float* d_s, int64_t lds, void* stream);
+
+/*
+ * uw_fp8_gemm (device). Y = X * W^T from codes: X [M][K] with row scales, W [N][K] with block
+ * scales (above),
+ *   Y[m][n] = sum over groups g of  sx[g][m] sw[n / 128][g] * sum over k in g of x[m][k] w[n][k]
+ * the inner sums in the matrix units, the scales and the sum over groups in fp32. Y is
+ * overwritten: fp32 or bf16 (y_type; one rounding to nearest even), ldy elements between
+ * rows. For fp32 outputs the inner sums are fp32 too. For bf16 outputs at larger M the matrix
+ * unit's own 8-bit product takes them, which drops bits below about 2^-18 of a group's
+ * largest product (up to 2^-11 of it over a group): below the rounding of the output unless
+ * groups cancel. A NaN code or scale reaches the outputs of its own row (or column) only.
+ * Results do not depend on the run: no atomics, and the order of every sum is fixed by M, N, K
+ * and the workspace given. Rows and columns of Y outside M x N are left as they are.
+ * Workspace: with d_ws of uw_fp8_gemm_workspace(M, N, K) bytes (16-byte aligned) shapes with
+ * few output tiles cut K into slices whose partial sums meet there; with d_ws NULL or
+ * ws_bytes smaller they run in one slice (correct, slower). It is free again when the call's
+ * work is done; calls that overlap need one each. uw_fp8_gemm_workspace is 0 for arguments
+ * that uw_fp8_gemm refuses and where no slices are cut.
+ * Errors: UW_ESHAPE (M < 0, N or K < 1), UW_EINVAL (NULL or misaligned pointers: codes and Y
+ * 16 bytes, scales 4; leading dimensions; an unknown type), UW_EUNSUPPORTED (a leading
+ * dimension of 2^24 bytes or more, M, N or K of 2^31 or more), UW_EHIP. M = 0 is a no-op.
+ */
+typedef struct {
+    int64_t M, N, K;
+    const uint8_t* d_x;  /* codes of X [M][ldx] */
+    int64_t ldx;
+    const float* d_sx;   /* row scales [G][ldsx] */
+    int64_t ldsx;        /* >= M */
+    const uint8_t* d_w;  /* codes of W [N][ldw] */
+    int64_t ldw;
+    const float* d_sw;   /* block scales [ceil(N / 128)][ldsw] */
+    int64_t ldsw;        /* >= G */
+    void* d_y;           /* [M][ldy] */
+    int64_t ldy;         /* >= N */
+    int32_t y_type;      /* uw_type */
+    void* d_ws;
+    size_t ws_bytes;
+} uw_fp8_gemm_args;
+
+uw_status uw_fp8_gemm(const uw_fp8_gemm_args* args, void* stream);
+size_t uw_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K);
+
+/*
+ * uw_sample (device). One token per row of logits, e.g. of the Y that the GEMM of a model's
+ * output projection writes. Row m, with its own settings:
+ *   1. tokens are ordered by logit, the largest first, equal ones by index; w_i = exp((l_i - max) / T)
+ *   2. top-k: the first k tokens stay (k <= 0 or k >= V: all)
+ *   3. top-p: of these, the shortest beginning stays whose mass (sum of w) is at least p times
+ *      the mass of all of them; at least one token (p >= 1: all)
+ *   4. min-p: tokens with w_i < min_p leave, the first one never does
+ *   5. the token drawn is the first in the order whose mass with all before it is more than
+ *      u times the mass of what is left
+ * d_prob (optional) receives w_token / (mass of what is left). T = 0 takes the first token
+ * (probability 1), so do negative T and NaN; an infinite T weighs all tokens the same. NaN in
+ * top_p or min_p leaves the step out; u is held to [0, 1), NaN counts as 0. Logits that are
+ * NaN or -inf are never drawn and count nowhere (masks); where some are +inf they share the
+ * mass. A row with nothing to draw gets token -1 and probability 0. Masses are integers, multiples
+ * of 2^-43 of the largest token's, so results are the same for every run and order;
+ * tokens below half of that weigh nothing and are never drawn.
+ * Settings are device arrays of M, so that a captured graph can be replayed with others; NULL
+ * leaves a step out (T = 1).
+ * d_ws: uw_sample_workspace(M, V) bytes, 16-byte aligned; free again when the call's work is
+ * done; calls that overlap need one each. NULL where that is 0.
+ * Errors: UW_ESHAPE (M < 0, V < 1), UW_EINVAL (NULL d_logits, d_u or d_token, misaligned
+ * pointers: that of their elements, ld < V, an unknown type), UW_ENOSPACE (workspace), UW_EUNSUPPORTED
+ * (V > UW_SAMPLE_MAX_V, M >= 2^24), UW_EHIP. M = 0 is a no-op.
+ */
+#define UW_SAMPLE_MAX_V (1 << 20)
+typedef struct {
+    int64_t M, V;
+    const void* d_logits;       /* [M][ld] */
+    int64_t ld;                 /* >= V, any */
+    int32_t type;               /* uw_type of the logits */
+    const float* d_u;           /* [M] uniform numbers in [0, 1) */
+    const float* d_temperature; /* [M] or NULL */
+    const int32_t* d_top_k;     /* [M] or NULL */
+    const float* d_top_p;       /* [M] or NULL */
+    const float* d_min_p;       /* [M] or NULL */
+    int32_t* d_token;           /* [M] */
+    float* d_prob;              /* [M] or NULL */
+    void* d_ws;
+    size_t ws_bytes;
+} uw_sample_args;
+
+uw_status uw_sample(const uw_sample_args* args, void* stream);
+size_t uw_sample_workspace(int64_t M, int64_t V);
+
+/*
  * MLP stack (device). One SwiGLU MLP per layer, layers in order: g = X Wg^T, u = X Wu^T,
  * h = bf16(silu(g) u) (uw_swiglu), Y = h Wd^T, each projection through its own pipeline,
  * GEMM variant and K split (e.g. from uw_autotune), all launched on `stream` ("Bundles and
