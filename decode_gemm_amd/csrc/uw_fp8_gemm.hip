@@ -18,8 +18,11 @@
 // the same operands are off by 1.4e-8.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "uw_internal.h"
 #include "uw_recon.h"
+#include "uw_tiles.h"
 
 namespace uw {
 
@@ -90,20 +93,39 @@ __device__ __forceinline__ floatx4 group_sum(const F8& a, const F8& b)
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, floatx4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
-// A 16-byte chunk at p of which the first `left` bytes belong to the row (none where left <= 0:
-// then nothing is read); the others become 0.
-__device__ __forceinline__ u32x4 chunk_cut(const uint8_t* p, int left)
+template <bool EXACT>
+struct Operand {
+    typedef F8 type;
+};
+template <>
+struct Operand<true> {
+    typedef B16 type;
+};
+template <bool EXACT>
+__device__ __forceinline__ typename Operand<EXACT>::type operand(const F8& f)
 {
-    u32x4 v = {0, 0, 0, 0};
-    if (left > 0) {
-        v = *reinterpret_cast<const u32x4*>(p);
+    if constexpr (EXACT)
+        return to_bf16(f);
+    else
+        return f;
+}
+
+// A 16-byte chunk of which the first `left` bytes belong to the row: the others become 0.
+__device__ __forceinline__ u32x4 cut(u32x4 v, int left)
+{
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int keep = left - 4 * i;
-            v[i] = keep >= 4 ? v[i] : keep <= 0 ? 0u : v[i] & (0xFFFFFFFFu >> (32 - 8 * keep));
-        }
+    for (int i = 0; i < 4; i++) {
+        const int keep = left < 4 * i ? 0 : left > 4 * i + 4 ? 4 : left - 4 * i;
+        v[i] &= static_cast<uint32_t>((uint64_t{1} << (8 * keep)) - 1);
     }
     return v;
+}
+
+// The same of the chunk at p; one with nothing of the row is not read.
+__device__ __forceinline__ u32x4 chunk_cut(const uint8_t* p, int left)
+{
+    if (left <= 0) return u32x4{0, 0, 0, 0};
+    return cut(*reinterpret_cast<const u32x4*>(p), left);
 }
 
 // Y[m][n .. n+3] (those inside), or the K slice's partial sums.
@@ -147,7 +169,9 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny(F8Args a)
     __shared__ floatx4 red[NW][RT * CT][64];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * RT), m0 = static_cast<int64_t>(blockIdx.y) * (16 * CT);
+    const uint32_t tiles_n = static_cast<uint32_t>((a.N + 16 * RT - 1) / (16 * RT));
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x % tiles_n) * (16 * RT);
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x / tiles_n) * (16 * CT);
     const uint32_t full = static_cast<uint32_t>(a.K / kG), G = static_cast<uint32_t>((a.K + kG - 1) / kG);
     const uint32_t j0 = blockIdx.z * a.slice, j1 = j0 + a.slice < G ? j0 + a.slice : G;
     const uint32_t f1 = j1 < full ? j1 : full;  // whole groups of this slice end here
@@ -253,12 +277,208 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny(F8Args a)
     }
 }
 
+// -------------------------------------------------------------------------- tiles
+// A BN x BM output tile per workgroup of WN x WM waves, K in steps of one scale group, both
+// operands and the scales sent from global memory straight into LDS (DMA) through NST stages.
+//
+// LDS layout of an operand in a stage: row rho at 128 rho, its 16-byte chunk c at slot
+// c ^ ((rho >> 1) & 7). A transfer covers 1 KB, lane l landing at 16 l: row 8 i + l / 8, slot
+// l mod 8, so it fetches chunk (l mod 8) ^ ((rho >> 1) & 7); the eight lanes of a row read its
+// whole 128-byte segment. A fragment read (lane 16 g + r: row 16 t + r, chunks g and 4 + g) hits
+// 16 distinct 16-byte bank groups in every 16 lanes.
+//
+// One barrier per step: behind it the step's transfers have landed (each wave waits for its own
+// before it) and every wave is done with the step before, whose stage takes the step NST - 1 ahead.
+__device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(base)
+                 : "memory");
+}
+
+template <int BN, int BM>
+constexpr int stage_bytes()
+{
+    return (BN + BM) * 128 + (BM < 64 ? 64 : BM) * 4 + BN / 128 * 256;
+}
+
+template <int BN, int BM, int WN, int WM, int NST, bool EXACT>
+__global__ void __launch_bounds__(64 * WN * WM) fp8_tile(F8Args a)
+{
+    constexpr int NW = WN * WM, TN = BN / 16 / WN, TM = BM / 16 / WM;
+    constexpr int OPW = BN * 128, OPX = BM * 128, SEG = BM < 64 ? 1 : BM / 64;
+    constexpr int STAGE = stage_bytes<BN, BM>();
+    constexpr int NLW = BN / 8 / NW, NLX = BM / 8 / NW;
+    constexpr int NL = NLW + NLX + 2;  // transfers per wave and step
+    static_assert(BN % 128 == 0 && 16 * TN <= 128 && 128 % (16 * TN) == 0 && NLX >= 1 && SEG <= NW, "tile shape");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+
+    const uint32_t tiles_n = static_cast<uint32_t>((a.N + BN - 1) / BN), tiles_m = static_cast<uint32_t>((a.M + BM - 1) / BM);
+    uint32_t tn, tm;
+    tile_of_block(blockIdx.x, gridDim.x, tiles_n, tiles_m, tn, tm);
+    const int64_t n0 = static_cast<int64_t>(tn) * BN, m0 = static_cast<int64_t>(tm) * BM;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave / WM, wm = wave % WM;
+    const uint32_t G = static_cast<uint32_t>((a.K + kG - 1) / kG);
+    const uint32_t j0 = blockIdx.z * a.slice, j1 = j0 + a.slice < G ? j0 + a.slice : G;
+    const int rest = static_cast<int>(a.K % kG);  // the last group's values, 0 = all
+
+    // per-lane byte offsets of this wave's transfers from the tile's first row (rows past N or M
+    // read the last row; 256 rows of less than 2^24 bytes stay below 2^32)
+    uint32_t woff[NLW], xoff[NLX], soff;
+    const int slot = lane & 7;
+#pragma unroll
+    for (int q = 0; q < NLW; q++) {
+        const int rho = 8 * (NLW * wave + q) + (lane >> 3);
+        const int64_t n = n0 + rho < a.N ? rho : a.N - 1 - n0;
+        woff[q] = static_cast<uint32_t>(n * a.ldw) + 16 * (slot ^ ((rho >> 1) & 7));
+    }
+#pragma unroll
+    for (int q = 0; q < NLX; q++) {
+        const int rho = 8 * (NLX * wave + q) + (lane >> 3);
+        const int64_t m = m0 + rho < a.M ? rho : a.M - 1 - m0;
+        xoff[q] = static_cast<uint32_t>(m * a.ldx) + 16 * (slot ^ ((rho >> 1) & 7));
+    }
+    {
+        const int m = 64 * (wave % SEG) + lane;
+        soff = 4 * static_cast<uint32_t>(m0 + m < a.M ? m : a.M - 1 - m0);
+    }
+    const uint32_t lds0 = lds_offset(lds);
+    const uint8_t* const wbase = a.w + n0 * a.ldw;
+    const uint8_t* const xbase = a.x + m0 * a.ldx;
+    const float* const sxbase = a.sx + m0;
+    const int nb = wn * (16 * TN) / 128;  // this wave's 128 block of the tile
+    const int64_t nblk = n0 / 128 + nb;
+    const float* const swbase = a.sw + (nblk < (a.N + 127) / 128 ? nblk : (a.N - 1) / 128) * a.ldsw;
+    // A short last group is read as the 128 bytes that end at K rounded up to 16, so that nothing behind
+    // a row is read (K >= 128); the bytes before its start and past K are cut to zero at use.
+    const int64_t last = (a.K + 15) / 16 * 16 - kG;
+    auto issue = [&](uint32_t j, int st) {
+        const int64_t k = rest && j + 1 == G ? last : static_cast<int64_t>(j) * kG;
+        const uint8_t* wb = wbase + k;
+        const uint8_t* xb = xbase + k;
+        const uint32_t dst = lds0 + st * STAGE;
+#pragma unroll
+        for (int q = 0; q < NLW; q++) dma16(wb, woff[q], dst + 1024 * (NLW * wave + q));
+#pragma unroll
+        for (int q = 0; q < NLX; q++) dma16(xb, xoff[q], dst + OPW + 1024 * (NLX * wave + q));
+        dma4(sxbase + static_cast<int64_t>(j) * a.ldsx, soff, dst + OPW + OPX + 256 * (wave % SEG));
+        dma4(swbase + j, 0, dst + OPW + OPX + 256 * (SEG + nb));
+    };
+
+    const int fo0 = 128 * r + 16 * (g ^ ((r >> 1) & 7)), fo1 = 128 * r + 16 * ((4 + g) ^ ((r >> 1) & 7));
+    auto frag = [&](const uint8_t* p, bool tail) {
+        F8 f;
+        f.a = *reinterpret_cast<const u32x4*>(p + fo0);
+        f.b = *reinterpret_cast<const u32x4*>(p + fo1);
+        if (tail) {
+            const int from = kG - (rest + 15) / 16 * 16, to = from + rest;  // the group's bytes of the 128
+            f.a = cut(f.a, 16 * g < from ? 0 : to - 16 * g);
+            f.b = cut(f.b, 16 * g + 64 < from ? 0 : to - 16 * g - 64);
+        }
+        return f;
+    };
+
+    floatx4 acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; i++)
+#pragma unroll
+        for (int c = 0; c < TM; c++) acc[i][c] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    auto step = [&](const uint8_t* S, auto tail) {
+        using Op = typename Operand<EXACT>::type;
+        const uint8_t* const W = S + 2048 * TN * wn;
+        const uint8_t* const X = S + OPW + 2048 * TM * wm;
+        const float* const sx = reinterpret_cast<const float*>(S + OPW + OPX) + 16 * TM * wm + r;
+        const float sw = *reinterpret_cast<const float*>(S + OPW + OPX + 256 * (SEG + nb));
+        Op bf[TM];
+        float s[TM];
+#pragma unroll
+        for (int c = 0; c < TM; c++) {
+            bf[c] = operand<EXACT>(frag(X + 2048 * c, tail));
+            s[c] = sx[16 * c] * sw;
+        }
+        F8 an = frag(W, tail);
+#pragma unroll
+        for (int i = 0; i < TN; i++) {
+            const Op ac = operand<EXACT>(an);
+            if (i + 1 < TN) an = frag(W + 2048 * (i + 1), tail);
+#pragma unroll
+            for (int c = 0; c < TM; c++) {
+                const floatx4 d = group_sum(ac, bf[c]);
+#pragma unroll
+                for (int q = 0; q < 4; q++) acc[i][c][q] = __builtin_fmaf(d[q], s[c], acc[i][c][q]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+#pragma unroll
+    for (int p = 0; p < NST - 1; p++)
+        if (j0 + p < j1) issue(j0 + p, p);
+    int st = 0, sn = NST - 1;  // stages of this step and of the one NST - 1 ahead
+    auto arrive = [&](uint32_t j) {
+        // this wave's transfers of step j have landed when only those of the NST - 2 younger steps
+        // may be left
+        if (NST > 2 && j + NST - 2 < j1) {
+            constexpr int younger = (NST > 2 ? NST - 2 : 0) * NL;
+            static_assert(younger < 64, "wait counter");
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(younger) : "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        __syncthreads();
+    };
+    const bool tail = rest && j1 == G;
+    const uint32_t jf = tail ? j1 - 1 : j1;
+    for (uint32_t j = j0; j < jf; j++) {
+        arrive(j);
+        if (j + NST - 1 < j1) issue(j + NST - 1, sn);
+        step(lds + st * STAGE, std::false_type{});
+        st = st + 1 < NST ? st + 1 : 0;
+        sn = sn + 1 < NST ? sn + 1 : 0;
+    }
+    if (tail) {
+        arrive(jf);
+        step(lds + st * STAGE, std::true_type{});
+    }
+#pragma unroll
+    for (int i = 0; i < TN; i++)
+#pragma unroll
+        for (int c = 0; c < TM; c++)
+            store4(a, m0 + 16 * (TM * wm + c) + r, n0 + 16 * (TN * wn + i) + 4 * g, acc[i][c]);
+}
+
+// Sum of the K slices' partial results, in slice order.
+__global__ void __launch_bounds__(256) fp8_join(F8Args a, const float* part, uint32_t slices)
+{
+    const int64_t q = a.N4 / 4, e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (e >= a.M * q) return;
+    const float* p = part + 4 * e;
+    floatx4 s = *reinterpret_cast<const floatx4*>(p);
+    for (uint32_t z = 1; z < slices; z++) s += *reinterpret_cast<const floatx4*>(p + z * a.M * a.N4);
+    store4(a, e / q, 4 * (e % q), s);
+}
+
 template <int CT, int RT, int U, int NW>
 hipError_t launch_skinny(const F8Args& a, uint32_t slices, hipStream_t s)
 {
-    const dim3 grid(static_cast<uint32_t>((a.N + 16 * RT - 1) / (16 * RT)), static_cast<uint32_t>((a.M + 16 * CT - 1) / (16 * CT)),
-                    slices);
+    const dim3 grid(static_cast<uint32_t>(((a.N + 16 * RT - 1) / (16 * RT)) * ((a.M + 16 * CT - 1) / (16 * CT))), 1, slices);
     hipLaunchKernelGGL((fp8_skinny<CT, RT, U, NW>), grid, dim3(64 * NW), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int BN, int BM, int WN, int WM, int NST, bool EXACT>
+hipError_t launch_tile(const F8Args& a, uint32_t slices, hipStream_t s)
+{
+    constexpr size_t lds = NST * stage_bytes<BN, BM>();
+    static_assert(lds <= 160 * 1024, "LDS");
+    static uint64_t attr_done = 0;  // devices the LDS limit was raised on
+    const void* fn = reinterpret_cast<const void*>(&fp8_tile<BN, BM, WN, WM, NST, EXACT>);
+    hipError_t e = allow_lds(fn, lds, attr_done);
+    if (e != hipSuccess) return e;
+    const dim3 grid(static_cast<uint32_t>(((a.N + BN - 1) / BN) * ((a.M + BM - 1) / BM)), 1, slices);
+    hipLaunchKernelGGL((fp8_tile<BN, BM, WN, WM, NST, EXACT>), grid, dim3(64 * WN * WM), lds, s, a);
     return hipGetLastError();
 }
 
@@ -318,13 +538,19 @@ uw_status uw_fp8_gemm(const uw_fp8_gemm_args* p, void* stream)
     a.ldy = p->ldy;
     a.bf16 = p->y_type == UW_BF16;
     a.slice = static_cast<uint32_t>((p->K + kG - 1) / kG);
+    // the smallest tiles are 16 x 16
+    if ((a.M + 15) / 16 * ((a.N + 15) / 16) > INT32_MAX) return fail(UW_EUNSUPPORTED, "more than 2^31 - 1 tiles");
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e;
     if (a.M <= 16)
         e = launch_skinny<1, 1, 4, 4>(a, 1, s);
     else if (a.M <= 32)
         e = launch_skinny<2, 2, 2, 4>(a, 1, s);
-    else
+    else if (a.M <= 64 || a.K < kG)  // the tiles read whole groups of K
         e = launch_skinny<4, 4, 2, 4>(a, 1, s);
+    else if (a.bf16)
+        e = launch_tile<256, 256, 2, 4, 2, false>(a, 1, s);
+    else
+        e = launch_tile<256, 256, 2, 4, 2, true>(a, 1, s);
     return e == hipSuccess ? UW_OK : fail(UW_EHIP, "GEMM launch failed: %s", hipGetErrorString(e));
 }

@@ -30,6 +30,7 @@
 
 #include "uw_internal.h"
 #include "uw_recon.h"
+#include "uw_tiles.h"
 
 namespace uw {
 
@@ -66,23 +67,6 @@ __device__ __forceinline__ floatx4 mfma16(const u32x4& a, const u32x4& b, const 
 
 // s_waitcnt that waits for LDS reads only (lgkmcnt 0; vmcnt and expcnt at their maxima).
 constexpr int kWaitLgkm0 = 0xC07F;
-
-// LDS byte offset of a pointer into the workgroup's LDS.
-__device__ __forceinline__ uint32_t lds_offset(const void* p)
-{
-    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
-}
-
-// One LDS DMA of 16 bytes per lane: lane l's bytes at base + voff go to LDS at lds + 16 l.
-// Issued from asm so that the compiler's wait counting does not make every later LDS read
-// wait for the newest transfer; the compiler then undercounts outstanding loads, which
-// only ever makes its own waits stricter. Callers order the reads of the target
-// themselves (a wait for a load issued after the transfer).
-__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t voff, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(base)
-                 : "memory");
-}
 
 // Rank of raw group j among the raw groups of row `row` (the row's bitmap words before
 // j's word are popcounted; only reached for raw groups).
@@ -1047,26 +1031,6 @@ struct TiledCfg {
     static constexpr int LDS = 2 * (A_BYTES + B_BYTES);
 };
 
-// blockIdx -> (n tile, m tile): consecutive hardware workgroups are dealt round-robin to
-// the 8 XCDs, so first regroup them so each XCD gets a contiguous run of logical tiles,
-// then walk the tiles in groups of 8 n-tiles so that concurrently resident workgroups
-// share W slices (same n tile) and X slices (same m tile) in that XCD's L2.
-__device__ __forceinline__ void tile_of_block(uint32_t bid, uint32_t nblocks, uint32_t tiles_n, uint32_t tiles_m,
-                                              uint32_t& tn, uint32_t& tm)
-{
-    constexpr uint32_t XCD = 8, GROUP = 8;
-    uint32_t pid = bid;
-    const uint32_t full = nblocks / XCD * XCD;
-    if (bid < full) pid = (bid % XCD) * (nblocks / XCD) + bid / XCD;
-    const uint32_t per_group = GROUP * tiles_m;
-    const uint32_t group = pid / per_group;
-    const uint32_t first_n = group * GROUP;
-    const uint32_t gsize = (tiles_n - first_n) < GROUP ? (tiles_n - first_n) : GROUP;
-    const uint32_t in_group = pid % per_group;
-    tn = first_n + in_group % gsize;
-    tm = in_group / gsize;
-}
-
 template <int SRC, bool CONTIG, int BN, int BM>
 __global__ void __launch_bounds__(256) gemm_tiled(GemmArgs a)
 {
@@ -1656,20 +1620,6 @@ const Variant kVariants[] = {
     {"dma 256x256", 3, 0, 8, 2, 256, 256},              {"dma 256x128 s3", 3, 0, 8, 3, 256, 128},
 };
 constexpr int kNumVariants = sizeof(kVariants) / sizeof(kVariants[0]);
-
-// Raise a kernel's dynamic LDS limit past the 64 KB default (gfx950 has 160 KB per CU),
-// once per device (bit d of `done`; a lost update between racing threads only repeats the
-// call).
-hipError_t allow_lds(const void* fn, size_t bytes, uint64_t& done)
-{
-    if (bytes <= 64 * 1024) return hipSuccess;
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
-    if ((done >> dev) & 1u) return hipSuccess;
-    hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == hipSuccess) done |= uint64_t{1} << dev;
-    return e;
-}
 
 template <int SRC, bool CONTIG, int CT, int RT, int U, int NW, bool XNEAR, int XT>
 hipError_t launch_skinny_ct(const GemmArgs& g, hipStream_t s)

@@ -518,7 +518,7 @@ uw_status uw_fp8_swiglu(const float* d_g, int64_t ldg, const float* d_u, int64_t
  * that uw_fp8_gemm refuses and where no slices are cut.
  * Errors: UW_ESHAPE (M < 0, N or K < 1), UW_EINVAL (NULL or misaligned pointers: codes and Y
  * 16 bytes, scales 4; leading dimensions; an unknown type), UW_EUNSUPPORTED (a leading
- * dimension of 2^24 bytes or more, M, N or K of 2^31 or more), UW_EHIP. M = 0 is a no-op.
+ * dimension of 2^24 bytes or more, M, N or K of 2^31 or more, M N of 2^39 or more), UW_EHIP. M = 0 is a no-op.
  */
 typedef struct {
     int64_t M, N, K;
