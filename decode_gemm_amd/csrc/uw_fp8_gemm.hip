@@ -43,7 +43,8 @@ struct F8Args {
     int32_t bf16;     // Y is bf16
     float* part;      // K slices: partial sums [slice][M][N4], N4 = N rounded up to 4
     int64_t N4;
-    uint32_t slice;   // groups per K slice
+    uint32_t slices;  // K slices: slice z takes the groups z, z + slices, ... (so that the slices that run
+                      // together read neighbouring bytes of a row)
 };
 
 // 32 bytes of an operand row (the lane's chunks of one group).
@@ -161,7 +162,7 @@ __device__ __forceinline__ void store4(const F8Args& a, int64_t m, int64_t n, co
 
 // ------------------------------------------------------------------------- skinny
 // Few rows of X: 16 RT rows of W x 16 CT rows of X per workgroup, whose NW waves take the
-// groups j = wave (mod NW) of the K slice and meet in LDS. Each wave keeps U groups of both
+// groups in turn and meet in LDS. Each wave keeps U groups of both
 // operands in flight in registers. Bound by HBM (W once), so it takes the exact sums always.
 template <int CT, int RT, int U, int NW>
 __global__ void __launch_bounds__(64 * NW) fp8_skinny(F8Args a)
@@ -173,8 +174,6 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny(F8Args a)
     const int64_t n0 = static_cast<int64_t>(blockIdx.x % tiles_n) * (16 * RT);
     const int64_t m0 = static_cast<int64_t>(blockIdx.x / tiles_n) * (16 * CT);
     const uint32_t full = static_cast<uint32_t>(a.K / kG), G = static_cast<uint32_t>((a.K + kG - 1) / kG);
-    const uint32_t j0 = blockIdx.z * a.slice, j1 = j0 + a.slice < G ? j0 + a.slice : G;
-    const uint32_t f1 = j1 < full ? j1 : full;  // whole groups of this slice end here
 
     const uint8_t* wp[RT];
     const uint8_t* xp[CT];
@@ -231,22 +230,24 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny(F8Args a)
             }
         }
     };
-    if (j0 + wave < f1) {
-        const uint32_t last = f1 - 1;
+    // groups first, first + stride, ...: the waves of all slices take neighbouring ones
+    const uint32_t stride = NW * a.slices, first = blockIdx.z * NW + wave;
+    if (first < full) {
+        const uint32_t last = full - 1;
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const uint32_t j = j0 + wave + u * NW;
+            const uint32_t j = first + u * stride;
             load(u, j < last ? j : last);
         }
-        for (uint32_t j = j0 + wave; j < f1; j += U * NW)
+        for (uint32_t j = first; j < full; j += U * stride)
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                if (j + u * NW < f1) multiply(u);
-                const uint32_t next = j + (u + U) * NW;
+                if (j + u * stride < full) multiply(u);
+                const uint32_t next = j + (u + U) * stride;
                 load(u, next < last ? next : last);
             }
     }
-    if (j1 > full && j0 <= full && wave == static_cast<int>((full - j0) % NW)) {  // the group that K ends inside
+    if (G > full && full % stride == first) {  // the group that K ends inside
         const int rest = static_cast<int>(a.K % kG);
         const int64_t o = static_cast<int64_t>(full) * kG;
 #pragma unroll
@@ -286,9 +287,6 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny(F8Args a)
 // l mod 8, so it fetches chunk (l mod 8) ^ ((rho >> 1) & 7); the eight lanes of a row read its
 // whole 128-byte segment. A fragment read (lane 16 g + r: row 16 t + r, chunks g and 4 + g) hits
 // 16 distinct 16-byte bank groups in every 16 lanes.
-//
-// One barrier per step: behind it the step's transfers have landed (each wave waits for its own
-// before it) and every wave is done with the step before, whose stage takes the step NST - 1 ahead.
 __device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(base)
@@ -301,152 +299,266 @@ constexpr int stage_bytes()
     return (BN + BM) * 128 + (BM < 64 ? 64 : BM) * 4 + BN / 128 * 256;
 }
 
-template <int BN, int BM, int WN, int WM, int NST, bool EXACT>
-__global__ void __launch_bounds__(64 * WN * WM) fp8_tile(F8Args a)
-{
-    constexpr int NW = WN * WM, TN = BN / 16 / WN, TM = BM / 16 / WM;
-    constexpr int OPW = BN * 128, OPX = BM * 128, SEG = BM < 64 ? 1 : BM / 64;
-    constexpr int STAGE = stage_bytes<BN, BM>();
-    constexpr int NLW = BN / 8 / NW, NLX = BM / 8 / NW;
-    constexpr int NL = NLW + NLX + 2;  // transfers per wave and step
+// What a workgroup of either tile kernel reads, and its place in the output.
+template <int BN, int BM, int WN, int WM>
+struct Tile {
+    static constexpr int NW = WN * WM, TN = BN / 16 / WN, TM = BM / 16 / WM;
+    static constexpr int OPW = BN * 128, OPX = BM * 128, SEG = BM < 64 ? 1 : BM / 64;
+    static constexpr int STAGE = stage_bytes<BN, BM>();
+    static constexpr int NLW = BN / 8 / NW, NLX = BM / 8 / NW;
+    static constexpr int NL = NLW + NLX + 2;  // transfers per wave and step
     static_assert(BN % 128 == 0 && 16 * TN <= 128 && 128 % (16 * TN) == 0 && NLX >= 1 && SEG <= NW, "tile shape");
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
-    const uint32_t tiles_n = static_cast<uint32_t>((a.N + BN - 1) / BN), tiles_m = static_cast<uint32_t>((a.M + BM - 1) / BM);
-    uint32_t tn, tm;
-    tile_of_block(blockIdx.x, gridDim.x, tiles_n, tiles_m, tn, tm);
-    const int64_t n0 = static_cast<int64_t>(tn) * BN, m0 = static_cast<int64_t>(tm) * BM;
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wn = wave / WM, wm = wave % WM;
-    const uint32_t G = static_cast<uint32_t>((a.K + kG - 1) / kG);
-    const uint32_t j0 = blockIdx.z * a.slice, j1 = j0 + a.slice < G ? j0 + a.slice : G;
-    const int rest = static_cast<int>(a.K % kG);  // the last group's values, 0 = all
-
-    // per-lane byte offsets of this wave's transfers from the tile's first row (rows past N or M
-    // read the last row; 256 rows of less than 2^24 bytes stay below 2^32)
+    int64_t n0, m0;
+    int lane, r, g, wave, wn, wm, nb;
+    uint32_t G, steps;  // groups of K, and of this slice: blockIdx.z + i * slices, i < steps
+    uint32_t slices;
+    int rest;  // the last group's values, 0 = all
     uint32_t woff[NLW], xoff[NLX], soff;
-    const int slot = lane & 7;
-#pragma unroll
-    for (int q = 0; q < NLW; q++) {
-        const int rho = 8 * (NLW * wave + q) + (lane >> 3);
-        const int64_t n = n0 + rho < a.N ? rho : a.N - 1 - n0;
-        woff[q] = static_cast<uint32_t>(n * a.ldw) + 16 * (slot ^ ((rho >> 1) & 7));
-    }
-#pragma unroll
-    for (int q = 0; q < NLX; q++) {
-        const int rho = 8 * (NLX * wave + q) + (lane >> 3);
-        const int64_t m = m0 + rho < a.M ? rho : a.M - 1 - m0;
-        xoff[q] = static_cast<uint32_t>(m * a.ldx) + 16 * (slot ^ ((rho >> 1) & 7));
-    }
+    const uint8_t *wbase, *xbase;
+    const float *sxbase, *swbase;
+    int64_t last, ldsx;
+    int fo0, fo1;
+
+    __device__ __forceinline__ explicit Tile(const F8Args& a)
     {
+        const uint32_t tiles_n = static_cast<uint32_t>((a.N + BN - 1) / BN), tiles_m = static_cast<uint32_t>((a.M + BM - 1) / BM);
+        uint32_t tn, tm;
+        tile_of_block(blockIdx.x, gridDim.x, tiles_n, tiles_m, tn, tm);
+        n0 = static_cast<int64_t>(tn) * BN;
+        m0 = static_cast<int64_t>(tm) * BM;
+        lane = threadIdx.x & 63;
+        r = lane & 15;
+        g = lane >> 4;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        wn = wave / WM;
+        wm = wave % WM;
+        G = static_cast<uint32_t>((a.K + kG - 1) / kG);
+        slices = a.slices;
+        steps = (G - blockIdx.z + slices - 1) / slices;
+        rest = static_cast<int>(a.K % kG);
+        // per-lane byte offsets of this wave's transfers from the tile's first row (rows past N or M
+        // read the last row; 256 rows of less than 2^24 bytes stay below 2^32)
+        const int slot = lane & 7;
+#pragma unroll
+        for (int q = 0; q < NLW; q++) {
+            const int rho = 8 * (NLW * wave + q) + (lane >> 3);
+            const int64_t n = n0 + rho < a.N ? rho : a.N - 1 - n0;
+            woff[q] = static_cast<uint32_t>(n * a.ldw) + 16 * (slot ^ ((rho >> 1) & 7));
+        }
+#pragma unroll
+        for (int q = 0; q < NLX; q++) {
+            const int rho = 8 * (NLX * wave + q) + (lane >> 3);
+            const int64_t m = m0 + rho < a.M ? rho : a.M - 1 - m0;
+            xoff[q] = static_cast<uint32_t>(m * a.ldx) + 16 * (slot ^ ((rho >> 1) & 7));
+        }
         const int m = 64 * (wave % SEG) + lane;
         soff = 4 * static_cast<uint32_t>(m0 + m < a.M ? m : a.M - 1 - m0);
+        wbase = a.w + n0 * a.ldw;
+        xbase = a.x + m0 * a.ldx;
+        sxbase = a.sx + m0;
+        nb = wn * (16 * TN) / 128;  // this wave's 128 block of the tile
+        const int64_t nblk = n0 / 128 + nb, blocks = (a.N + 127) / 128;
+        swbase = a.sw + (nblk < blocks ? nblk : blocks - 1) * a.ldsw;
+        // A short last group is read as the 128 bytes that end at K rounded up to 16, so that nothing
+        // behind a row is read (K >= 128); the bytes before its start and past K are cut at use.
+        last = (a.K + 15) / 16 * 16 - kG;
+        ldsx = a.ldsx;
+        fo0 = 128 * r + 16 * (g ^ ((r >> 1) & 7));
+        fo1 = 128 * r + 16 * ((4 + g) ^ ((r >> 1) & 7));
     }
-    const uint32_t lds0 = lds_offset(lds);
-    const uint8_t* const wbase = a.w + n0 * a.ldw;
-    const uint8_t* const xbase = a.x + m0 * a.ldx;
-    const float* const sxbase = a.sx + m0;
-    const int nb = wn * (16 * TN) / 128;  // this wave's 128 block of the tile
-    const int64_t nblk = n0 / 128 + nb;
-    const float* const swbase = a.sw + (nblk < (a.N + 127) / 128 ? nblk : (a.N - 1) / 128) * a.ldsw;
-    // A short last group is read as the 128 bytes that end at K rounded up to 16, so that nothing behind
-    // a row is read (K >= 128); the bytes before its start and past K are cut to zero at use.
-    const int64_t last = (a.K + 15) / 16 * 16 - kG;
-    auto issue = [&](uint32_t j, int st) {
+
+    // Whether the slice ends with a short group.
+    __device__ __forceinline__ bool short_end() const { return rest && blockIdx.z + (steps - 1) * slices + 1 == G; }
+
+    // Send the slice's i-th group to the stage at LDS offset dst.
+    __device__ __forceinline__ void issue(uint32_t i, uint32_t dst) const
+    {
+        const uint32_t j = blockIdx.z + i * slices;
         const int64_t k = rest && j + 1 == G ? last : static_cast<int64_t>(j) * kG;
         const uint8_t* wb = wbase + k;
         const uint8_t* xb = xbase + k;
-        const uint32_t dst = lds0 + st * STAGE;
 #pragma unroll
         for (int q = 0; q < NLW; q++) dma16(wb, woff[q], dst + 1024 * (NLW * wave + q));
 #pragma unroll
         for (int q = 0; q < NLX; q++) dma16(xb, xoff[q], dst + OPW + 1024 * (NLX * wave + q));
-        dma4(sxbase + static_cast<int64_t>(j) * a.ldsx, soff, dst + OPW + OPX + 256 * (wave % SEG));
+        dma4(sxbase + static_cast<int64_t>(j) * ldsx, soff, dst + OPW + OPX + 256 * (wave % SEG));
         dma4(swbase + j, 0, dst + OPW + OPX + 256 * (SEG + nb));
-    };
+    }
 
-    const int fo0 = 128 * r + 16 * (g ^ ((r >> 1) & 7)), fo1 = 128 * r + 16 * ((4 + g) ^ ((r >> 1) & 7));
-    auto frag = [&](const uint8_t* p, bool tail) {
+    __device__ __forceinline__ F8 frag(const uint8_t* p) const
+    {
         F8 f;
         f.a = *reinterpret_cast<const u32x4*>(p + fo0);
         f.b = *reinterpret_cast<const u32x4*>(p + fo1);
-        if (tail) {
-            const int from = kG - (rest + 15) / 16 * 16, to = from + rest;  // the group's bytes of the 128
-            f.a = cut(f.a, 16 * g < from ? 0 : to - 16 * g);
-            f.b = cut(f.b, 16 * g + 64 < from ? 0 : to - 16 * g - 64);
-        }
         return f;
-    };
+    }
+    __device__ __forceinline__ F8 wfrag(const uint8_t* S, int i) const { return frag(S + 2048 * (TN * wn + i)); }
+    __device__ __forceinline__ F8 xfrag(const uint8_t* S, int c) const { return frag(S + OPW + 2048 * (TM * wm + c)); }
+    // scale of X for tile column c, and of this wave's W block
+    __device__ __forceinline__ float sx(const uint8_t* S, int c) const
+    {
+        return reinterpret_cast<const float*>(S + OPW + OPX)[16 * (TM * wm + c) + r];
+    }
+    __device__ __forceinline__ float sw(const uint8_t* S) const
+    {
+        return *reinterpret_cast<const float*>(S + OPW + OPX + 256 * (SEG + nb));
+    }
+
+    // The bytes of the short last group among the 128 read.
+    __device__ __forceinline__ F8 cut_tail(F8 f) const
+    {
+        const int from = kG - (rest + 15) / 16 * 16, to = from + rest;
+        f.a = cut(f.a, 16 * g < from ? 0 : to - 16 * g);
+        f.b = cut(f.b, 16 * g + 64 < from ? 0 : to - 16 * g - 64);
+        return f;
+    }
+
+    __device__ __forceinline__ void store(const F8Args& a, const floatx4 (&acc)[TN][TM]) const
+    {
+#pragma unroll
+        for (int i = 0; i < TN; i++)
+#pragma unroll
+            for (int c = 0; c < TM; c++) store4(a, m0 + 16 * (TM * wm + c) + r, n0 + 16 * (TN * wn + i) + 4 * g, acc[i][c]);
+    }
+};
+
+// Wait until this wave's transfers of a step have landed, `younger` later steps of NL transfers
+// each being allowed to be on the way.
+template <int N>
+__device__ __forceinline__ void wait_transfers()
+{
+    static_assert(N >= 0 && N < 64, "wait counter");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// One barrier per step, placed where every fragment of the
+// step is in registers: behind it the stage takes the step NST ahead, and the next step's
+// fragments of X replace this step's as the last MFMAs let go of them, so the matrix cores do not
+// wait for LDS at the start of a step. The wave's W tiles go through registers one ahead of their
+// MFMAs; the last P of them are held (ar) and multiplied behind the barrier, column by column. A
+// group sum is added one W tile (or column) after its MFMA, so no MFMA is waited for.
+// EXACT: the codes become bf16 behind the LDS reads.
+template <int BN, int BM, int WN, int WM, int NST, int P, bool EXACT>
+__global__ void __launch_bounds__(64 * WN * WM) fp8_tile(F8Args a)
+{
+    using T = Tile<BN, BM, WN, WM>;
+    constexpr int TN = T::TN, TM = T::TM, F = TN - P, NL = T::NL;
+    static_assert(F >= 1 && P >= 1 && NST >= 2, "W tiles before and behind the barrier");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const T t(a);
+    const uint32_t steps = t.steps, lds0 = lds_offset(lds);
 
     floatx4 acc[TN][TM];
 #pragma unroll
     for (int i = 0; i < TN; i++)
 #pragma unroll
         for (int c = 0; c < TM; c++) acc[i][c] = floatx4{0.f, 0.f, 0.f, 0.f};
+    using Op = typename Operand<EXACT>::type;
+    F8 an, ar[P];
+    Op bf[TM];
+    float s[TM];
+    auto add = [&](int i, int c, const floatx4& d) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) acc[i][c][q] = __builtin_fmaf(d[q], s[c], acc[i][c][q]);
+    };
 
-    auto step = [&](const uint8_t* S, auto tail) {
-        using Op = typename Operand<EXACT>::type;
-        const uint8_t* const W = S + 2048 * TN * wn;
-        const uint8_t* const X = S + OPW + 2048 * TM * wm;
-        const float* const sx = reinterpret_cast<const float*>(S + OPW + OPX) + 16 * TM * wm + r;
-        const float sw = *reinterpret_cast<const float*>(S + OPW + OPX + 256 * (SEG + nb));
-        Op bf[TM];
-        float s[TM];
+#pragma unroll
+    for (int p = 0; p < NST; p++)
+        if (p < steps) t.issue(p, lds0 + p * T::STAGE);
+    if (NST - 1 < steps)
+        wait_transfers<(NST - 1) * NL>();
+    else
+        wait_transfers<0>();
+    __syncthreads();
+    {
+        const float sw = t.sw(lds);
+        an = t.wfrag(lds, 0);
 #pragma unroll
         for (int c = 0; c < TM; c++) {
-            bf[c] = operand<EXACT>(frag(X + 2048 * c, tail));
-            s[c] = sx[16 * c] * sw;
+            bf[c] = operand<EXACT>(t.xfrag(lds, c));
+            s[c] = t.sx(lds, c) * sw;
         }
-        F8 an = frag(W, tail);
+    }
+    int st = 0;
+    const bool tail = t.short_end();
+    const uint32_t whole = tail ? steps - 1 : steps;
+    for (uint32_t j = 0; j < whole; j++) {
+        const int sn = st + 1 < NST ? st + 1 : 0;
+        const uint8_t *S = lds + st * T::STAGE, *Sn = lds + sn * T::STAGE;
+        floatx4 d[TM];
 #pragma unroll
-        for (int i = 0; i < TN; i++) {
+        for (int i = 0; i < F; i++) {
             const Op ac = operand<EXACT>(an);
-            if (i + 1 < TN) an = frag(W + 2048 * (i + 1), tail);
+            if (i + 1 < F) an = t.wfrag(S, i + 1);
+            if (i >= F - P) ar[i - (F - P)] = t.wfrag(S, F + i - (F - P));
 #pragma unroll
             for (int c = 0; c < TM; c++) {
-                const floatx4 d = group_sum(ac, bf[c]);
-#pragma unroll
-                for (int q = 0; q < 4; q++) acc[i][c][q] = __builtin_fmaf(d[q], s[c], acc[i][c][q]);
+                const floatx4 e = group_sum(ac, bf[c]);
+                if (i > 0) {
+                    add(i - 1, c, d[c]);
+                    // held here: the compiler would sink the sums past the branch below, and the MFMA
+                    // results with them into 100 registers that are not there
+                    asm volatile("" : "+v"(acc[i - 1][c]));
+                }
+                d[c] = e;
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-    };
-
+        if constexpr (F < P) {
 #pragma unroll
-    for (int p = 0; p < NST - 1; p++)
-        if (j0 + p < j1) issue(j0 + p, p);
-    int st = 0, sn = NST - 1;  // stages of this step and of the one NST - 1 ahead
-    auto arrive = [&](uint32_t j) {
-        // this wave's transfers of step j have landed when only those of the NST - 2 younger steps
-        // may be left
-        if (NST > 2 && j + NST - 2 < j1) {
-            constexpr int younger = (NST > 2 ? NST - 2 : 0) * NL;
-            static_assert(younger < 64, "wait counter");
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(younger) : "memory");
-        } else {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            for (int i = 0; i < P - F; i++) ar[i] = t.wfrag(S, F + i);
         }
+        if (NST > 2 && j + NST - 1 < steps)
+            wait_transfers<(NST > 2 ? NST - 2 : 0) * NL>();
+        else
+            wait_transfers<0>();
         __syncthreads();
-    };
-    const bool tail = rest && j1 == G;
-    const uint32_t jf = tail ? j1 - 1 : j1;
-    for (uint32_t j = j0; j < jf; j++) {
-        arrive(j);
-        if (j + NST - 1 < j1) issue(j + NST - 1, sn);
-        step(lds + st * STAGE, std::false_type{});
-        st = st + 1 < NST ? st + 1 : 0;
-        sn = sn + 1 < NST ? sn + 1 : 0;
+        if (j + NST < steps) t.issue(j + NST, lds0 + st * T::STAGE);
+        // (past the last step these reads find an older step's bytes, and nothing uses them)
+        float sx[TM];
+        const float sw = t.sw(Sn);
+#pragma unroll
+        for (int c = 0; c < TM; c++) sx[c] = t.sx(Sn, c);
+        an = t.wfrag(Sn, 0);
+        Op aw[P];
+        floatx4 h[P];
+#pragma unroll
+        for (int i = 0; i < P; i++) aw[i] = operand<EXACT>(ar[i]);
+#pragma unroll
+        for (int c = 0; c < TM; c++) {
+            floatx4 e[P];
+#pragma unroll
+            for (int i = 0; i < P; i++) e[i] = group_sum(aw[i], bf[c]);
+            bf[c] = operand<EXACT>(t.xfrag(Sn, c));
+            add(F - 1, c, d[c]);
+            if (c > 0) {
+#pragma unroll
+                for (int i = 0; i < P; i++) add(F + i, c - 1, h[i]);
+                s[c - 1] = sx[c - 1] * sw;
+            }
+#pragma unroll
+            for (int i = 0; i < P; i++) h[i] = e[i];
+        }
+#pragma unroll
+        for (int i = 0; i < P; i++) add(F + i, TM - 1, h[i]);
+        s[TM - 1] = sx[TM - 1] * sw;
+        __builtin_amdgcn_sched_barrier(0);
+        st = sn;
     }
     if (tail) {
-        arrive(jf);
-        step(lds + st * STAGE, std::true_type{});
+        const uint8_t* S = lds + st * T::STAGE;
+#pragma unroll
+        for (int c = 0; c < TM; c++) bf[c] = operand<EXACT>(t.cut_tail(t.xfrag(S, c)));
+#pragma unroll
+        for (int i = 0; i < TN; i++) {
+            const Op ac = operand<EXACT>(t.cut_tail(t.wfrag(S, i)));
+#pragma unroll
+            for (int c = 0; c < TM; c++) add(i, c, group_sum(ac, bf[c]));
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < TN; i++)
-#pragma unroll
-        for (int c = 0; c < TM; c++)
-            store4(a, m0 + 16 * (TM * wm + c) + r, n0 + 16 * (TN * wn + i) + 4 * g, acc[i][c]);
+    t.store(a, acc);
 }
 
 // Sum of the K slices' partial results, in slice order.
@@ -461,25 +573,153 @@ __global__ void __launch_bounds__(256) fp8_join(F8Args a, const float* part, uin
 }
 
 template <int CT, int RT, int U, int NW>
-hipError_t launch_skinny(const F8Args& a, uint32_t slices, hipStream_t s)
+hipError_t launch_skinny(const F8Args& a, hipStream_t s)
 {
-    const dim3 grid(static_cast<uint32_t>(((a.N + 16 * RT - 1) / (16 * RT)) * ((a.M + 16 * CT - 1) / (16 * CT))), 1, slices);
+    const dim3 grid(static_cast<uint32_t>(((a.N + 16 * RT - 1) / (16 * RT)) * ((a.M + 16 * CT - 1) / (16 * CT))), 1, a.slices);
     hipLaunchKernelGGL((fp8_skinny<CT, RT, U, NW>), grid, dim3(64 * NW), 0, s, a);
     return hipGetLastError();
 }
 
-template <int BN, int BM, int WN, int WM, int NST, bool EXACT>
-hipError_t launch_tile(const F8Args& a, uint32_t slices, hipStream_t s)
+template <int BN, int BM, int WN, int WM, int NST, int P, bool EXACT>
+hipError_t launch_tile(const F8Args& a, hipStream_t s)
 {
     constexpr size_t lds = NST * stage_bytes<BN, BM>();
     static_assert(lds <= 160 * 1024, "LDS");
     static uint64_t attr_done = 0;  // devices the LDS limit was raised on
-    const void* fn = reinterpret_cast<const void*>(&fp8_tile<BN, BM, WN, WM, NST, EXACT>);
-    hipError_t e = allow_lds(fn, lds, attr_done);
+    const auto fn = fp8_tile<BN, BM, WN, WM, NST, P, EXACT>;
+    hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds, attr_done);
     if (e != hipSuccess) return e;
-    const dim3 grid(static_cast<uint32_t>(((a.N + BN - 1) / BN) * ((a.M + BM - 1) / BM)), 1, slices);
-    hipLaunchKernelGGL((fp8_tile<BN, BM, WN, WM, NST, EXACT>), grid, dim3(64 * WN * WM), lds, s, a);
+    const dim3 grid(static_cast<uint32_t>(((a.N + BN - 1) / BN) * ((a.M + BM - 1) / BM)), 1, a.slices);
+    hipLaunchKernelGGL(fn, grid, dim3(64 * WN * WM), lds, s, a);
     return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------- choice
+// Kernel shapes and what a launch of them takes. The time of a launch is modelled as
+//   fixed + max(rounds of workgroups, bytes from HBM, bytes into the CUs) [+ joining K slices]
+// with constants fitted to 25000 launches measured on MI355X (M 1 to 4096, 12 pairs of N and K from
+// 128 to 28672, K slices 1 to 16): over those sizes the shape that the model picks takes 3% longer
+// than the fastest one on average, and 18% longer for one size in twenty.
+struct Shape {
+    int bn, bm, waves_k;  // rows of W and X per workgroup; waves that share a group out (tiles: 1)
+    int per_cu;           // workgroups that fit a CU
+    hipError_t (*launch)(const F8Args&, hipStream_t);
+    float fixed;       // us: launch, first loads, last stores
+    float extra;       // steps: filling and draining the pipeline
+    float step1, stepn;  // us per step with one and with per_cu workgroups on a CU
+    float hbm, cu;     // TB/s from memory, into the CUs
+    float again;       // share of W read again for every further tile along M
+};
+constexpr float kJoinFixed = 2.7f, kJoinRate = 2.7f;  // us; TB/s of partial sums written and read
+
+const Shape kSums[] = {
+    {256, 256, 1, 1, launch_tile<256, 256, 2, 4, 2, 2, false>, 7.21f, 1.79f, 1.37f, 1.37f, 4.2f, 9.12f, 0.85f},
+    {256, 128, 1, 1, launch_tile<256, 128, 4, 2, 3, 2, false>, 4.52f, 2.57f, 0.828f, 0.828f, 5.3f, 11.2f, 0.66f},
+    {128, 128, 1, 2, launch_tile<128, 128, 4, 2, 2, 1, false>, 4.45f, 0.586f, 0.578f, 1.03f, 5.74f, 14.0f, 0.76f},
+    {128, 64, 1, 2, launch_tile<128, 64, 4, 1, 3, 1, false>, 3.56f, 2.4f, 0.493f, 0.74f, 5.75f, 16.5f, 0.51f},
+    {128, 32, 1, 2, launch_tile<128, 32, 4, 1, 3, 1, false>, 3.42f, 2.04f, 0.342f, 0.515f, 6.08f, 20.1f, 0.31f},
+    {16, 16, 8, 8, launch_skinny<1, 1, 1, 8>, 3.18f, 0.47f, 0.523f, 3.75f, 5.5f, 10.1f, 0.3f},
+    {16, 16, 16, 2, launch_skinny<1, 1, 1, 16>, 3.07f, 0.48f, 1.04f, 2.4f, 5.8f, 9.6f, 0.3f},
+    {32, 16, 16, 2, launch_skinny<1, 2, 1, 16>, 3.1f, 0.335f, 1.83f, 4.82f, 5.5f, 10.0f, 0.5f},
+    {32, 32, 16, 1, launch_skinny<2, 2, 1, 16>, 2.88f, 0.316f, 2.85f, 2.85f, 3.6f, 8.25f, 0.3f},
+    {32, 64, 8, 2, launch_skinny<4, 2, 1, 8>, 3.5f, 0.295f, 1.9f, 3.66f, 3.2f, 9.5f, 0.3f},
+};
+const Shape kExact[] = {
+    {256, 128, 1, 1, launch_tile<256, 128, 4, 2, 3, 1, true>, 4.23f, 1.2f, 1.65f, 1.65f, 3.59f, 6.56f, 0.7f},
+    {128, 128, 1, 2, launch_tile<128, 128, 4, 2, 2, 1, true>, 3.8f, 1.23f, 0.998f, 2.07f, 3.25f, 7.29f, 0.78f},
+    {128, 64, 1, 2, launch_tile<128, 64, 4, 1, 3, 1, true>, 4.16f, 0.757f, 0.726f, 1.15f, 4.73f, 10.5f, 0.55f},
+    {128, 32, 1, 2, launch_tile<128, 32, 4, 1, 3, 1, true>, 3.37f, 1.73f, 0.495f, 0.729f, 5.36f, 13.8f, 0.42f},
+    kSums[5], kSums[6], kSums[7], kSums[8], kSums[9],
+};
+constexpr uint32_t kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16};
+
+struct Plan {
+    const Shape* shape;
+    uint32_t slices;
+    double us;
+};
+
+size_t part_bytes(int64_t M, int64_t N, uint32_t slices)
+{
+    return slices > 1 ? static_cast<size_t>(slices) * M * ((N + 3) / 4 * 4) * sizeof(float) : 0;
+}
+
+double model_us(const Shape& h, int64_t M, int64_t N, int64_t K, bool bf16, uint32_t slices, uint32_t cus)
+{
+    const int64_t G = (K + kG - 1) / kG, tn = (N + h.bn - 1) / h.bn, tm = (M + h.bm - 1) / h.bm;
+    const int64_t groups = tn * tm * slices, round = static_cast<int64_t>(cus) * h.per_cu;
+    const int64_t last = (groups % round + cus - 1) / cus;
+    auto step = [&](int64_t k) {
+        return k == 0 ? 0.0 : h.per_cu == 1 ? h.step1 : h.step1 + (h.stepn - h.step1) * static_cast<double>(k - 1) / (h.per_cu - 1);
+    };
+    const double steps = static_cast<double>((G + slices - 1) / slices) / h.waves_k + h.extra;
+    const double run = (static_cast<double>(groups / round) * step(h.per_cu) + step(last)) * steps;
+    const double nk = static_cast<double>(N) * K, mk = static_cast<double>(M) * K, mn = static_cast<double>(M) * N;
+    const double hbm = (mk + nk * (1 + h.again * static_cast<double>((tm < 4 ? tm : 4) - 1)) + mn * (bf16 ? 2 : 4)) / (h.hbm * 1e6);
+    const double cu = static_cast<double>(tn) * tm * G * (h.bn + h.bm) * kG / (h.cu * 1e6);
+    const double join = slices > 1 ? kJoinFixed + static_cast<double>(part_bytes(M, N, slices)) / (kJoinRate * 1e6) : 0.0;
+    return h.fixed + (run > hbm ? (run > cu ? run : cu) : (hbm > cu ? hbm : cu)) + join;
+}
+
+// The fastest shape and slice count by the model, for a workspace of ws bytes.
+Plan make_plan(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws, uint32_t cus)
+{
+    const Shape* shapes = bf16 ? kSums : kExact;
+    const int n = bf16 ? sizeof kSums / sizeof(Shape) : sizeof kExact / sizeof(Shape);
+    const int64_t G = (K + kG - 1) / kG;
+    Plan best = {nullptr, 1, 0};
+    for (int i = 0; i < n; i++) {
+        if (shapes[i].waves_k == 1 && K < kG) continue;  // the tiles read whole groups of K
+        for (uint32_t s : kSlices) {
+            if (s > 1 && (G < 2 * s || part_bytes(M, N, s) > ws)) break;
+            const double us = model_us(shapes[i], M, N, K, bf16, s, cus);
+            if (!best.shape || us < best.us) best = {&shapes[i], s, us};
+        }
+    }
+    return best;
+}
+
+// The plan of a call, kept per thread by the sizes it follows from (the model takes about 2 us).
+Plan plan_for(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws)
+{
+    struct Entry {
+        int64_t M, N, K;
+        size_t ws;
+        uint32_t cus;
+        bool bf16;
+        Plan plan;
+    };
+    static thread_local Entry kept[64] = {};
+    const uint32_t cus = cu_count();
+    const uint64_t hash = static_cast<uint64_t>(M) * 0x9E3779B97F4A7C15u ^ static_cast<uint64_t>(N) * 0xC2B2AE3D27D4EB4Fu ^
+                          static_cast<uint64_t>(K) * 0x165667B19E3779F9u ^ (bf16 ? 0x27D4EB2F165667C5u : 0);
+    Entry& e = kept[hash >> 58];
+    if (!e.plan.shape || e.M != M || e.N != N || e.K != K || e.ws != ws || e.cus != cus || e.bf16 != bf16)
+        e = {M, N, K, ws, cus, bf16, make_plan(M, N, K, bf16, ws, cus)};
+    return e.plan;
+}
+
+hipError_t run_plan(F8Args& a, const Plan& p, void* d_ws, hipStream_t s)
+{
+    if (p.slices == 1) return p.shape->launch(a, s);
+    a.slices = p.slices;
+    a.N4 = (a.N + 3) / 4 * 4;
+    a.part = static_cast<float*>(d_ws);
+    const hipError_t e = p.shape->launch(a, s);
+    if (e != hipSuccess) return e;
+    a.part = nullptr;
+    const int64_t quads = a.M * (a.N4 / 4);
+    hipLaunchKernelGGL(fp8_join, dim3(static_cast<uint32_t>((quads + 255) / 256)), dim3(256), 0, s, a,
+                       static_cast<const float*>(d_ws), p.slices);
+    return hipGetLastError();
+}
+
+constexpr size_t kWorkspaceMost = size_t{256} << 20;  // K slices that need more are not planned
+
+bool gemm_sizes_ok(int64_t M, int64_t N, int64_t K)
+{
+    return M >= 0 && N >= 1 && K >= 1 && M <= INT32_MAX && N <= INT32_MAX && K <= INT32_MAX &&
+           (M + 15) / 16 * ((N + 15) / 16) <= INT32_MAX;  // the smallest tiles are 16 x 16
 }
 
 uw_status check_gemm(const uw_fp8_gemm_args* p)
@@ -487,7 +727,7 @@ uw_status check_gemm(const uw_fp8_gemm_args* p)
     if (!p) return fail(UW_EINVAL, "NULL argument");
     if (p->M < 0 || p->N < 1 || p->K < 1)
         return fail(UW_ESHAPE, "bad shape M=%lld N=%lld K=%lld", (long long)p->M, (long long)p->N, (long long)p->K);
-    if (p->M > INT32_MAX || p->N > INT32_MAX || p->K > INT32_MAX) return fail(UW_EUNSUPPORTED, "M, N or K too large");
+    if (!gemm_sizes_ok(p->M, p->N, p->K)) return fail(UW_EUNSUPPORTED, "M, N or K too large");
     if (p->y_type != UW_F32 && p->y_type != UW_BF16) return fail(UW_EINVAL, "bad y_type %d", p->y_type);
     if (p->M == 0) return UW_OK;
     if (!p->d_x || !p->d_sx || !p->d_w || !p->d_sw || !p->d_y) return fail(UW_EINVAL, "NULL device pointer");
@@ -511,10 +751,14 @@ using namespace uw;
 
 size_t uw_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K)
 {
-    (void)M;
-    (void)N;
-    (void)K;
-    return 0;
+    if (!gemm_sizes_ok(M, N, K) || M == 0) return 0;
+    size_t most = 0;
+    for (int bf16 = 0; bf16 < 2; bf16++) {
+        const Plan p = plan_for(M, N, K, bf16, kWorkspaceMost);
+        const size_t need = part_bytes(M, N, p.slices);
+        most = need > most ? need : most;
+    }
+    return most;
 }
 
 uw_status uw_fp8_gemm(const uw_fp8_gemm_args* p, void* stream)
@@ -537,20 +781,9 @@ uw_status uw_fp8_gemm(const uw_fp8_gemm_args* p, void* stream)
     a.ldsw = p->ldsw;
     a.ldy = p->ldy;
     a.bf16 = p->y_type == UW_BF16;
-    a.slice = static_cast<uint32_t>((p->K + kG - 1) / kG);
-    // the smallest tiles are 16 x 16
-    if ((a.M + 15) / 16 * ((a.N + 15) / 16) > INT32_MAX) return fail(UW_EUNSUPPORTED, "more than 2^31 - 1 tiles");
+    a.slices = 1;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e;
-    if (a.M <= 16)
-        e = launch_skinny<1, 1, 4, 4>(a, 1, s);
-    else if (a.M <= 32)
-        e = launch_skinny<2, 2, 2, 4>(a, 1, s);
-    else if (a.M <= 64 || a.K < kG)  // the tiles read whole groups of K
-        e = launch_skinny<4, 4, 2, 4>(a, 1, s);
-    else if (a.bf16)
-        e = launch_tile<256, 256, 2, 4, 2, false>(a, 1, s);
-    else
-        e = launch_tile<256, 256, 2, 4, 2, true>(a, 1, s);
+    const Plan plan = plan_for(a.M, a.N, a.K, a.bf16, p->d_ws ? (p->ws_bytes < kWorkspaceMost ? p->ws_bytes : kWorkspaceMost) : 0);
+    const hipError_t e = run_plan(a, plan, p->d_ws, s);
     return e == hipSuccess ? UW_OK : fail(UW_EHIP, "GEMM launch failed: %s", hipGetErrorString(e));
 }
