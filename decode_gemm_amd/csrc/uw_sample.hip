@@ -2,17 +2,25 @@
 // number, one token per row.
 //
 // Mathematics. With tokens ordered by (logit descending, index ascending), every filter keeps
-// a beginning of the order, and the draw asks where a running mass crosses a number. So no row is
-// ever sorted: each question is "the first token in the order at which the running count or mass
-// reaches t", and it is answered from a histogram over the exponent y = (l - max) log2(e) / T
-// (monotone in l, so bins are in order), then among the tokens of one bin. Masses are
-// integers, round(2^43 * 2^y) from a 64-bit exponential, so sums are exact, the same in any order
-// (atomics included), and two questions about the same tokens never contradict each other.
+// a beginning of the order, and the draw asks where a running mass crosses a number. So each
+// question is "the first token in the order at which the running count or mass reaches t", and no
+// row is ever sorted as a whole:
+//   - the beginning of the order, a few hundred tokens, is gathered and sorted. Its lower end tau
+//     comes from the largest logit of each thread's share: the q-th largest of those is reached
+//     by at least q tokens, and hardly more while q is well below the number of threads.
+//   - a question that reaches past it is answered from a histogram of masses over the
+//     exponent y = (l - max) log2(e) / T (monotone in l, so bins are in order), and then among the
+//     tokens of one bin.
+// Masses are integers, round(2^43 2^y) from a 64-bit exponential, so sums are exact, the same in
+// any order (atomics included), and two questions about the same tokens never contradict each
+// other.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "uw_internal.h"
+#include "uw_recon.h"
 
 namespace uw {
 
@@ -20,12 +28,12 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 1024;
-constexpr int kWaves = kThreads / 64;
-constexpr int kBins = 2048;            // 46 per unit of y: the 44 units that have mass fill 2024 of them
+constexpr int kBins = 2048;            // 46 per unit of y: the 44 units that have mass fill 2025 of them
 constexpr double kBinsPerUnit = 46.0;
 constexpr double kDeepest = -44.0;     // 2^43 * 2^y rounds to 0 from here down
-constexpr int kList = 2048;            // tokens of the questioned bins that are sorted in LDS
+constexpr int kList = 2048;            // tokens that are sorted in LDS
+constexpr uint32_t kAim = 256;         // tokens that the gathered beginning of the order has at least
+constexpr int kShort = 512;            // largest k that it is made to hold
 constexpr u64 kOne = u64{1} << 43;     // mass of the row's largest token
 
 struct SampleArgs {
@@ -44,31 +52,27 @@ struct SampleArgs {
 __device__ __forceinline__ float value(const float* x, int i) { return x[i]; }
 __device__ __forceinline__ float value(const uint16_t* x, int i) { return __uint_as_float(static_cast<uint32_t>(x[i]) << 16); }
 
-// 2^f for f in [-0.5, 0.5] by its series in (f ln 2), twelve terms: the first one left out is
-// below 2e-16 of the result.
-__device__ __forceinline__ double exp2_poly(double f)
-{
-    const double t = f * 0.69314718055994530942;
-    double p = 1.0 / 479001600.0;
-    p = __builtin_fma(p, t, 1.0 / 39916800.0);
-    p = __builtin_fma(p, t, 1.0 / 3628800.0);
-    p = __builtin_fma(p, t, 1.0 / 362880.0);
-    p = __builtin_fma(p, t, 1.0 / 40320.0);
-    p = __builtin_fma(p, t, 1.0 / 5040.0);
-    p = __builtin_fma(p, t, 1.0 / 720.0);
-    p = __builtin_fma(p, t, 1.0 / 120.0);
-    p = __builtin_fma(p, t, 1.0 / 24.0);
-    p = __builtin_fma(p, t, 1.0 / 6.0);
-    p = __builtin_fma(p, t, 0.5);
-    p = __builtin_fma(p, t, 1.0);
-    return __builtin_fma(p, t, 1.0);
-}
+// Adding kRound to a double of less than 2^31 leaves its nearest whole number in the low 32 bits: two
+// additions in place of a rounding and a conversion, which take four times an addition's time each.
+constexpr double kRound = 6755399441055744.0;  // 3 * 2^51
+__device__ __forceinline__ int low_bits(double v) { return static_cast<int>(__double_as_longlong(v)); }
 
-// 2^43 * 2^y as a double, for y in (-44, 0].
+// 2^43 * 2^y for y in (-44, 0]: 2^f for the fraction f in [-0.5, 0.5] as 1 + f q(f), q the polynomial
+// that meets (2^f - 1) / f at the eight Chebyshev points; within 2.2e-12 of the value, and exact at 0.
+// The whole part goes into the exponent bits.
 __device__ __forceinline__ double weight(double y)
 {
-    const double n = __builtin_rint(y);
-    return __builtin_ldexp(exp2_poly(y - n), static_cast<int>(n) + 43);
+    const double t = y + kRound, f = y - (t - kRound);
+    double q = 0x1.63b2d796f0517p-20;
+    q = __builtin_fma(q, f, 0x1.00c0e4e1521c8p-16);
+    q = __builtin_fma(q, f, 0x1.4308c7183d81ep-13);
+    q = __builtin_fma(q, f, 0x1.5d877598350f3p-10);
+    q = __builtin_fma(q, f, 0x1.3b2ab70ad2565p-7);
+    q = __builtin_fma(q, f, 0x1.c6b08da70cce3p-5);
+    q = __builtin_fma(q, f, 0x1.ebfbdff82a734p-3);
+    q = __builtin_fma(q, f, 0x1.62e42fef9cc69p-1);
+    const u64 b = static_cast<u64>(__double_as_longlong(__builtin_fma(q, f, 1.0)));
+    return __longlong_as_double(static_cast<long long>(b + (static_cast<u64>(static_cast<uint32_t>(low_bits(t) + 43) << 20) << 32)));
 }
 
 // Nearest whole number (ties to even) of 0 <= w < 2^52.
@@ -81,16 +85,16 @@ __device__ __forceinline__ u64 whole(double w)
 struct Scale {
     float top;  // largest logit
     double c;   // log2(e) / T
-    // y of logit l; anything at or below kDeepest has no mass
+    // y of logit l. Masked logits come out as -inf or NaN, and finite ones beside an infinite top
+    // too: callers take y > kDeepest only.
     __device__ __forceinline__ double y(float l) const
     {
-        if (l == top) return 0.0;                    // also +inf - +inf
-        if (!(l < top) || top == INFINITY || l == -INFINITY) return -INFINITY;  // NaN; finite beside +inf; masked
-        return (static_cast<double>(l) - static_cast<double>(top)) * c;
+        return l == top ? 0.0 : (static_cast<double>(l) - static_cast<double>(top)) * c;
     }
 };
 
-__device__ __forceinline__ int bin_of(double y) { return static_cast<int>(-y * kBinsPerUnit); }
+// Bin b holds the y nearest to -b / 46.
+__device__ __forceinline__ int bin_of(double y) { return low_bits(__builtin_fma(y, -kBinsPerUnit, kRound)); }
 
 // Sort key of (logit, index): ascending keys are the order. -0 and +0 are equal logits.
 __device__ __forceinline__ uint32_t order_bits(float l)
@@ -99,44 +103,70 @@ __device__ __forceinline__ uint32_t order_bits(float l)
     return (b & 0x80000000u) ? b : ~(b | 0x80000000u);  // larger logits get smaller bits
 }
 __device__ __forceinline__ float order_value(uint32_t o) { return __uint_as_float((o & 0x80000000u) ? o : ~o & 0x7FFFFFFFu); }
+__device__ __forceinline__ u64 key_of(float l, int i) { return (static_cast<u64>(order_bits(l)) << 32) | static_cast<uint32_t>(i); }
+__device__ __forceinline__ float key_value(u64 key) { return order_value(static_cast<uint32_t>(key >> 32)); }
 
-struct Shared {
-    u64 H[kBins + 1];       // mass before each bin (while the histogram is made: mass of it)
-    uint32_t C[kBins + 1];  // tokens before each bin
-    u64 base[kBins];        // list path: H[bin] - mass in the list before the bin
-    uint32_t cbase[kBins];  // likewise for counts (mod 2^32); slow path: digit histogram
-    u64 list[kList];
-    uint32_t take[kBins / 32];  // bins whose tokens go to the list
-    u64 wsum[kWaves];
-    uint32_t wcnt[kWaves];
-    float wmax[kWaves];
-    uint32_t n;
-    int found[4];
-    u64 mass[4];
-    u64 drawn;
+// Bins in which the answers of a row's questions lie, and the logits of each range of bins (a little
+// widened): 0 top-k, 1 top-p, 2 min-p, 3 the draw.
+struct Marks {
+    u64 Z;              // mass of the row
+    float from[4], to[4];
+    uint32_t by_k;      // top-k cuts, in bin b1, before which are c1 tokens
+    int32_t b1;
+    uint32_t c1;
+    int32_t q0, q1;     // bins of min-p's cut
+    uint32_t take[kBins / 32];  // all these bins
 };
 
-__device__ __forceinline__ u64 shfl_up64(u64 v, int d)
+template <int NT>
+struct Shared {
+    u64 H[kBins + 1];       // mass before each bin (while the histogram is made: mass of it)
+    uint32_t C[kBins + 1];  // tokens before each bin, likewise
+    u64 list[kList];
+    u64 upto[kList];        // mass up to and with each token of the sorted list; scratch before that
+    Marks marks;
+    u64 wsum[NT / 64];
+    uint32_t wcnt[NT / 64];
+    float wmax[NT / 64];
+    uint32_t n, first, last, crowd;
+    int found[4];
+    u64 mass[4];
+    u64 drawn, kept;
+};
+
+// Inclusive sums over a wave's lanes (DPP: shifts within rows of 16, then row ends broadcast).
+__device__ __forceinline__ uint32_t dpp_from(uint32_t v, int step)
 {
-    const uint32_t lo = __shfl_up(static_cast<uint32_t>(v), d), hi = __shfl_up(static_cast<uint32_t>(v >> 32), d);
-    return (static_cast<u64>(hi) << 32) | lo;
+    switch (step) {
+    case 0: return __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+    case 1: return __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    case 2: return __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    case 3: return __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    case 4: return __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+    default: return __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+    }
+}
+__device__ __forceinline__ uint32_t wave_sums(uint32_t v)
+{
+#pragma unroll
+    for (int s = 0; s < 6; s++) v += dpp_from(v, s);
+    return v;
+}
+__device__ __forceinline__ u64 wave_sums(u64 v)
+{
+#pragma unroll
+    for (int s = 0; s < 6; s++)
+        v += (static_cast<u64>(dpp_from(static_cast<uint32_t>(v >> 32), s)) << 32) | dpp_from(static_cast<uint32_t>(v), s);
+    return v;
 }
 
 // Exclusive sums over the workgroup's threads.
-__device__ void block_scan(Shared& S, u64 m, uint32_t c, u64& em, uint32_t& ec)
+template <int NT>
+__device__ void block_sums(Shared<NT>& S, u64 m, uint32_t c, u64& em, uint32_t& ec)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    u64 im = m;
-    uint32_t ic = c;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const u64 a = shfl_up64(im, d);
-        const uint32_t b = __shfl_up(ic, d);
-        if (lane >= d) {
-            im += a;
-            ic += b;
-        }
-    }
+    const u64 im = wave_sums(m);
+    const uint32_t ic = wave_sums(c);
     __syncthreads();
     if (lane == 63) {
         S.wsum[wave] = im;
@@ -145,19 +175,412 @@ __device__ void block_scan(Shared& S, u64 m, uint32_t c, u64& em, uint32_t& ec)
     __syncthreads();
     em = im - m;
     ec = ic - c;
-    for (int w = 0; w < wave; w++) {
-        em += S.wsum[w];
-        ec += S.wcnt[w];
+#pragma unroll
+    for (int w = 0; w < NT / 64 - 1; w++) {
+        const u64 a = S.wsum[w];
+        const uint32_t b = S.wcnt[w];
+        em += w < wave ? a : 0;
+        ec += w < wave ? b : 0;
     }
 }
 
-// Smallest bin b with H[b + 1] >= t (1 <= t <= H[kBins]); all threads get it.
-__device__ int find_mass(Shared& S, u64 t, int slot)
+// Largest of the threads' values, for all of them.
+template <int NT>
+__device__ __forceinline__ float block_max(Shared<NT>& S, float v)
 {
-    for (int b = threadIdx.x; b < kBins; b += kThreads)
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) S.wmax[threadIdx.x >> 6] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 64; w++) v = fmaxf(v, S.wmax[w]);
+    return v;
+}
+
+// test(logit) for the logits i0 .. i1-1 of a row, once each, by all threads of the workgroup, and
+// act(logit, index) for those that pass (NaN must not). 16-byte loads between the 16-byte boundaries, up
+// to 32 logits on the way per thread. What passes is noted in a mask and acted on in one loop: most
+// code here runs once or twice per launch, and fetching instructions costs more than running them, so
+// only the test is unrolled.
+template <int NT, int L, class T, class Test, class Act>
+__device__ __forceinline__ void each_if(const T* x, int i0, int i1, Test test, Act act)
+{
+    constexpr int W = 16 / sizeof(T), U = L / W;  // logits per load, loads on the way
+    static_assert(L <= 32 && U >= 1, "mask");
+    const int tid = threadIdx.x;
+    int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x + i0) & 15)) & 15) / static_cast<int>(sizeof(T));
+    head = head < i1 - i0 ? head : i1 - i0;
+    const int a = i0 + head, nv = (i1 - a) / W, tail = a + nv * W;
+    const u32x4* v = reinterpret_cast<const u32x4*>(x + a);
+    for (int j0 = 0; j0 < nv; j0 += U * NT) {
+        u32x4 q[U];
+#pragma unroll
+        for (int e = 0; e < U; e++) {
+            const int j = j0 + e * NT + tid;
+            q[e] = u32x4{~0u, ~0u, ~0u, ~0u};  // NaN
+            if (j < nv) q[e] = v[j];
+        }
+        uint32_t passed = 0;
+#pragma unroll
+        for (int e = 0; e < U; e++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                if constexpr (W == 4) {
+                    passed |= test(__uint_as_float(q[e][c])) ? 1u << (W * e + c) : 0u;
+                } else {
+                    passed |= test(__uint_as_float(q[e][c] << 16)) ? 1u << (W * e + 2 * c) : 0u;
+                    passed |= test(__uint_as_float(q[e][c] & 0xFFFF0000u)) ? 1u << (W * e + 2 * c + 1) : 0u;
+                }
+            }
+        while (passed) {
+            const int b = __ffs(passed) - 1;
+            passed &= passed - 1;
+            const int at = a + W * (j0 + b / W * NT + tid) + b % W;
+            act(value(x, at), at);
+        }
+    }
+    if (tid < head + (i1 - tail)) {
+        const int at = tid < head ? i0 + tid : tail + tid - head;
+        const float l = value(x, at);
+        if (test(l)) act(l, at);
+    }
+}
+
+// f(logit) for the logits of a whole row that have mass, with their y.
+template <int NT, class T, class F>
+__device__ __forceinline__ void each_mass(const T* x, int V, const Scale& sc, F f)
+{
+    each_if<NT, 8>(x, 0, V, [&](float l) { return sc.y(l) > kDeepest; }, [&](float l, int) { f(l, sc.y(l)); });
+}
+
+// A row's settings, brought into range.
+struct Row {
+    bool by_k, by_p, by_m;
+    int64_t k;
+    float temp;  // 1 for the greedy choice, which is k = 1
+    float p, least, u;
+    bool only_first;  // min-p above 1
+
+    __device__ __forceinline__ Row(const SampleArgs& a, int64_t row)
+    {
+        const float t = a.temperature ? a.temperature[row] : 1.0f;
+        const int32_t kk = a.top_k ? a.top_k[row] : 0;
+        const float m = a.min_p ? a.min_p[row] : 0.0f, v = a.u[row];
+        p = a.top_p ? a.top_p[row] : 1.0f;
+        const bool greedy = !(t > 0.0f);
+        temp = greedy ? 1.0f : t;
+        k = greedy ? 1 : kk;
+        by_k = k > 0 && k < a.V;
+        by_p = p < 1.0f;
+        by_m = m > 0.0f && m >= 0x1p-44f;
+        only_first = m > 1.0f;
+        least = fminf(m, 1.0f);
+        u = v > 0.0f ? fminf(v, 0x1.fffffep-1f) : 0.0f;
+    }
+    // the mass that top-p asks of m, and the one that the draw asks of m
+    __device__ __forceinline__ u64 p_target(u64 m) const
+    {
+        const double t = ceil(static_cast<double>(p) * static_cast<double>(m));
+        const u64 v = t >= 1.0 ? static_cast<u64>(t) : 1;
+        return v < m ? v : m;
+    }
+    __device__ __forceinline__ u64 u_target(u64 m) const { return static_cast<u64>(static_cast<double>(u) * static_cast<double>(m)) + 1; }
+    // the least whole mass that min-p keeps
+    __device__ __forceinline__ u64 least_mass() const { return static_cast<u64>(ceil(static_cast<double>(least) * static_cast<double>(kOne))); }
+    // whether the beginning of the order answers top-k: then no masses of other tokens are needed
+    __device__ __forceinline__ bool short_k() const { return by_k && k <= kShort; }
+    __device__ __forceinline__ Scale scale(float top) const { return Scale{top, 1.4426950408889634074 / static_cast<double>(temp)}; }
+};
+
+// Smallest bin b with H[b + 1] >= t (1 <= t <= H[kBins]); all threads get it.
+template <int NT>
+__device__ int find_mass(Shared<NT>& S, u64 t, int slot)
+{
+    for (int b = threadIdx.x; b < kBins; b += NT)
         if (S.H[b] < t && t <= S.H[b + 1]) S.found[slot] = b;
     __syncthreads();
     return S.found[slot];
+}
+
+// H and (counts) C from contents of bins to sums before each bin.
+template <int NT>
+__device__ void bins_to_sums(Shared<NT>& S, bool masses, bool counts)
+{
+    constexpr int B = kBins / NT;
+    const int b0 = B * threadIdx.x;
+    u64 m[B], mt = 0;
+    uint32_t c[B], ct = 0;
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < B; b++) {
+        m[b] = masses ? S.H[b0 + b] : 0;
+        c[b] = counts ? S.C[b0 + b] : 0;
+        mt += m[b];
+        ct += c[b];
+    }
+    u64 em;
+    uint32_t ec;
+    block_sums(S, mt, ct, em, ec);
+#pragma unroll
+    for (int b = 0; b < B; b++) {
+        if (masses) S.H[b0 + b] = em;
+        if (counts) S.C[b0 + b] = ec;
+        em += m[b];
+        ec += c[b];
+    }
+    if (threadIdx.x == NT - 1) {
+        if (masses) S.H[kBins] = em;
+        if (counts) S.C[kBins] = ec;
+    }
+    __syncthreads();
+}
+
+template <int NT>
+__device__ __forceinline__ void clear_bins(Shared<NT>& S, bool masses, bool counts)
+{
+    for (int b = threadIdx.x; b < kBins; b += NT) {
+        if (masses) S.H[b] = 0;
+        if (counts) S.C[b] = 0;
+    }
+}
+
+// A logit at or below the lower end of bin b (bins of smaller number hold larger logits).
+__device__ __forceinline__ float below_bin(const Scale& sc, int b)
+{
+    if (sc.top == INFINITY) return INFINITY;
+    const float t = static_cast<float>(static_cast<double>(sc.top) - (static_cast<double>(b) + 0.5) / kBinsPerUnit / sc.c);
+    return t - fabsf(t) * 0x1p-22f - FLT_MIN;  // a little less, for the roundings; -inf where all logits weigh the same
+}
+
+// A logit that at least q of the threads' maxima `mine` reach; -inf if fewer than q have mass.
+template <int NT>
+__device__ float reached_by(Shared<NT>& S, float mine, const Scale& sc, uint32_t q)
+{
+    clear_bins(S, false, true);
+    if (threadIdx.x == 0) S.found[0] = -1;
+    __syncthreads();
+    const double y = sc.y(mine);
+    if (y > kDeepest) atomicAdd(&S.C[bin_of(y)], 1u);
+    bins_to_sums(S, false, true);
+    for (int b = threadIdx.x; b < kBins; b += NT)
+        if (S.C[b] < q && q <= S.C[b + 1]) S.found[0] = b;
+    __syncthreads();
+    const int b = S.found[0];
+    return b < 0 ? -INFINITY : below_bin(sc, b);
+}
+
+template <int NT>
+__device__ __forceinline__ void append(Shared<NT>& S, float l, int i)
+{
+    const uint32_t at = atomicAdd(&S.n, 1u);
+    if (at < kList) S.list[at] = key_of(l, i);
+}
+
+// The tokens of i0 .. i1-1 that reach tau go to the list (counted in S.n, which may pass kList); with
+// `masses` all tokens' masses go to the histogram.
+template <int NT, class T>
+__device__ void gather(Shared<NT>& S, const T* x, int i0, int i1, const Scale& sc, float tau, bool masses)
+{
+    auto act = [&](float l, int i) {
+        if (sc.y(l) > kDeepest) append(S, l, i);
+    };
+    const double top = static_cast<double>(sc.top);
+    const float end = below_bin(sc, static_cast<int>(-kDeepest * kBinsPerUnit));
+    if (masses)
+        each_if<NT, 16>(
+            x, i0, i1,
+            [&](float l) {
+                // Without branches, so that the exponentials of several logits overlap: what has no mass (NaN
+                // too) adds to a place of its lane's own. (The largest logit is finite here, and masses
+                // a little below the end are 0.)
+                const double y = fmax((static_cast<double>(l) - top) * sc.c, kDeepest - 0.49);
+                atomicAdd(l > end ? &S.H[bin_of(y)] : &S.upto[threadIdx.x & 63], whole(weight(y)));
+                return l >= tau;
+            },
+            act);
+    else
+        each_if<NT, 32>(x, i0, i1, [&](float l) { return l >= tau; }, act);
+}
+
+// Sort the n (1 .. kList) tokens of the list: into bins that share out the range between its largest
+// and smallest logit, then by comparing within a bin. Lists that crowd a bin (ties) go through a
+// bitonic network instead. Uses C.
+template <int NT>
+__device__ void sort_list(Shared<NT>& S, int n)
+{
+    const int tid = threadIdx.x;
+    uint32_t lo = ~0u, hi = 0;
+    if (tid == 0) {
+        S.first = ~0u;
+        S.last = 0;
+        S.crowd = 0;
+    }
+    clear_bins(S, false, true);
+    for (int i = tid; i < n; i += NT) {
+        const uint32_t o = static_cast<uint32_t>(S.list[i] >> 32);
+        lo = o < lo ? o : lo;
+        hi = o > hi ? o : hi;
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        const uint32_t a = __shfl_xor(lo, d), b = __shfl_xor(hi, d);
+        lo = a < lo ? a : lo;
+        hi = b > hi ? b : hi;
+    }
+    __syncthreads();
+    if ((tid & 63) == 0) {
+        atomicMin(&S.first, lo);
+        atomicMax(&S.last, hi);
+    }
+    __syncthreads();
+    const float top = order_value(S.first), span = top - order_value(S.last);
+    const float scale = span > 0.f && span < INFINITY ? (kBins - 1) / span : 0.f;
+    auto bin = [&](u64 k) {
+        const int b = scale > 0.f ? static_cast<int>((top - key_value(k)) * scale) : 0;
+        return b < kBins - 1 ? b : kBins - 1;
+    };
+    for (int i = tid; i < n; i += NT)
+        if (atomicAdd(&S.C[bin(S.list[i])], 1u) == 31) S.crowd = 1;
+    __syncthreads();
+    if (!S.crowd) {
+        bins_to_sums(S, false, true);
+        for (int i = tid; i < n; i += NT) {
+            const u64 k = S.list[i];
+            S.upto[atomicAdd(&S.C[bin(k)], 1u)] = k;
+        }
+        __syncthreads();
+        // C[b] has come to the end of bin b
+        for (int i = tid; i < n; i += NT) {
+            const u64 k = S.upto[i];
+            const int b = bin(k), i0 = b ? S.C[b - 1] : 0, i1 = S.C[b];
+            int at = i0;
+            for (int e = i0; e < i1; e++) at += S.upto[e] < k;
+            S.list[at] = k;
+        }
+        __syncthreads();
+        return;
+    }
+    int size = 64;
+    while (size < n) size <<= 1;
+    for (int i = n + tid; i < size; i += NT) S.list[i] = ~u64{0};
+    __syncthreads();
+    for (int width = 2; width <= size; width <<= 1)
+        for (int d = width >> 1; d; d >>= 1) {
+            for (int i = tid; i < size / 2; i += NT) {
+                const int a0 = 2 * i - (i & (d - 1)), a1 = a0 + d;
+                const u64 v0 = S.list[a0], v1 = S.list[a1];
+                if ((v0 > v1) == ((a0 & width) == 0)) {
+                    S.list[a0] = v1;
+                    S.list[a1] = v0;
+                }
+            }
+            __syncthreads();
+        }
+}
+
+__device__ __forceinline__ u64 mass_of(const Scale& sc, u64 key) { return whole(weight(sc.y(key_value(key)))); }
+
+// upto[] of the sorted list: masses summed within the list (rows == false), or over the row by the
+// sums in H, where the list holds whole bins (H of those bins is used up). Returns the place of the
+// first token of bin b1 in the list (rows only).
+template <int NT>
+__device__ int sum_list(Shared<NT>& S, int n, const Scale& sc, bool rows, int b1)
+{
+    const int tid = threadIdx.x, share = (n + NT - 1) / NT;
+    const int from = tid * share < n ? tid * share : n, to = from + share < n ? from + share : n;
+    u64 total = 0, before;
+    for (int i = from; i < to; i++) {
+        const u64 m = mass_of(sc, S.list[i]);
+        S.upto[i] = m;
+        total += m;
+    }
+    uint32_t unused;
+    if (tid == 0) S.found[3] = 0;
+    block_sums(S, total, 0, before, unused);
+    u64 m = before;
+    auto bin = [&](int i) { return bin_of(sc.y(key_value(S.list[i]))); };
+    for (int i = from; i < to; i++) {
+        if (rows) {
+            const int b = bin(i);
+            if (i == 0 || bin(i - 1) != b) {
+                S.H[b] -= m;  // what comes before the bin and is not in the list
+                if (b == b1) S.found[3] = i;
+            }
+        }
+        m += S.upto[i];
+        S.upto[i] = m;
+    }
+    __syncthreads();
+    if (rows) {
+        for (int i = from; i < to; i++) S.upto[i] += S.H[bin(i)];
+        __syncthreads();
+    }
+    return S.found[3];
+}
+
+// First i < n with reached(i), which once true stays true; n if none. By one wave, two looks of 64.
+template <class F>
+__device__ __forceinline__ int first_that(int n, F reached)
+{
+    const int lane = threadIdx.x & 63, stride = (n + 63) / 64;  // n <= 64 * 64
+    const int end = (lane + 1) * stride < n ? (lane + 1) * stride : n;
+    const u64 a = __ballot(reached(end - 1));
+    if (!a) return n;
+    const int from = (__ffsll(static_cast<long long>(a)) - 1) * stride;
+    const u64 b = __ballot(lane < stride && (from + lane >= n || reached(from + lane)));
+    return from + __ffsll(static_cast<long long>(b)) - 1;
+}
+
+// Answer from the sorted beginning of the order (n tokens; all: every token with mass is in it; Z: the
+// row's mass, 0 if not known). Leaves the token in S.drawn and returns the mass kept; 0 if a
+// question reaches past the list.
+template <int NT>
+__device__ u64 from_list(Shared<NT>& S, const Row& r, const Scale& sc, int n, bool all, u64 Z)
+{
+    if (Z && !r.by_m) {
+        // without min-p the first question decides: does it reach past the list?
+        u64 m = 0, before;
+        uint32_t unused;
+        for (int i = threadIdx.x; i < n; i += NT) m += mass_of(sc, S.list[i]);
+        block_sums(S, m, 0, before, unused);
+        if (threadIdx.x == NT - 1) S.mass[0] = before + m;
+        __syncthreads();
+        if ((r.by_p ? r.p_target(Z) : r.u_target(Z)) > S.mass[0]) return 0;
+    }
+    sort_list(S, n);
+    sum_list(S, n, sc, false, 0);
+    if (threadIdx.x < 64) {
+        const u64 L = S.upto[n - 1];
+        u64 kept = all ? L : Z;  // 0: not known, but more than the list
+        bool open = false;       // a question reaches past the list
+        if (r.by_k && r.k <= n)
+            kept = S.upto[r.k - 1];
+        else if (r.by_k && !all)
+            open = true;
+        if (r.by_p) {
+            const u64 t = kept ? r.p_target(kept) : ~u64{0};
+            kept = t <= L ? S.upto[first_that(n, [&](int i) { return S.upto[i] >= t; })] : 0;
+        }
+        if (r.by_m) {
+            const u64 w = r.least_mass();
+            const int i = r.only_first ? 1 : first_that(n, [&](int j) { return mass_of(sc, S.list[j]) < w; });
+            const u64 m = i > 0 ? S.upto[i - 1] : S.upto[0];
+            if (i < n || all)
+                kept = kept && kept < m ? kept : m;
+            else if (kept > L)
+                kept = 0;  // the cut may lie past the list
+        }
+        const u64 t = kept ? r.u_target(kept) : ~u64{0};
+        open |= t > L;
+        if (!open) {
+            const int i = first_that(n, [&](int j) { return S.upto[j] >= t; });
+            if (threadIdx.x == 0) S.drawn = S.list[i];
+        }
+        if (threadIdx.x == 0) S.kept = open ? 0 : kept;
+    }
+    __syncthreads();
+    return S.kept;
 }
 
 // Where the running count (by_count) or mass reaches t inside bin b, found without a list: four
@@ -165,14 +588,15 @@ __device__ int find_mass(Shared& S, u64 t, int slot)
 // share those already known, leave one logit; its tokens weigh the same, so the crossing
 // one is found by division. Returns the mass up to and with the crossing token; if `index`, also
 // the token (a pass that counts that logit's tokens in order of index).
-template <class T>
-__device__ u64 search_row(Shared& S, const T* x, int V, const Scale& sc, int b, bool by_count, u64 t, bool index)
+template <int NT, class T>
+__device__ u64 search_row(Shared<NT>& S, const T* x, int V, const Scale& sc, int b, bool by_count, u64 t, bool index)
 {
     u64 m0 = S.H[b];
-    uint32_t c0 = S.C[b];
+    uint32_t c0 = by_count ? S.C[b] : 0;
     uint32_t prefix = 0;
-    u64* const dm = S.base;         // 256 digits' masses
-    uint32_t* const dc = S.cbase;   // and counts
+    u64* const dm = S.upto;                                      // 256 digits' masses
+    uint32_t* const dc = reinterpret_cast<uint32_t*>(S.list);    // and counts
+#pragma unroll 1
     for (int level = 0; level < 4; level++) {
         const int shift = 24 - 8 * level;
         __syncthreads();
@@ -181,22 +605,20 @@ __device__ u64 search_row(Shared& S, const T* x, int V, const Scale& sc, int b, 
             dc[threadIdx.x] = 0;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < V; i += kThreads) {
-            const float l = value(x, i);
-            const double y = sc.y(l);
-            if (!(y > kDeepest) || bin_of(y) != b) continue;
+        each_mass<NT>(x, V, sc, [&](float l, double y) {
+            if (bin_of(y) != b) return;
             const uint32_t o = order_bits(l);
-            if (level && (o >> (shift + 8)) != prefix) continue;
+            if (level && (o >> (shift + 8)) != prefix) return;
             const uint32_t d = (o >> shift) & 255u;
             atomicAdd(&dm[d], whole(weight(y)));
             atomicAdd(&dc[d], 1u);
-        }
+        });
         __syncthreads();
         const u64 m = threadIdx.x < 256 ? dm[threadIdx.x] : 0;
         const uint32_t c = threadIdx.x < 256 ? dc[threadIdx.x] : 0;
         u64 em;
         uint32_t ec;
-        block_scan(S, m, c, em, ec);
+        block_sums(S, m, c, em, ec);
         const bool here = by_count ? c0 + ec < t && t <= c0 + ec + c : m0 + em < t && t <= m0 + em + m;
         if (here) {
             S.found[3] = static_cast<int>(threadIdx.x);
@@ -212,281 +634,453 @@ __device__ u64 search_row(Shared& S, const T* x, int V, const Scale& sc, int b, 
     const u64 w = whole(weight(sc.y(l)));
     const u64 j = by_count ? t - c0 : (t - m0 + w - 1) / w;  // the j-th token of this logit, from 1
     if (index) {
-        const int chunk = (V + kThreads - 1) / kThreads;
+        const int chunk = (V + NT - 1) / NT;
         const int i0 = threadIdx.x * chunk, i1 = i0 + chunk < V ? i0 + chunk : V;
         uint32_t mine = 0;
         for (int i = i0; i < i1; i++) mine += value(x, i) == l;
         u64 em;
         uint32_t ec;
-        block_scan(S, 0, mine, em, ec);
+        block_sums(S, 0, mine, em, ec);
         if (ec < j && j <= ec + mine) {
             uint32_t seen = ec;
             for (int i = i0; i < i1; i++)
-                if (value(x, i) == l && ++seen == j) S.drawn = (static_cast<u64>(prefix) << 32) | static_cast<uint32_t>(i);
+                if (value(x, i) == l && ++seen == j) S.drawn = key_of(l, i);
         }
         __syncthreads();
     }
     return m0 + j * w;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) sample_rows(SampleArgs a)
+// The row's histogram of masses and counts, as sums.
+template <int NT, class T>
+__device__ void count_row(Shared<NT>& S, const T* x, int V, const Scale& sc)
 {
-    __shared__ Shared S;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t row = blockIdx.x;
-    const T* const x = static_cast<const T*>(a.x) + row * a.ld;
-    const int V = a.V;
-
-    // the row's settings
-    const float temp = a.temperature ? a.temperature[row] : 1.0f;
-    const bool greedy = !(temp > 0.0f);
-    int64_t k = greedy ? 1 : a.top_k ? a.top_k[row] : 0;
-    const float p = a.top_p ? a.top_p[row] : 1.0f;
-    const float mp = a.min_p ? a.min_p[row] : 0.0f;
-    float u = a.u[row];
-    u = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
-
-    // the largest logit
-    float top = -INFINITY;
-    for (int i = tid; i < V; i += kThreads) top = fmaxf(top, value(x, i));
-#pragma unroll
-    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    if (lane == 0) S.wmax[wave] = top;
-    for (int b = tid; b < kBins; b += kThreads) {
-        S.H[b] = 0;
-        S.C[b] = 0;
-    }
-    if (tid < kBins / 32) S.take[tid] = 0;
-    if (tid == 0) {
-        S.n = 0;
-        S.drawn = 0;
-    }
     __syncthreads();
-    for (int w = 0; w < kWaves; w++) top = fmaxf(top, S.wmax[w]);
-    if (top == -INFINITY) {  // nothing to draw
-        if (tid == 0) {
-            a.token[row] = -1;
-            if (a.prob) a.prob[row] = 0.0f;
-        }
-        return;
-    }
-    const Scale sc{top, 1.4426950408889634074 / (greedy ? 1.0 : static_cast<double>(temp))};
-
-    // histogram of counts and masses
-    for (int i = tid; i < V; i += kThreads) {
-        const double y = sc.y(value(x, i));
-        if (!(y > kDeepest)) continue;
+    clear_bins(S, true, true);
+    __syncthreads();
+    each_mass<NT>(x, V, sc, [&](float, double y) {
         const int b = bin_of(y);
         atomicAdd(&S.H[b], whole(weight(y)));
         atomicAdd(&S.C[b], 1u);
-    }
-    __syncthreads();
-    {
-        const u64 m0 = S.H[2 * tid], m1 = S.H[2 * tid + 1];
-        const uint32_t c0 = S.C[2 * tid], c1 = S.C[2 * tid + 1];
-        u64 em;
-        uint32_t ec;
-        block_scan(S, m0 + m1, c0 + c1, em, ec);
-        S.H[2 * tid] = em;
-        S.H[2 * tid + 1] = em + m0;
-        S.C[2 * tid] = ec;
-        S.C[2 * tid + 1] = ec + c0;
-        if (tid == kThreads - 1) {
-            S.H[kBins] = em + m0 + m1;
-            S.C[kBins] = ec + c0 + c1;
-        }
-    }
-    __syncthreads();
+    });
+    bins_to_sums(S, true, true);
+}
+
+// S.marks from the histogram (H as sums, and C if top-k is set). Later questions depend on earlier
+// answers, which are known so far to a bin: they get the range of bins that the bounds allow.
+template <int NT>
+__device__ void mark_bins(Shared<NT>& S, const Row& r, const Scale& sc)
+{
+    const int tid = threadIdx.x;
+    Marks& K = S.marks;
     const u64 Z = S.H[kBins];
-    const uint32_t tokens = S.C[kBins];
-
-    // Bins in which each question's answer lies. Later questions depend on earlier answers,
-    // which are known so far to a bin: they get the range of bins that the bounds allow.
-    const bool by_k = k > 0 && k < static_cast<int64_t>(tokens);
-    int b1 = 0;
-    u64 lo = Z, hi = Z;  // bounds of the mass kept
-    if (by_k) {
-        for (int b = tid; b < kBins; b += kThreads)
-            if (S.C[b] < k && k <= S.C[b + 1]) S.found[0] = b;
-        __syncthreads();
-        b1 = S.found[0];
-        lo = S.H[b1];
-        hi = S.H[b1 + 1];
-        if (lo < 1) lo = 1;
-        if (tid == 0) atomicOr(&S.take[b1 >> 5], 1u << (b1 & 31));
-    }
-    const bool by_p = p < 1.0f;
-    auto p_target = [&](u64 m) {
-        const double t = ceil(static_cast<double>(p) * static_cast<double>(m));
-        const u64 v = t >= 1.0 ? static_cast<u64>(t) : 1;
-        return v < m ? v : m;
-    };
-    if (by_p) {
-        const int f = find_mass(S, p_target(lo), 1), g = find_mass(S, p_target(hi), 2);
-        lo = S.H[f] < 1 ? 1 : S.H[f];
-        if (S.H[g + 1] < hi) hi = S.H[g + 1];
-        for (int b = f + tid; b <= g; b += kThreads) atomicOr(&S.take[b >> 5], 1u << (b & 31));
-    }
-    const bool by_m = mp > 0.0f && mp >= 0x1p-44f;
-    const float least = fminf(mp, 1.0f);
-    int q0 = 0, q1 = 0;
-    if (by_m) {
-        const int c = bin_of(log2(static_cast<double>(least)));
-        q0 = c > 0 ? c - 1 : 0;
-        q1 = c + 1 < kBins - 1 ? c + 1 : kBins - 1;
-        if (S.H[q0] < lo) lo = S.H[q0] < 1 ? 1 : S.H[q0];
-        if (S.H[q1 + 1] < hi) hi = S.H[q1 + 1];
-        for (int b = q0 + tid; b <= q1; b += kThreads) atomicOr(&S.take[b >> 5], 1u << (b & 31));
-    }
-    auto u_target = [&](u64 m) { return static_cast<u64>(static_cast<double>(u) * static_cast<double>(m)) + 1; };
-    {
-        __syncthreads();
-        const int f = find_mass(S, u_target(lo), 1), g = find_mass(S, u_target(hi), 2);
-        for (int b = f + tid; b <= g; b += kThreads) atomicOr(&S.take[b >> 5], 1u << (b & 31));
-    }
-    __syncthreads();
-    uint32_t n = 0;
-    {
-        uint32_t c = 0;
-        for (int b = 2 * tid; b < 2 * tid + 2; b++)
-            if ((S.take[b >> 5] >> (b & 31)) & 1u) c += S.C[b + 1] - S.C[b];
-        if (c) atomicAdd(&S.n, c);
-        __syncthreads();
-        n = S.n;
-        __syncthreads();
-        if (tid == 0) S.n = 0;
-    }
-    __syncthreads();
-
-    u64 kept = Z;
-    if (n <= kList) {
-        // their tokens, sorted
-        for (int i = tid; i < V; i += kThreads) {
-            const float l = value(x, i);
-            const double y = sc.y(l);
-            if (!(y > kDeepest)) continue;
-            const int b = bin_of(y);
-            if (!((S.take[b >> 5] >> (b & 31)) & 1u)) continue;
-            const uint32_t at = atomicAdd(&S.n, 1u);
-            S.list[at] = (static_cast<u64>(order_bits(l)) << 32) | static_cast<uint32_t>(i);
-        }
-        __syncthreads();
-        int size = 64;
-        while (size < static_cast<int>(n)) size <<= 1;
-        for (int i = n + tid; i < size; i += kThreads) S.list[i] = ~u64{0};
-        __syncthreads();
-        for (int span = 2; span <= size; span <<= 1)
-            for (int d = span >> 1; d; d >>= 1) {
-                for (int i = tid; i < size / 2; i += kThreads) {
-                    const int a0 = 2 * i - (i & (d - 1)), a1 = a0 + d;
-                    const u64 v0 = S.list[a0], v1 = S.list[a1];
-                    if ((v0 > v1) == ((a0 & span) == 0)) {
-                        S.list[a0] = v1;
-                        S.list[a1] = v0;
-                    }
-                }
-                __syncthreads();
-            }
-        // mass before each of a thread's two tokens
-        u64 key[2], mass[2], before[2];
-        int bin[2];
-        double w[2];
-        for (int e = 0; e < 2; e++) {
-            const int i = 2 * tid + e;
-            key[e] = i < static_cast<int>(n) ? S.list[i] : ~u64{0};
-            mass[e] = 0;
-            bin[e] = -1;
-            w[e] = 0;
-            if (i < static_cast<int>(n)) {
-                const double y = sc.y(order_value(static_cast<uint32_t>(key[e] >> 32)));
-                w[e] = weight(y);
-                mass[e] = whole(w[e]);
-                bin[e] = bin_of(y);
-            }
-        }
-        uint32_t unused;
-        block_scan(S, mass[0] + mass[1], 0, before[0], unused);
-        before[1] = before[0] + mass[0];
-        for (int e = 0; e < 2; e++) {
-            const int i = 2 * tid + e;
-            if (bin[e] < 0) continue;
-            const int prev = i == 0 ? -1 : e ? bin[0] : bin_of(sc.y(order_value(static_cast<uint32_t>(S.list[i - 1] >> 32))));
-            if (prev != bin[e]) {
-                S.base[bin[e]] = S.H[bin[e]] - before[e];
-                S.cbase[bin[e]] = S.C[bin[e]] - i;
-            }
-        }
-        __syncthreads();
-        uint32_t rank[2];
-        for (int e = 0; e < 2; e++)
-            if (bin[e] >= 0) {
-                before[e] += S.base[bin[e]];
-                rank[e] = S.cbase[bin[e]] + 2 * tid + e;
-            }
-        if (by_k) {
-            for (int e = 0; e < 2; e++)
-                if (bin[e] >= 0 && rank[e] == k - 1) S.mass[0] = before[e] + mass[e];
-            __syncthreads();
-            kept = S.mass[0];
-        }
-        if (by_p) {
-            const u64 t = p_target(kept);
-            for (int e = 0; e < 2; e++)
-                if (bin[e] >= 0 && before[e] < t && t <= before[e] + mass[e]) S.mass[1] = before[e] + mass[e];
-            __syncthreads();
-            kept = S.mass[1];
-        }
-        if (by_m) {
-            if (tid == 0) S.mass[2] = S.H[q0] > kOne ? S.H[q0] : kOne;
-            __syncthreads();
-            const double wl = static_cast<double>(least) * static_cast<double>(kOne);
-            for (int e = 0; e < 2; e++)
-                if (bin[e] >= q0 && bin[e] <= q1 && w[e] >= wl) atomicMax(&S.mass[2], before[e] + mass[e]);
-            __syncthreads();
-            if (mp > 1.0f) kept = kOne;
-            else if (S.mass[2] < kept) kept = S.mass[2];
-        }
-        const u64 t = u_target(kept);
-        for (int e = 0; e < 2; e++)
-            if (bin[e] >= 0 && before[e] < t && t <= before[e] + mass[e]) S.drawn = key[e];
-        __syncthreads();
-    } else {
-        // too many tokens in those bins (long runs of equal logits): passes over the row
-        if (by_k) kept = search_row(S, x, V, sc, b1, true, static_cast<u64>(k), false);
-        if (by_p) {
-            const u64 t = p_target(kept);
-            __syncthreads();
-            const int b = find_mass(S, t, 1);
-            kept = search_row(S, x, V, sc, b, false, t, false);
-        }
-        if (by_m) {
-            const double wl = static_cast<double>(least) * static_cast<double>(kOne);
-            u64 m = 0;
-            for (int i = tid; i < V; i += kThreads) {
-                const double y = sc.y(value(x, i));
-                if (!(y > kDeepest)) continue;
-                const double w = weight(y);
-                if (w >= wl) m += whole(w);
-            }
-            if (tid == 0) S.mass[2] = 0;
-            __syncthreads();
-            if (m) atomicAdd(&S.mass[2], m);
-            __syncthreads();
-            if (mp > 1.0f) kept = kOne;
-            else if (S.mass[2] < kept) kept = S.mass[2];
-        }
-        const u64 t = u_target(kept);
-        __syncthreads();
-        const int b = find_mass(S, t, 1);
-        search_row(S, x, V, sc, b, false, t, true);
-        __syncthreads();
+    const bool by_k = r.by_k && r.k < static_cast<int64_t>(S.C[kBins]);
+    if (tid < kBins / 32) K.take[tid] = 0;
+    if (tid < 4) {
+        K.from[tid] = INFINITY;
+        K.to[tid] = -INFINITY;
     }
     if (tid == 0) {
-        const u64 d = S.drawn;
-        a.token[row] = static_cast<int32_t>(d & 0xFFFFFFFFu);
-        if (a.prob)
-            a.prob[row] = static_cast<float>(weight(sc.y(order_value(static_cast<uint32_t>(d >> 32)))) / static_cast<double>(kept));
+        K.Z = Z;
+        K.by_k = by_k;
+        S.n = 0;
+    }
+    __syncthreads();
+    u64 lo = Z, hi = Z;  // bounds of the mass kept
+    auto mark = [&](int w, int f, int g) {
+        for (int b = f + tid; b <= g; b += NT) atomicOr(&K.take[b >> 5], 1u << (b & 31));
+        if (tid == 0) {
+            K.from[w] = below_bin(sc, g);
+            const float t = f ? below_bin(sc, f - 1) : INFINITY;
+            K.to[w] = f ? t + fabsf(t) * 0x1p-20f + 3 * FLT_MIN : INFINITY;
+        }
+    };
+    if (by_k) {
+        for (int b = tid; b < kBins; b += NT)
+            if (S.C[b] < r.k && r.k <= S.C[b + 1]) S.found[0] = b;
+        __syncthreads();
+        const int b1 = S.found[0];
+        lo = S.H[b1] < 1 ? 1 : S.H[b1];
+        hi = S.H[b1 + 1];
+        mark(0, b1, b1);
+        if (tid == 0) {
+            K.b1 = b1;
+            K.c1 = S.C[b1];
+        }
+    }
+    if (r.by_p) {
+        const int f = find_mass(S, r.p_target(lo), 1), g = find_mass(S, r.p_target(hi), 2);
+        lo = S.H[f] < 1 ? 1 : S.H[f];
+        hi = S.H[g + 1] < hi ? S.H[g + 1] : hi;
+        mark(1, f, g);
+    }
+    if (r.by_m) {
+        const int c = bin_of(log2(static_cast<double>(r.least)));
+        const int q0 = c > 0 ? c - 1 : 0, q1 = c + 1 < kBins - 1 ? c + 1 : kBins - 1;
+        if (S.H[q0] < lo) lo = S.H[q0] < 1 ? 1 : S.H[q0];
+        hi = S.H[q1 + 1] < hi ? S.H[q1 + 1] : hi;
+        mark(2, q0, q1);
+        if (tid == 0) {
+            K.q0 = q0;
+            K.q1 = q1;
+        }
+    }
+    __syncthreads();
+    const int f = find_mass(S, r.u_target(lo), 1), g = find_mass(S, r.u_target(hi), 2);
+    mark(3, f, g);
+    __syncthreads();
+}
+
+// The tokens of the marked bins among i0 .. i1-1 go to the list (counted in S.n, which may pass kList).
+// Most are outside by their logits alone: that is tested without branches, for the draw's range
+// alone, or top-p's too, or all.
+template <int NT, class T>
+__device__ void gather_marked(Shared<NT>& S, const T* x, int i0, int i1, const Row& r, const Scale& sc)
+{
+    const Marks& K = S.marks;
+    auto check = [&](float l, int i) {
+        const double y = sc.y(l);
+        if (!(y > kDeepest)) return;
+        const int b = bin_of(y);
+        if ((K.take[b >> 5] >> (b & 31)) & 1u) append(S, l, i);
+    };
+    const float f0 = K.from[0], f1 = K.from[1], f2 = K.from[2], f3 = K.from[3];
+    const float t0 = K.to[0], t1 = K.to[1], t2 = K.to[2], t3 = K.to[3];
+    if (K.by_k || r.by_m)
+        each_if<NT, 32>(
+            x, i0, i1,
+            [&](float l) { return ((l >= f0) & (l <= t0)) | ((l >= f1) & (l <= t1)) | ((l >= f2) & (l <= t2)) | ((l >= f3) & (l <= t3)); },
+            check);
+    else if (r.by_p)
+        each_if<NT, 32>(x, i0, i1, [&](float l) { return ((l >= f1) & (l <= t1)) | ((l >= f3) & (l <= t3)); }, check);
+    else
+        each_if<NT, 32>(x, i0, i1, [&](float l) { return (l >= f3) & (l <= t3); }, check);
+    __syncthreads();
+}
+
+// Answer from the marked bins: from their n tokens in the list, or, where more than fit (long runs of
+// equal logits), by passes over the row. H holds sums, C too if top-k cuts and n > kList. Leaves the
+// token in S.drawn and returns the mass kept.
+template <int NT, class T>
+__device__ u64 from_marked(Shared<NT>& S, const T* x, int V, const Row& r, const Scale& sc, int n)
+{
+    const int tid = threadIdx.x;
+    const Marks& K = S.marks;
+    const bool by_k = K.by_k;
+    __syncthreads();
+    if (n <= kList) {
+        sort_list(S, n);
+        const u64 before_m = r.by_m ? S.H[K.q0] : 0;  // mass before min-p's bins
+        const int before_b1 = sum_list(S, n, sc, true, by_k ? K.b1 : -2);
+        if (tid < 64) {
+            u64 kept = by_k ? S.upto[r.k - 1 - K.c1 + before_b1] : K.Z;
+            if (r.by_p) {
+                const u64 t = r.p_target(kept);
+                kept = S.upto[first_that(n, [&](int i) { return S.upto[i] >= t; })];
+            }
+            if (r.by_m) {
+                u64 m = kOne;  // the first token is never left out
+                if (!r.only_first) {
+                    const u64 w = r.least_mass();
+                    const int i = first_that(n, [&](int j) { return mass_of(sc, S.list[j]) < w; });
+                    m = i > 0 && bin_of(sc.y(key_value(S.list[i - 1]))) >= K.q0 ? S.upto[i - 1] : before_m;
+                    m = m > kOne ? m : kOne;
+                }
+                kept = m < kept ? m : kept;
+            }
+            const u64 t = r.u_target(kept);
+            const int i = first_that(n, [&](int j) { return S.upto[j] >= t; });
+            if (tid == 0) {
+                S.drawn = S.list[i];
+                S.kept = kept;
+            }
+        }
+        __syncthreads();
+        return S.kept;
+    }
+    u64 kept = K.Z;
+    if (by_k) kept = search_row(S, x, V, sc, K.b1, true, static_cast<u64>(r.k), false);
+    if (r.by_p) {
+        const u64 t = r.p_target(kept);
+        __syncthreads();
+        const int b = find_mass(S, t, 1);
+        kept = search_row(S, x, V, sc, b, false, t, false);
+    }
+    if (r.by_m) {
+        const u64 w = r.least_mass();
+        u64 m = 0;
+        each_mass<NT>(x, V, sc, [&](float, double y) {
+            const u64 v = whole(weight(y));
+            if (v >= w) m += v;
+        });
+        if (tid == 0) S.mass[2] = 0;
+        __syncthreads();
+        if (m) atomicAdd(&S.mass[2], m);
+        __syncthreads();
+        m = r.only_first || S.mass[2] < kOne ? kOne : S.mass[2];
+        kept = m < kept ? m : kept;
+    }
+    const u64 t = r.u_target(kept);
+    __syncthreads();
+    const int b = find_mass(S, t, 1);
+    search_row(S, x, V, sc, b, false, t, true);
+    __syncthreads();
+    return kept;
+}
+
+// All of that for a row in one workgroup; the histogram of masses may be there already.
+template <int NT, class T>
+__device__ u64 from_row(Shared<NT>& S, const T* x, int V, const Row& r, const Scale& sc, bool have_masses)
+{
+    if (!have_masses) count_row(S, x, V, sc);
+    __syncthreads();
+    mark_bins(S, r, sc);
+    gather_marked(S, x, 0, V, r, sc);
+    return from_marked(S, x, V, r, sc, static_cast<int>(S.n));
+}
+
+// Whether the list that tau gives has every token with mass.
+__device__ __forceinline__ bool holds_all(const Scale& sc, float tau) { return tau == -INFINITY || sc.top == INFINITY; }
+
+// Whether the masses of all tokens are needed beside the list that tau gives.
+__device__ __forceinline__ bool needs_masses(const Row& r, const Scale& sc, float tau)
+{
+    if (r.by_k || holds_all(sc, tau)) return false;  // the list answers, or from_row counts for itself
+    if (r.by_p || !r.by_m) return true;
+    return !(sc.y(tau) < log2(static_cast<double>(r.least)) - 0.01);  // min-p alone, and its cut lies in the list
+}
+
+__device__ __forceinline__ void write_row(const SampleArgs& a, int64_t row, int32_t token, float prob)
+{
+    if (threadIdx.x == 0) {
+        a.token[row] = token;
+        if (a.prob) a.prob[row] = prob;
+    }
+}
+
+__device__ __forceinline__ void write_drawn(const SampleArgs& a, int64_t row, const Scale& sc, u64 drawn, u64 kept)
+{
+    write_row(a, row, static_cast<int32_t>(drawn & 0xFFFFFFFFu),
+              static_cast<float>(weight(sc.y(key_value(drawn))) / static_cast<double>(kept)));
+}
+
+constexpr uint32_t kMostParts = 32;
+struct RowSpace {
+    uint32_t n;        // tokens in the list
+    uint32_t arrived;  // workgroups done with the row
+    u64 Z;             // mass of the row
+    float top[kMostParts], tau[kMostParts];
+    u64 list[kList];
+};
+static_assert(sizeof(RowSpace) % 16 == 0, "layout");
+
+// Data that workgroups of one launch hand to another: written through to, and read from, where all of
+// the device sees it.
+__device__ __forceinline__ void put(u64* p, u64 v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+template <class U>
+__device__ __forceinline__ U got(const U* p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The part's list (S.n tokens, of which kList at most are there) is added to the row's; true for the
+// workgroup that is the row's last. put() writes through to memory, and every wave's writes are there
+// before its barrier; so the last workgroup finds all of them (a fence would write back the whole
+// L2: with 512 workgroups that took 10 us).
+template <int NT>
+__device__ bool hand_over(Shared<NT>& S, u64* list, uint32_t* n, uint32_t* arrived, uint32_t parts)
+{
+    const uint32_t mine = S.n < kList ? S.n : kList;
+    if (threadIdx.x == 0) S.found[0] = static_cast<int>(atomicAdd(n, S.n));
+    __syncthreads();
+    const uint32_t at = static_cast<uint32_t>(S.found[0]);
+    for (uint32_t i = threadIdx.x; i < mine; i += NT)
+        if (at + i < kList) put(&list[at + i], S.list[i]);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) S.found[1] = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == parts;
+    __syncthreads();
+    return S.found[1];
+}
+
+__device__ __forceinline__ int part_begin(int V, uint32_t part, uint32_t parts)
+{
+    return static_cast<int>(static_cast<int64_t>(V) * part / parts);
+}
+
+// One workgroup per row.
+template <class T, int NT>
+__global__ void __launch_bounds__(NT) sample_rows(SampleArgs a)
+{
+    __shared__ Shared<NT> S;
+    const int64_t row = blockIdx.x;
+    const T* const x = static_cast<const T*>(a.x) + row * a.ld;
+    const Row r(a, row);
+    float mine = -INFINITY;
+    each_if<NT, 32>(
+        x, 0, a.V,
+        [&](float l) {
+            mine = fmaxf(mine, l);
+            return false;
+        },
+        [](float, int) {});
+    const float top = block_max(S, mine);
+    if (top == -INFINITY) return write_row(a, row, -1, 0.0f);  // nothing to draw
+    const Scale sc = r.scale(top);
+    const bool listed = !r.by_k || r.short_k();
+    float tau = 0.f;
+    bool masses = false;
+    if (listed) {
+        // room for the tokens that share the last one's bin
+        tau = reached_by(S, mine, sc, r.by_k ? (r.k > 32 ? static_cast<uint32_t>(r.k) : 32u) : kAim);
+        masses = needs_masses(r, sc, tau);
+        clear_bins(S, masses, false);
+        if (threadIdx.x == 0) S.n = 0;
+        __syncthreads();
+        gather(S, x, 0, a.V, sc, tau, masses);
+        __syncthreads();
+    }
+    const int n = listed ? static_cast<int>(S.n) : 0;
+    if (masses) bins_to_sums(S, true, false);
+    u64 kept = 0;
+    if (listed && n <= kList) kept = from_list(S, r, sc, n, holds_all(sc, tau), masses ? S.H[kBins] : 0);
+    if (!kept) kept = from_row(S, x, a.V, r, sc, masses);
+    write_drawn(a, row, sc, S.drawn, kept);
+}
+
+// Few rows: `parts` workgroups per row, in two launches. The first finds each part's largest logit and
+// a logit that enough of its threads reach. The second gathers the beginning of the order and, where
+// it is needed, the histogram; the workgroup that is last to do so for a row answers, from the list or
+// with passes over the whole row. (A third launch that shared those passes out over the CUs took
+// longer than it saved: 64 rows of 50257 50 us with it and 44 without, 256 of 131072 100 and 88.)
+template <class T, int NT>
+__global__ void __launch_bounds__(NT) sample_tops(SampleArgs a, RowSpace* space, uint32_t parts)
+{
+    __shared__ Shared<NT> S;
+    const int64_t row = blockIdx.x / parts;
+    const uint32_t part = blockIdx.x % parts;
+    const T* const x = static_cast<const T*>(a.x) + row * a.ld;
+    const Row r(a, row);
+    float mine = -INFINITY;
+    each_if<NT, 32>(
+        x, part_begin(a.V, part, parts), part_begin(a.V, part + 1, parts),
+        [&](float l) {
+            mine = fmaxf(mine, l);
+            return false;
+        },
+        [](float, int) {});
+    const float top = block_max(S, mine);
+    float tau = -INFINITY;
+    const uint32_t aim = r.short_k() ? static_cast<uint32_t>(r.k) + 32 : kAim;
+    if (top > -INFINITY) tau = reached_by(S, mine, r.scale(top), (aim + parts - 1) / parts);
+    if (threadIdx.x == 0) {
+        space[row].top[part] = top;
+        space[row].tau[part] = tau == -INFINITY ? INFINITY : tau;  // a part with few tokens has no say
+        if (part == 0) {
+            RowSpace& R = space[row];
+            R.n = R.arrived = 0;
+            R.Z = 0;
+        }
+    }
+}
+
+template <class T, int NT>
+__global__ void __launch_bounds__(NT) sample_parts(SampleArgs a, RowSpace* space, u64* hist, uint32_t parts)
+{
+    __shared__ Shared<NT> S;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t row = blockIdx.x / parts;
+    const uint32_t part = blockIdx.x % parts;
+    const T* const x = static_cast<const T*>(a.x) + row * a.ld;
+    RowSpace& R = space[row];
+    float top = lane < static_cast<int>(parts) ? R.top[lane] : -INFINITY;
+    float tau = lane < static_cast<int>(parts) ? R.tau[lane] : INFINITY;
+    const Row r(a, row);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        top = fmaxf(top, __shfl_xor(top, d));
+        tau = fminf(tau, __shfl_xor(tau, d));
+    }
+    if (top == -INFINITY) {  // nothing to draw
+        if (part == 0) write_row(a, row, -1, 0.0f);
+        return;
+    }
+    const Scale sc = r.scale(top);
+    // no part had enough tokens: all of them (tau is +inf also where the largest logits are)
+    if (tau == INFINITY && top < INFINITY) tau = -INFINITY;
+    const bool listed = !r.by_k || r.short_k();
+    const bool masses = needs_masses(r, sc, tau);
+    clear_bins(S, masses, false);
+    if (tid == 0) S.n = 0;
+    __syncthreads();
+    if (listed) gather(S, x, part_begin(a.V, part, parts), part_begin(a.V, part + 1, parts), sc, tau, masses);
+    __syncthreads();
+    // this part's tokens, mass and histogram go to the row's space
+    u64* const H = hist + row * parts * kBins;
+    if (masses) {
+        u64 m = 0;
+        for (int b = tid; b < kBins; b += NT) {
+            put(&H[part * kBins + b], S.H[b]);
+            m += S.H[b];
+        }
+        m = wave_sums(m);
+        if (lane == 63) atomicAdd(&R.Z, m);
+    }
+    if (!hand_over(S, R.list, &R.n, &R.arrived, parts)) return;
+    const uint32_t n = got(&R.n);
+    const u64 Z = got(&R.Z);
+    u64 kept = 0;
+    if (listed && n <= kList) {
+        for (uint32_t i = tid; i < n; i += NT) S.list[i] = got(&R.list[i]);
+        __syncthreads();
+        kept = from_list(S, r, sc, static_cast<int>(n), holds_all(sc, tau), Z);
+    }
+    if (!kept) {
+        if (masses) {
+            __syncthreads();
+            for (int b = tid; b < kBins; b += NT) {
+                u64 m = 0;
+                for (uint32_t s = 0; s < parts; s += 8) {  // eight loads on the way at a time
+                    u64 v[8];
+#pragma unroll
+                    for (uint32_t e = 0; e < 8; e++) v[e] = got(&H[(s + e < parts ? s + e : s) * kBins + b]);
+#pragma unroll
+                    for (uint32_t e = 0; e < 8; e++) m += s + e < parts ? v[e] : 0;
+                }
+                S.H[b] = m;
+            }
+            bins_to_sums(S, true, false);
+        }
+        kept = from_row(S, x, a.V, r, sc, masses);
+    }
+    write_drawn(a, row, sc, S.drawn, kept);
+}
+
+// How a call is launched: workgroups per row and their threads. With few rows 512 threads pass their
+// barriers sooner (1 row of 131072: 15.7 us, 17.5 with 1024 threads); with more rows 1024 threads and
+// one workgroup for each of 256 CUs win (16 rows: 45 us, 54 with 512 threads and two; 64 rows of
+// 50257: 49 and 56 us). No part has less than 2048 logits.
+struct Launch {
+    uint32_t parts, threads;
+};
+
+Launch plan_launch(int64_t M, int64_t V)
+{
+    const bool few = M <= 8;
+    int64_t p = (few ? 512 : 256) / (M > 0 ? M : 1);
+    p = p < V / 2048 ? p : V / 2048;
+    return {static_cast<uint32_t>(p < 1 ? 1 : p > kMostParts ? kMostParts : p), few ? 512u : 1024u};
+}
+
+template <class T, int NT>
+void launch_rows(const SampleArgs& a, RowSpace* space, u64* hist, const Launch& l, hipStream_t s)
+{
+    const uint32_t M = static_cast<uint32_t>(a.M);
+    if (l.parts == 1) {
+        hipLaunchKernelGGL((sample_rows<T, NT>), dim3(M), dim3(NT), 0, s, a);
+    } else {
+        hipLaunchKernelGGL((sample_tops<T, NT>), dim3(M * l.parts), dim3(NT), 0, s, a, space, l.parts);
+        hipLaunchKernelGGL((sample_parts<T, NT>), dim3(M * l.parts), dim3(NT), 0, s, a, space, hist, l.parts);
     }
 }
 
@@ -520,9 +1114,9 @@ using namespace uw;
 
 size_t uw_sample_workspace(int64_t M, int64_t V)
 {
-    (void)M;
-    (void)V;
-    return 0;
+    if (M < 1 || V < 1 || V > UW_SAMPLE_MAX_V || M >= (1 << 24)) return 0;
+    const Launch l = plan_launch(M, V);
+    return l.parts == 1 ? 0 : static_cast<size_t>(M) * (sizeof(RowSpace) + l.parts * kBins * sizeof(u64));
 }
 
 uw_status uw_sample(const uw_sample_args* args, void* stream)
@@ -542,12 +1136,14 @@ uw_status uw_sample(const uw_sample_args* args, void* stream)
     a.min_p = args->d_min_p;
     a.token = args->d_token;
     a.prob = args->d_prob;
-    const dim3 grid(static_cast<uint32_t>(a.M));
     hipStream_t s = static_cast<hipStream_t>(stream);
+    const Launch l = plan_launch(a.M, a.V);
+    RowSpace* space = l.parts > 1 ? static_cast<RowSpace*>(args->d_ws) : nullptr;
+    u64* hist = reinterpret_cast<u64*>(space + a.M);
     if (args->type == UW_F32)
-        hipLaunchKernelGGL(sample_rows<float>, grid, dim3(kThreads), 0, s, a);
+        l.threads == 512 ? launch_rows<float, 512>(a, space, hist, l, s) : launch_rows<float, 1024>(a, space, hist, l, s);
     else
-        hipLaunchKernelGGL(sample_rows<uint16_t>, grid, dim3(kThreads), 0, s, a);
+        l.threads == 512 ? launch_rows<uint16_t, 512>(a, space, hist, l, s) : launch_rows<uint16_t, 1024>(a, space, hist, l, s);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? UW_OK : fail(UW_EHIP, "sample launch failed: %s", hipGetErrorString(e));
 }

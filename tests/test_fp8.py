@@ -96,7 +96,7 @@ def test_gemm_refusals():
 
 def test_sample_refusals():
     def f(**k):
-        d = dict(d_logits=P, d_u=P, d_token=P, M=4, V=1000, type=uw.F32, d_ws=P, ws_bytes=1 << 30, stream=0)
+        d = dict(d_logits=P, d_u=P, d_token=P, M=4, V=100000, type=uw.F32, d_ws=P, ws_bytes=1 << 30, stream=0)
         d.update(k)
         return _status(uw.sample, **d)
 
@@ -111,12 +111,12 @@ def test_sample_refusals():
     assert f(type=uw.BF16, d_logits=P + 1) == uw.EINVAL
     for name in ("d_temperature", "d_top_k", "d_top_p", "d_min_p", "d_prob"):
         assert f(**{name: P + 1}) == uw.EINVAL
-    assert f(ld=999) == uw.EINVAL
-    need = uw.sample_workspace(4, 1000)
-    if need:
-        assert f(d_ws=None) == uw.EINVAL
-        assert f(d_ws=P + 8) == uw.EINVAL
-        assert f(ws_bytes=need - 1) == uw.ENOSPACE
+    assert f(ld=99999) == uw.EINVAL
+    need = uw.sample_workspace(4, 100000)
+    assert need > 0
+    assert f(d_ws=None) == uw.EINVAL
+    assert f(d_ws=P + 8) == uw.EINVAL
+    assert f(ws_bytes=need - 1) == uw.ENOSPACE
     assert uw.lib.uw_sample(None, None) == uw.EINVAL
 
 
@@ -132,6 +132,11 @@ def test_workspace_sizes():
         assert uw.fp8_gemm_workspace(M, N, K) == 0
     for M, V in ((0, 100), (-1, 100), (4, 0), (4, (1 << 20) + 1), (1 << 24, 10)):
         assert uw.sample_workspace(M, V) == 0
+
+
+    assert uw.sample_workspace(1, 131072) > 0
+    assert uw.sample_workspace(2000, 131072) == 0  # one workgroup per row, which does all of it
+    assert uw.sample_workspace(1, 2000) == 0
 
 
 def test_types_follow_the_tensor():

@@ -1,10 +1,10 @@
 """uw_sample on the GPU against its definition, row by row on the host.
 
 The masses are whole multiples of 2^-43 of the largest token's, so the oracle's sums are exact
-integers too and tokens have to be equal. The oracle's exponential is NumPy's (about 2^-52 of the
-value): a mass may round to a neighbouring integer, which moves a border by 2^-43 of the
-row's mass or less; the random numbers are multiples of 2^-24, and no seed here puts one that near a
-border. Probabilities: one fp32 rounding, 2^-24, and the kept mass's 2^-30.
+integers too and tokens have to be equal. The kernel's exponential is within 2.2e-12 of the value
+and the oracle's is NumPy's, so borders between tokens may differ by 2^-38 of the row's mass; the
+random numbers are multiples of 2^-24, and no seed here puts one that near a border.
+Probabilities: one fp32 rounding, 2^-24, and the kept mass's 2^-30.
 """
 import math
 
