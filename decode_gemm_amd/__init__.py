@@ -410,28 +410,36 @@ def swiglu(d_g, d_u, d_h, n: int, stream=None) -> None:
     _check(lib.uw_swiglu(_ptr(d_g), _ptr(d_u), n, _ptr(d_h), _stream(stream)))
 
 
+_TYPES = {}  # torch dtype -> uw_type, filled on first use (torch is imported by callers that have tensors)
+
+
 def _type(t, given):
     """uw_type of a tensor's elements (bf16 also carried as 16-bit integers); a raw address needs it given."""
     if given is not None:
         return given
-    name = str(getattr(t, "dtype", ""))
-    if name == "torch.float32":
-        return F32
-    if name in ("torch.bfloat16", "torch.int16", "torch.uint16"):
-        return BF16
-    raise ValueError(f"type must be given for {name or 'a raw address'}: F32 or BF16")
+    dtype = getattr(t, "dtype", None)
+    if not _TYPES and dtype is not None:
+        import torch
+
+        _TYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.int16: BF16, torch.uint16: BF16})
+    try:
+        return _TYPES[dtype]
+    except (KeyError, TypeError):
+        raise ValueError(f"type must be given for {dtype or 'a raw address'}: F32 or BF16") from None
 
 
-def _launch(t, call, stream):
-    """call(stream) with the device of t current and, without a stream, that device's current one."""
+def _launch(t, stream, call, *args):
+    """call(*args, stream) with the device of tensor t current and, without a stream, that device's
+    current one. (One import and two lookups: at batch size 1 the host's share of a call is what counts.)"""
     if t is None or isinstance(t, int) or not t.is_cuda:
-        return _check(call(_stream(stream)))
+        return _check(call(*args, _stream(stream)))
     import torch
 
-    if t.device.index == torch.cuda.current_device():
-        return _check(call(_stream(stream)))
-    with torch.cuda.device(t.device):
-        return _check(call(_stream(stream)))
+    dev = t.get_device()
+    if dev == torch.cuda.current_device():
+        return _check(call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)))
+    with torch.cuda.device(dev):
+        return _check(call(*args, _stream(stream)))
 
 
 def fp8_quantize(d_x, d_q, d_s, M: int, K: int, block_rows: int = 1, x_type: int | None = None, ldx: int | None = None,
@@ -440,16 +448,15 @@ def fp8_quantize(d_x, d_q, d_s, M: int, K: int, block_rows: int = 1, x_type: int
     (block_rows 1, scales [ceil(K / 128)][lds]) or per 128 x 128 block (block_rows 128, scales
     [ceil(M / 128)][lds]). x_type follows a tensor's dtype unless given."""
     st = lds if lds is not None else M if block_rows == 1 else (K + 127) // 128
-    _launch(d_x, lambda s: lib.uw_fp8_quantize(_ptr(d_x), _type(d_x, x_type), M, K, K if ldx is None else ldx, block_rows,
-                                               _ptr(d_q), K if ldq is None else ldq, _ptr(d_s), st, s), stream)
+    _launch(d_x, stream, lib.uw_fp8_quantize, _ptr(d_x), _type(d_x, x_type), M, K, K if ldx is None else ldx, block_rows,
+            _ptr(d_q), K if ldq is None else ldq, _ptr(d_s), st)
 
 
 def fp8_swiglu(d_g, d_u, d_q, d_s, M: int, K: int, ldg: int | None = None, ldu: int | None = None,
                ldq: int | None = None, lds: int | None = None, stream=None) -> None:
     """uw_fp8_swiglu: silu(g) * u of fp32 g and u, as e4m3 codes and row scales."""
-    _launch(d_g, lambda s: lib.uw_fp8_swiglu(_ptr(d_g), K if ldg is None else ldg, _ptr(d_u), K if ldu is None else ldu, M,
-                                             K, _ptr(d_q), K if ldq is None else ldq, _ptr(d_s),
-                                             M if lds is None else lds, s), stream)
+    _launch(d_g, stream, lib.uw_fp8_swiglu, _ptr(d_g), K if ldg is None else ldg, _ptr(d_u), K if ldu is None else ldu, M, K,
+            _ptr(d_q), K if ldq is None else ldq, _ptr(d_s), M if lds is None else lds)
 
 
 def fp8_gemm_workspace(M: int, N: int, K: int) -> int:
@@ -464,7 +471,7 @@ def fp8_gemm(d_x, d_sx, d_w, d_sw, d_y, M: int, N: int, K: int, ldx: int | None 
     a = Fp8GemmArgs(M, N, K, _ptr(d_x), K if ldx is None else ldx, _ptr(d_sx), M if ldsx is None else ldsx, _ptr(d_w),
                     K if ldw is None else ldw, _ptr(d_sw), (K + 127) // 128 if ldsw is None else ldsw, _ptr(d_y),
                     N if ldy is None else ldy, _type(d_y, y_type), _ptr(d_ws), ws_bytes)
-    _launch(d_x, lambda s: lib.uw_fp8_gemm(ctypes.byref(a), s), stream)
+    _launch(d_x, stream, lib.uw_fp8_gemm, ctypes.byref(a))
 
 
 def sample_workspace(M: int, V: int) -> int:
@@ -478,7 +485,7 @@ def sample(d_logits, d_u, d_token, M: int, V: int, ld: int | None = None, type: 
     receives the drawn token's probability. d_ws: sample_workspace(M, V) bytes."""
     a = SampleArgs(M, V, _ptr(d_logits), V if ld is None else ld, _type(d_logits, type), _ptr(d_u), _ptr(d_temperature),
                    _ptr(d_top_k), _ptr(d_top_p), _ptr(d_min_p), _ptr(d_token), _ptr(d_prob), _ptr(d_ws), ws_bytes)
-    _launch(d_logits, lambda s: lib.uw_sample(ctypes.byref(a), s), stream)
+    _launch(d_logits, stream, lib.uw_sample, ctypes.byref(a))
 
 
 def proj(h: Header, d_blob, pipeline: int = PIPE_DIRECT, d_direct=None, variant: int = -1, split_k: int = 0) -> Proj:

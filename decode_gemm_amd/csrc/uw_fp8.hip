@@ -139,49 +139,45 @@ struct LoadSwiglu {
     }
 };
 
-// Row groups: 16 lanes hold one group's 128 values, eight each, so the group's maximum is a
-// DPP row reduction and nothing passes through LDS. A workgroup of 256 threads covers ROWS rows
-// x (16 / ROWS) x STEP groups.
-template <class Load, int ROWS, int STEP>
+// Row groups: 16 lanes hold one group's 128 values, eight each, so the group's maximum is a DPP row
+// reduction and nothing passes through LDS. A workgroup of 256 threads covers ROWS rows x 16 / ROWS
+// groups, one group per 16 lanes: more per thread is slower at every size (2 groups 4%, 4 groups 15%
+// at 4096 x 14336), as the registers then hold fewer waves. HBM-bound: the activation of 4096 x 14336
+// moves 530 MB in 92.5 us (5.7 TB/s, part of it from the cache behind the L2), bf16 to codes at
+// 4096 x 4096 51 MB in 12.5 us.
+template <class Load, int ROWS>
 __global__ void __launch_bounds__(256) quantize_rows(QuantArgs a)
 {
     constexpr int GC = 16 / ROWS;  // groups side by side
     const uint32_t tk = blockIdx.x % a.tiles_k, tm = blockIdx.x / a.tiles_k;
     const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
-    const int64_t m = static_cast<int64_t>(tm) * ROWS + sub % ROWS;
-    if (m >= a.M) return;
-    const int64_t g0 = static_cast<int64_t>(tk) * (GC * STEP) + sub / ROWS;
-    const int64_t G = (a.K + kG - 1) / kG;
-    float v[STEP][8];
-#pragma unroll
-    for (int t = 0; t < STEP; t++) {
-        const int64_t g = g0 + t * GC;
-        if (g < G) Load::row(a, m, g * kG + 8 * l, v[t]);
-    }
-#pragma unroll
-    for (int t = 0; t < STEP; t++) {
-        const int64_t g = g0 + t * GC;
-        if (g >= G) break;
-        const float s = scale_of(row_max16(amax8(v[t])));
-        store8(a.q + m * a.ldq, g * kG + 8 * l, a.K, codes8(v[t], s, 1.0f / s));
-        if (l == 0) a.s[g * a.lds + m] = s;
-    }
+    const int64_t m = static_cast<int64_t>(tm) * ROWS + sub % ROWS, g = static_cast<int64_t>(tk) * GC + sub / ROWS;
+    if (m >= a.M || g * kG >= a.K) return;
+    float v[8];
+    Load::row(a, m, g * kG + 8 * l, v);
+    const float s = scale_of(row_max16(amax8(v)));
+    store8(a.q + m * a.ldq, g * kG + 8 * l, a.K, codes8(v, s, 1.0f / s));
+    if (l == 0) a.s[g * a.lds + m] = s;
 }
 
-// 128 x 128 blocks, one workgroup each: the block stays in registers (64 values per thread)
-// between the maximum, joined over the waves in LDS, and the codes.
+// 128 x 128 blocks, one workgroup each: the block stays in registers between the maximum, joined over
+// the waves in LDS, and the codes. HBM-bound: bf16 to codes at 14336 x 4096 moves 176 MB in 38.1 us (4.6
+// TB/s; 38.8 with 512 threads, 43.2 with 256). A matrix of few blocks waits for one block's loads and
+// barrier: 1000 x 1000 4.1 us, 4.6 with 512 threads, 7.0 with 256.
+constexpr int kBlockThreads = 1024;
 template <class T>
-__global__ void __launch_bounds__(256) quantize_blocks(QuantArgs a)
+__global__ void __launch_bounds__(kBlockThreads) quantize_blocks(QuantArgs a)
 {
-    __shared__ float part[4];
+    constexpr int STEP = kBlockThreads / 16, N = kG / STEP;  // rows per step, steps
+    __shared__ float part[kBlockThreads / 64];
     const uint32_t g = blockIdx.x % a.tiles_k;
     const int64_t nb = blockIdx.x / a.tiles_k;
     const int64_t m0 = nb * kG + (threadIdx.x >> 4), k = static_cast<int64_t>(g) * kG + 8 * (threadIdx.x & 15);
-    float v[8][8];
+    float v[N][8];
     float top = 0.f;
 #pragma unroll
-    for (int t = 0; t < 8; t++) {
-        const int64_t m = m0 + 16 * t;
+    for (int t = 0; t < N; t++) {
+        const int64_t m = m0 + STEP * t;
         if (m < a.M) {
             LoadX<T>::row(a, m, k, v[t]);
         } else {
@@ -190,17 +186,19 @@ __global__ void __launch_bounds__(256) quantize_blocks(QuantArgs a)
         }
     }
 #pragma unroll
-    for (int t = 0; t < 8; t++) top = fmaxf(top, amax8(v[t]));
+    for (int t = 0; t < N; t++) top = fmaxf(top, amax8(v[t]));
     top = row_max16(top);
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
     __syncthreads();
-    const float s = scale_of(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
+#pragma unroll
+    for (int w = 0; w < kBlockThreads / 64; w++) top = fmaxf(top, part[w]);
+    const float s = scale_of(top);
     const float r = 1.0f / s;
 #pragma unroll
-    for (int t = 0; t < 8; t++) {
-        const int64_t m = m0 + 16 * t;
+    for (int t = 0; t < N; t++) {
+        const int64_t m = m0 + STEP * t;
         if (m < a.M) store8(a.q + m * a.ldq, k, a.K, codes8(v[t], s, r));
     }
     if (threadIdx.x == 0) a.s[nb * a.lds + g] = s;
@@ -217,21 +215,24 @@ uw_status check_quant(int64_t M, int64_t K, const void* q, int64_t ldq, const vo
     return UW_OK;
 }
 
+template <class Load, int ROWS>
+uw_status launch_rows(QuantArgs& a, hipStream_t s)
+{
+    const int64_t G = (a.K + kG - 1) / kG, wide = 16 / ROWS;
+    const int64_t tk = (G + wide - 1) / wide, tm = (a.M + ROWS - 1) / ROWS;
+    if (tk > INT32_MAX || tm > INT32_MAX / tk) return fail(UW_EUNSUPPORTED, "too many groups for one launch");
+    a.tiles_k = static_cast<uint32_t>(tk);
+    hipLaunchKernelGGL((quantize_rows<Load, ROWS>), dim3(static_cast<uint32_t>(tk * tm)), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? UW_OK : fail(UW_EHIP, "quantize launch failed: %s", hipGetErrorString(e));
+}
+
+// Eight rows side by side fill 32 bytes of a scale row per store; one or two rows take groups instead
+// (1 x 4096: 2.3 us, 2.7 with eight).
 template <class Load>
 uw_status launch_rows(QuantArgs& a, hipStream_t s)
 {
-    const int64_t G = (a.K + kG - 1) / kG;
-    const int64_t rows = a.M < 16 ? 1 : 16, wide = a.M < 16 ? 16 : 4;
-    const int64_t tk = (G + wide - 1) / wide, tm = (a.M + rows - 1) / rows;
-    if (tk > INT32_MAX || tm > INT32_MAX / tk) return fail(UW_EUNSUPPORTED, "too many groups for one launch");
-    a.tiles_k = static_cast<uint32_t>(tk);
-    const dim3 grid(static_cast<uint32_t>(tk * tm));
-    if (a.M < 16)
-        hipLaunchKernelGGL((quantize_rows<Load, 1, 1>), grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((quantize_rows<Load, 16, 4>), grid, dim3(256), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? UW_OK : fail(UW_EHIP, "quantize launch failed: %s", hipGetErrorString(e));
+    return a.M <= 2 ? launch_rows<Load, 1>(a, s) : launch_rows<Load, 8>(a, s);
 }
 
 template <class T>
@@ -240,7 +241,7 @@ uw_status launch_blocks(QuantArgs& a, hipStream_t s)
     const int64_t G = (a.K + kG - 1) / kG, nb = (a.M + kG - 1) / kG;
     if (G > INT32_MAX || nb > INT32_MAX / G) return fail(UW_EUNSUPPORTED, "too many blocks for one launch");
     a.tiles_k = static_cast<uint32_t>(G);
-    hipLaunchKernelGGL(quantize_blocks<T>, dim3(static_cast<uint32_t>(G * nb)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(quantize_blocks<T>, dim3(static_cast<uint32_t>(G * nb)), dim3(kBlockThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? UW_OK : fail(UW_EHIP, "quantize launch failed: %s", hipGetErrorString(e));
 }
