@@ -430,16 +430,20 @@ def _type(t, given):
 
 def _launch(t, stream, call, *args):
     """call(*args, stream) with the device of tensor t current and, without a stream, that device's
-    current one. (One import and two lookups: at batch size 1 the host's share of a call is what counts.)"""
+    current one. (Two lookups in torch's C layer: at batch size 1 the host's share of a call counts.)"""
     if t is None or isinstance(t, int) or not t.is_cuda:
         return _check(call(*args, _stream(stream)))
-    import torch
-
+    global _torch
+    if _torch is None:
+        import torch as _torch
     dev = t.get_device()
-    if dev == torch.cuda.current_device():
-        return _check(call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)))
-    with torch.cuda.device(dev):
+    if dev == _torch._C._cuda_getDevice():
+        return _check(call(*args, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)))
+    with _torch.cuda.device(dev):
         return _check(call(*args, _stream(stream)))
+
+
+_torch = None
 
 
 def fp8_quantize(d_x, d_q, d_s, M: int, K: int, block_rows: int = 1, x_type: int | None = None, ldx: int | None = None,

@@ -567,8 +567,15 @@ __global__ void __launch_bounds__(256) fp8_join(F8Args a, const float* part, uin
     const int64_t q = a.N4 / 4, e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (e >= a.M * q) return;
     const float* p = part + 4 * e;
-    floatx4 s = *reinterpret_cast<const floatx4*>(p);
-    for (uint32_t z = 1; z < slices; z++) s += *reinterpret_cast<const floatx4*>(p + z * a.M * a.N4);
+    floatx4 s = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t z = 0; z < slices; z += 4) {  // four loads on the way at a time
+        floatx4 v[4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; i++) v[i] = *reinterpret_cast<const floatx4*>(p + (z + i < slices ? z + i : z) * a.M * a.N4);
+#pragma unroll
+        for (uint32_t i = 0; i < 4; i++)
+            if (z + i < slices) s += v[i];
+    }
     store4(a, e / q, 4 * (e % q), s);
 }
 
@@ -597,9 +604,9 @@ hipError_t launch_tile(const F8Args& a, hipStream_t s)
 // ------------------------------------------------------------------------- choice
 // Kernel shapes and what a launch of them takes. The time of a launch is modelled as
 //   fixed + max(rounds of workgroups, bytes from HBM, bytes into the CUs) [+ joining K slices]
-// with constants fitted to 25000 launches measured on MI355X (M 1 to 4096, 12 pairs of N and K from
-// 128 to 28672, K slices 1 to 16): over those sizes the shape that the model picks takes 3% longer
-// than the fastest one on average, and 18% longer for one size in twenty.
+// with constants fitted to 24000 launches measured on MI355X (M 1 to 4096, 12 pairs of N and K from
+// 128 to 28672, K slices 1 to 16): over those sizes the shape that the model picks takes 2.2% longer
+// than the fastest one on average, and 11% longer for one size in twenty.
 struct Shape {
     int bn, bm, waves_k;  // rows of W and X per workgroup; waves that share a group out (tiles: 1)
     int per_cu;           // workgroups that fit a CU
@@ -610,25 +617,25 @@ struct Shape {
     float hbm, cu;     // TB/s from memory, into the CUs
     float again;       // share of W read again for every further tile along M
 };
-constexpr float kJoinFixed = 2.7f, kJoinRate = 2.7f;  // us; TB/s of partial sums written and read
+constexpr float kJoinFixed = 2.2f, kJoinRate = 2.7f;  // us; TB/s of partial sums written and read
 
 const Shape kSums[] = {
-    {256, 256, 1, 1, launch_tile<256, 256, 2, 4, 2, 2, false>, 7.21f, 1.79f, 1.37f, 1.37f, 4.2f, 9.12f, 0.85f},
-    {256, 128, 1, 1, launch_tile<256, 128, 4, 2, 3, 2, false>, 4.52f, 2.57f, 0.828f, 0.828f, 5.3f, 11.2f, 0.66f},
-    {128, 128, 1, 2, launch_tile<128, 128, 4, 2, 2, 1, false>, 4.45f, 0.586f, 0.578f, 1.03f, 5.74f, 14.0f, 0.76f},
-    {128, 64, 1, 2, launch_tile<128, 64, 4, 1, 3, 1, false>, 3.56f, 2.4f, 0.493f, 0.74f, 5.75f, 16.5f, 0.51f},
-    {128, 32, 1, 2, launch_tile<128, 32, 4, 1, 3, 1, false>, 3.42f, 2.04f, 0.342f, 0.515f, 6.08f, 20.1f, 0.31f},
-    {16, 16, 8, 8, launch_skinny<1, 1, 1, 8>, 3.18f, 0.47f, 0.523f, 3.75f, 5.5f, 10.1f, 0.3f},
-    {16, 16, 16, 2, launch_skinny<1, 1, 1, 16>, 3.07f, 0.48f, 1.04f, 2.4f, 5.8f, 9.6f, 0.3f},
-    {32, 16, 16, 2, launch_skinny<1, 2, 1, 16>, 3.1f, 0.335f, 1.83f, 4.82f, 5.5f, 10.0f, 0.5f},
-    {32, 32, 16, 1, launch_skinny<2, 2, 1, 16>, 2.88f, 0.316f, 2.85f, 2.85f, 3.6f, 8.25f, 0.3f},
-    {32, 64, 8, 2, launch_skinny<4, 2, 1, 8>, 3.5f, 0.295f, 1.9f, 3.66f, 3.2f, 9.5f, 0.3f},
+    {256, 256, 1, 1, launch_tile<256, 256, 2, 4, 2, 2, false>, 6.31f, 1.75f, 1.41f, 1.41f, 4.06f, 8.94f, 0.81f},
+    {256, 128, 1, 1, launch_tile<256, 128, 4, 2, 3, 2, false>, 6.37f, 0.0f, 0.858f, 0.858f, 5.78f, 11.7f, 0.64f},
+    {128, 128, 1, 2, launch_tile<128, 128, 4, 2, 2, 1, false>, 4.32f, 0.517f, 0.599f, 1.04f, 5.71f, 14.1f, 0.75f},
+    {128, 64, 1, 2, launch_tile<128, 64, 4, 2, 3, 1, false>, 4.01f, 1.03f, 0.373f, 0.738f, 6.31f, 16.9f, 0.46f},
+    {128, 32, 1, 2, launch_tile<128, 32, 4, 1, 3, 1, false>, 3.43f, 1.61f, 0.354f, 0.527f, 6.15f, 19.2f, 0.32f},
+    {16, 16, 8, 8, launch_skinny<1, 1, 1, 8>, 3.12f, 0.37f, 0.578f, 4.15f, 6.0f, 10.0f, 0.31f},
+    {16, 16, 16, 2, launch_skinny<1, 1, 1, 16>, 2.96f, 0.49f, 1.13f, 2.32f, 4.64f, 9.28f, 0.3f},
+    {32, 16, 16, 2, launch_skinny<1, 2, 1, 16>, 3.0f, 0.32f, 1.96f, 4.83f, 5.04f, 8.66f, 0.3f},
+    {32, 32, 16, 1, launch_skinny<2, 2, 1, 16>, 2.89f, 0.285f, 2.96f, 2.96f, 3.57f, 8.19f, 0.31f},
+    {32, 64, 8, 2, launch_skinny<4, 2, 1, 8>, 3.5f, 0.25f, 2.0f, 3.85f, 3.13f, 9.34f, 0.3f},
 };
 const Shape kExact[] = {
-    {256, 128, 1, 1, launch_tile<256, 128, 4, 2, 3, 1, true>, 4.23f, 1.2f, 1.65f, 1.65f, 3.59f, 6.56f, 0.7f},
-    {128, 128, 1, 2, launch_tile<128, 128, 4, 2, 2, 1, true>, 3.8f, 1.23f, 0.998f, 2.07f, 3.25f, 7.29f, 0.78f},
-    {128, 64, 1, 2, launch_tile<128, 64, 4, 1, 3, 1, true>, 4.16f, 0.757f, 0.726f, 1.15f, 4.73f, 10.5f, 0.55f},
-    {128, 32, 1, 2, launch_tile<128, 32, 4, 1, 3, 1, true>, 3.37f, 1.73f, 0.495f, 0.729f, 5.36f, 13.8f, 0.42f},
+    {256, 128, 1, 1, launch_tile<256, 128, 4, 2, 3, 1, true>, 4.36f, 0.927f, 1.69f, 1.69f, 3.46f, 6.54f, 0.65f},
+    {128, 128, 1, 2, launch_tile<128, 128, 4, 2, 2, 1, true>, 3.73f, 1.09f, 1.02f, 2.13f, 3.19f, 7.19f, 0.78f},
+    {128, 64, 1, 2, launch_tile<128, 64, 4, 2, 3, 1, true>, 4.0f, 0.63f, 0.674f, 1.21f, 4.79f, 10.3f, 0.62f},
+    {128, 32, 1, 2, launch_tile<128, 32, 4, 1, 3, 1, true>, 3.38f, 1.37f, 0.511f, 0.752f, 5.41f, 13.5f, 0.43f},
     kSums[5], kSums[6], kSums[7], kSums[8], kSums[9],
 };
 constexpr uint32_t kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16};
