@@ -205,13 +205,12 @@ __global__ void __launch_bounds__(kBlockThreads) quantize_blocks(QuantArgs a)
 }
 
 // Checks that the two quantizers share.
-uw_status check_quant(int64_t M, int64_t K, const void* q, int64_t ldq, const void* s, int64_t lds, int64_t lds_least)
+uw_status check_quant(int64_t K, const void* q, int64_t ldq, const void* s, int64_t lds, int64_t lds_least)
 {
     if (!q || !s) return fail(UW_EINVAL, "NULL device pointer");
     if (!aligned(q, 16) || !aligned(s, 4)) return fail(UW_EINVAL, "codes must be 16-byte aligned, scales 4-byte aligned");
     if (ldq < K || ldq % 16) return fail(UW_EINVAL, "ldq must be >= K and a multiple of 16");
     if (lds < lds_least) return fail(UW_EINVAL, "lds too small");
-    (void)M;
     return UW_OK;
 }
 
@@ -220,7 +219,7 @@ uw_status launch_rows(QuantArgs& a, hipStream_t s)
 {
     const int64_t G = (a.K + kG - 1) / kG, wide = 16 / ROWS;
     const int64_t tk = (G + wide - 1) / wide, tm = (a.M + ROWS - 1) / ROWS;
-    if (tk > INT32_MAX || tm > INT32_MAX / tk) return fail(UW_EUNSUPPORTED, "too many groups for one launch");
+    if (tk > kThreadsMost / 256 || tm > kThreadsMost / 256 / tk) return fail(UW_EUNSUPPORTED, "too many groups for one launch");
     a.tiles_k = static_cast<uint32_t>(tk);
     hipLaunchKernelGGL((quantize_rows<Load, ROWS>), dim3(static_cast<uint32_t>(tk * tm)), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
@@ -239,7 +238,7 @@ template <class T>
 uw_status launch_blocks(QuantArgs& a, hipStream_t s)
 {
     const int64_t G = (a.K + kG - 1) / kG, nb = (a.M + kG - 1) / kG;
-    if (G > INT32_MAX || nb > INT32_MAX / G) return fail(UW_EUNSUPPORTED, "too many blocks for one launch");
+    if (G > kThreadsMost / kBlockThreads || nb > kThreadsMost / kBlockThreads / G) return fail(UW_EUNSUPPORTED, "too many blocks for one launch");
     a.tiles_k = static_cast<uint32_t>(G);
     hipLaunchKernelGGL(quantize_blocks<T>, dim3(static_cast<uint32_t>(G * nb)), dim3(kBlockThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
@@ -262,7 +261,7 @@ uw_status uw_fp8_quantize(const void* d_x, int32_t x_type, int64_t M, int64_t K,
     if (M == 0) return UW_OK;
     if (!d_x || !aligned(d_x, 16)) return fail(UW_EINVAL, "d_x must be 16-byte aligned and not NULL");
     if (ldx < K || ldx % (x_type == UW_BF16 ? 8 : 4)) return fail(UW_EINVAL, "ldx must be >= K and keep rows 16-byte aligned");
-    uw_status st = check_quant(M, K, d_q, ldq, d_s, lds, block_rows == 1 ? M : (K + kG - 1) / kG);
+    uw_status st = check_quant(K, d_q, ldq, d_s, lds, block_rows == 1 ? M : (K + kG - 1) / kG);
     if (st != UW_OK) return st;
     QuantArgs a{};
     a.x = d_x;
@@ -286,7 +285,7 @@ uw_status uw_fp8_swiglu(const float* d_g, int64_t ldg, const float* d_u, int64_t
     if (M == 0) return UW_OK;
     if (!d_g || !d_u || !aligned(d_g, 16) || !aligned(d_u, 16)) return fail(UW_EINVAL, "d_g and d_u must be 16-byte aligned and not NULL");
     if (ldg < K || ldu < K || ldg % 4 || ldu % 4) return fail(UW_EINVAL, "ldg and ldu must be >= K and multiples of 4");
-    uw_status st = check_quant(M, K, d_q, ldq, d_s, lds, M);
+    uw_status st = check_quant(K, d_q, ldq, d_s, lds, M);
     if (st != UW_OK) return st;
     QuantArgs a{};
     a.x = d_g;

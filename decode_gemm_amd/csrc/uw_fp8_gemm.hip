@@ -671,7 +671,8 @@ double model_us(const Shape& h, int64_t M, int64_t N, int64_t K, bool bf16, uint
     return h.fixed + (run > hbm ? (run > cu ? run : cu) : (hbm > cu ? hbm : cu)) + join;
 }
 
-// The fastest shape and slice count by the model, for a workspace of ws bytes.
+// The fastest shape and slice count by the model, for a workspace of ws bytes; no shape where none can
+// be launched.
 Plan make_plan(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws, uint32_t cus)
 {
     const Shape* shapes = bf16 ? kSums : kExact;
@@ -680,6 +681,8 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, bool bf16, size_t ws, uint32_t c
     Plan best = {nullptr, 1, 0};
     for (int i = 0; i < n; i++) {
         if (shapes[i].waves_k == 1 && K < kG) continue;  // the tiles read whole groups of K
+        const int64_t groups = ((M + shapes[i].bm - 1) / shapes[i].bm) * ((N + shapes[i].bn - 1) / shapes[i].bn);
+        if (groups * (shapes[i].waves_k > 1 ? 64 * shapes[i].waves_k : 512) > kThreadsMost) continue;
         for (uint32_t s : kSlices) {
             if (s > 1 && (G < 2 * s || part_bytes(M, N, s) > ws)) break;
             const double us = model_us(shapes[i], M, N, K, bf16, s, cus);
@@ -765,7 +768,7 @@ size_t uw_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K)
     size_t most = 0;
     for (int bf16 = 0; bf16 < 2; bf16++) {
         const Plan p = plan_for(M, N, K, bf16, kWorkspaceMost);
-        const size_t need = part_bytes(M, N, p.slices);
+        const size_t need = p.shape ? part_bytes(M, N, p.slices) : 0;
         most = need > most ? need : most;
     }
     return most;
@@ -794,6 +797,7 @@ uw_status uw_fp8_gemm(const uw_fp8_gemm_args* p, void* stream)
     a.slices = 1;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Plan plan = plan_for(a.M, a.N, a.K, a.bf16, p->d_ws ? (p->ws_bytes < kWorkspaceMost ? p->ws_bytes : kWorkspaceMost) : 0);
+    if (!plan.shape) return fail(UW_EUNSUPPORTED, "M x N too large for one launch");
     const hipError_t e = run_plan(a, plan, p->d_ws, s);
     return e == hipSuccess ? UW_OK : fail(UW_EHIP, "GEMM launch failed: %s", hipGetErrorString(e));
 }

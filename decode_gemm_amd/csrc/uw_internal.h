@@ -70,6 +70,7 @@ struct ZeroTarget {
 uw_status launch_gate_up_gemm(const uw_gemm_args* gate, const uw_gemm_args* up, uint16_t* d_h, int64_t ldh,
                               void* stream, const ZeroTarget* clear = nullptr);
 int default_variant(int64_t N, int64_t K, int64_t M, int32_t src);
+constexpr int64_t kThreadsMost = UINT32_MAX;  // threads along one axis of a launch
 uint32_t cu_count();  // compute units of the current device
 uint32_t stream_cu_count(void* stream);  // compute units a hipStream_t may use (its CU mask)
 uint64_t direct_plane_bytes(const uw_header* h);

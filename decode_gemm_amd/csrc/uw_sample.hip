@@ -1084,13 +1084,15 @@ void launch_rows(const SampleArgs& a, RowSpace* space, u64* hist, const Launch& 
     }
 }
 
+constexpr int64_t kRowsMost = kThreadsMost / 1024;  // a workgroup per row
+
 uw_status check_sample(const uw_sample_args* p)
 {
     if (!p) return fail(UW_EINVAL, "NULL argument");
     if (p->M < 0 || p->V < 1) return fail(UW_ESHAPE, "bad shape %lld x %lld", (long long)p->M, (long long)p->V);
     if (p->type != UW_F32 && p->type != UW_BF16) return fail(UW_EINVAL, "bad type %d", p->type);
     if (p->V > UW_SAMPLE_MAX_V) return fail(UW_EUNSUPPORTED, "V > %d", UW_SAMPLE_MAX_V);
-    if (p->M >= (1 << 24)) return fail(UW_EUNSUPPORTED, "M >= 2^24");
+    if (p->M > kRowsMost) return fail(UW_EUNSUPPORTED, "M >= 2^22");
     if (p->M == 0) return UW_OK;
     if (!p->d_logits || !p->d_u || !p->d_token) return fail(UW_EINVAL, "NULL device pointer");
     if (p->ld < p->V) return fail(UW_EINVAL, "ld must be >= V");
@@ -1114,7 +1116,7 @@ using namespace uw;
 
 size_t uw_sample_workspace(int64_t M, int64_t V)
 {
-    if (M < 1 || V < 1 || V > UW_SAMPLE_MAX_V || M >= (1 << 24)) return 0;
+    if (M < 1 || V < 1 || V > UW_SAMPLE_MAX_V || M > kRowsMost) return 0;
     const Launch l = plan_launch(M, V);
     return l.parts == 1 ? 0 : static_cast<size_t>(M) * (sizeof(RowSpace) + l.parts * kBins * sizeof(u64));
 }

@@ -22,6 +22,7 @@
  *   - Weights W are [N][K] row-major bf16 bit patterns (PyTorch Linear layout: N = out
  *     features, K = in features). K must be a multiple of 64. X is [M][K] bf16 row-major
  *     with leading dimension ldx; Y = X * W^T is [M][N] fp32 with leading dimension ldy.
+ *     (The 8-bit path and the sampler name their own types and sizes.)
  *   - "d_" pointers are device (HBM) pointers; all others are host pointers.
  *   - The caller owns every buffer. The library never allocates or frees device memory
  *     and keeps no pointer after a call returns. Every kernel is the library's own; it
@@ -32,7 +33,8 @@
  *   - No C++ exception crosses this boundary. On failure a status code is returned and
  *     a thread-local message is available from uw_last_error().
  *   - All functions are re-entrant. The only global state is a once-per-process flag per
- *     kernel recording that its LDS-size attribute has been raised.
+ *     kernel recording that its LDS-size attribute has been raised, and per thread the launch
+ *     shapes last chosen for sizes of the 8-bit GEMM.
  */
 #ifndef UW_H
 #define UW_H
@@ -489,7 +491,8 @@ uw_status uw_swiglu(const float* d_g, const float* d_u, int64_t n, uint16_t* d_h
  *
  * Errors: UW_ESHAPE (M < 0, K < 1), UW_EINVAL (NULL or misaligned pointers: 16 bytes, scales
  * 4; a leading dimension too small or not the multiple named; an unknown type or block_rows),
- * UW_EUNSUPPORTED (more than 2^31 - 1 workgroups), UW_EHIP. M = 0 is a no-op.
+ * UW_EUNSUPPORTED (more than about 2^35 values), UW_EHIP. M = 0 is a no-op. d_x, d_q and d_s
+ * must not overlap.
  */
 #define UW_FP8_GROUP 128
 typedef enum { UW_F32 = 0, UW_BF16 = 1 } uw_type;
@@ -518,7 +521,9 @@ uw_status uw_fp8_swiglu(const float* d_g, int64_t ldg, const float* d_u, int64_t
  * that uw_fp8_gemm refuses and where no slices are cut.
  * Errors: UW_ESHAPE (M < 0, N or K < 1), UW_EINVAL (NULL or misaligned pointers: codes and Y
  * 16 bytes, scales 4; leading dimensions; an unknown type), UW_EUNSUPPORTED (a leading
- * dimension of 2^24 bytes or more, M, N or K of 2^31 or more, M N of 2^39 or more), UW_EHIP. M = 0 is a no-op.
+ * dimension of 2^24 bytes or more, M, N or K of 2^31 or more, an M x N of more tiles than one
+ * launch takes: 2^23 of 64 x 32 are taken), UW_EHIP. M = 0 is a no-op. Y and d_ws must not
+ * overlap each other or an operand.
  */
 typedef struct {
     int64_t M, N, K;
@@ -563,7 +568,7 @@ size_t uw_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K);
  * done; calls that overlap need one each. NULL where that is 0.
  * Errors: UW_ESHAPE (M < 0, V < 1), UW_EINVAL (NULL d_logits, d_u or d_token, misaligned
  * pointers: that of their elements, ld < V, an unknown type), UW_ENOSPACE (workspace), UW_EUNSUPPORTED
- * (V > UW_SAMPLE_MAX_V, M >= 2^24), UW_EHIP. M = 0 is a no-op.
+ * (V > UW_SAMPLE_MAX_V, M >= 2^22), UW_EHIP. M = 0 is a no-op.
  */
 #define UW_SAMPLE_MAX_V (1 << 20)
 typedef struct {

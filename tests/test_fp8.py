@@ -42,6 +42,10 @@ def test_quantize_refusals():
     assert _quantize(K=100, ldx=104) == uw.EINVAL     # ldq defaults to K, no multiple of 16
     assert _quantize(lds=3) == uw.EINVAL              # rows: lds >= M
     assert _quantize(block_rows=128, lds=1) == uw.EINVAL  # blocks: lds >= ceil(K / 128)
+    # more threads than a launch has along an axis (2^32)
+    assert _quantize(M=1 << 28, K=2048) == uw.EUNSUPPORTED
+    assert _quantize(M=2, K=1 << 36) == uw.EUNSUPPORTED
+    assert _quantize(M=1 << 30, K=128, block_rows=128) == uw.EUNSUPPORTED
 
 
 def test_swiglu_refusals():
@@ -62,6 +66,7 @@ def test_swiglu_refusals():
     assert f(ldu=257) == uw.EINVAL
     assert f(ldq=250) == uw.EINVAL
     assert f(lds=2) == uw.EINVAL
+    assert f(M=1 << 28, K=2048) == uw.EUNSUPPORTED
 
 
 def test_gemm_refusals():
@@ -75,6 +80,9 @@ def test_gemm_refusals():
     assert f(K=0) == uw.ESHAPE
     assert f(M=1 << 31, ldsx=1 << 31) == uw.EUNSUPPORTED
     assert f(N=1 << 31) == uw.EUNSUPPORTED
+    assert f(M=1 << 30, N=16, K=16, ldsx=1 << 30) == uw.EUNSUPPORTED  # more threads than a launch has
+    assert f(M=1 << 30, N=1 << 12, ldsx=1 << 30) == uw.EUNSUPPORTED
+    assert uw.fp8_gemm_workspace(1 << 30, 16, 16) == 0
     assert f(y_type=5) == uw.EINVAL
     for name in ("d_x", "d_sx", "d_w", "d_sw", "d_y"):
         assert f(**{name: None}) == uw.EINVAL
@@ -105,6 +113,7 @@ def test_sample_refusals():
     assert f(type=3) == uw.EINVAL
     assert f(V=(1 << 20) + 1) == uw.EUNSUPPORTED
     assert f(M=1 << 24) == uw.EUNSUPPORTED
+    assert f(M=1 << 22) == uw.EUNSUPPORTED
     for name in ("d_logits", "d_u", "d_token"):
         assert f(**{name: None}) == uw.EINVAL
         assert f(**{name: P + 2}) == uw.EINVAL

@@ -315,3 +315,77 @@ def test_mlp_from_a_blob_end_to_end():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(captured, step()[3])
+
+
+def _far(x, ld, dtype):
+    """x in the first columns of rows ld elements apart; the rest is never written."""
+    torch = torch_cuda()
+    t = torch.empty(x.shape[0], ld, dtype=dtype, device="cuda")
+    t[:, : x.shape[1]] = x
+    return t
+
+
+def test_rows_past_32_bits():
+    """Strides that put the last rows more than 2^32 bytes behind the first, in every operand."""
+    uw, torch = _uw(), torch_cuda()
+    K = 200
+    rng = np.random.default_rng(21)
+    for M, N in ((300, 290), (20, 290)):
+        ld0, (qx, sx, x), (qw, sw, w) = _operands(uw, rng, M, N, K)
+        ld = (1 << 24) - 16
+        fx, fw = _far(qx, ld, torch.uint8), _far(qw, ld, torch.uint8)
+        for dt in (torch.float32, torch.bfloat16):
+            ldy = (1 << 24) + 5
+            y = torch.empty(M, ldy, dtype=dt, device="cuda")
+            uw.fp8_gemm(fx, sx, fw, sw, y, M, N, K, ldx=ld, ldw=ld, ldy=ldy)
+            _check(y[:, :N].double().cpu().numpy(), x, w, K, dt == torch.bfloat16, f"M={M} {dt}")
+        del fx, fw, y
+    M = 300
+    for dt, ld in ((torch.float32, (1 << 22) + 4), (torch.bfloat16, (1 << 23) + 8)):
+        v = torch.from_numpy(_values(rng, M, K)).cuda().to(dt)
+        fv = _far(v, ld, dt)
+        for rows in (1, 128):
+            q, qf = torch.zeros(M, 208, dtype=torch.uint8, device="cuda"), torch.empty(M, 1 << 24, dtype=torch.uint8, device="cuda")
+            s, sf = torch.zeros(2, 3, M, device="cuda")
+            lds = M if rows == 1 else 2
+            uw.fp8_quantize(v, q, s, M, K, block_rows=rows, ldq=208, lds=lds)
+            uw.fp8_quantize(fv, qf, sf, M, K, block_rows=rows, ldx=ld, ldq=1 << 24, lds=lds)
+            assert torch.equal(q[:, :K], qf[:, :K]) and torch.equal(s, sf)
+        del fv, qf
+    g, u = (torch.from_numpy(_values(rng, M, K)).cuda() for _ in range(2))
+    fg = _far(torch.cat([g, u], 1), (1 << 22) + 4, torch.float32)
+    s, sf = torch.zeros(2, 2, M, device="cuda")
+    uw.fp8_swiglu(g, u, q, s, M, K, ldq=208)
+    q2 = torch.zeros_like(q)
+    uw.fp8_swiglu(fg, fg[:, K:], q2, sf, M, K, ldg=(1 << 22) + 4, ldu=(1 << 22) + 4, ldq=208)
+    assert torch.equal(q[:, :K], q2[:, :K]) and torch.equal(s, sf)
+
+
+def test_gemm_slices_in_two_graphs_at_once():
+    """K in slices through a workspace, two captured products with one each, replayed on two streams."""
+    uw, torch = _uw(), torch_cuda()
+    M, N, K = 40, 512, 8192
+    need = uw.fp8_gemm_workspace(M, N, K)
+    assert need > 0
+    runs = []
+    for i in range(2):
+        ld, (qx, sx, x), (qw, sw, w) = _operands(uw, np.random.default_rng(30 + i), M, N, K)
+        y, ws = torch.zeros(M, N, device="cuda"), torch.empty(need, dtype=torch.uint8, device="cuda")
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        call = lambda: uw.fp8_gemm(qx, sx, qw, sw, y, M, N, K, ldx=ld, ldw=ld, d_ws=ws, ws_bytes=need)
+        call()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            call()
+        runs.append((graph, stream, y, x, w, (qx, sx, qw, sw, ws)))
+    for _ in range(4):
+        for graph, stream, y, *_ in runs:
+            y.zero_()
+        torch.cuda.synchronize()
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+                graph.replay()
+        torch.cuda.synchronize()
+        for graph, stream, y, x, w, _ in runs:
+            _check(y.double().cpu().numpy(), x, w, K, False, "replay")

@@ -294,3 +294,19 @@ def test_two_streams_at_once():
         ref = [_draw(l, float(v))[0] for l, v in zip(x.double().cpu().numpy(), u)]
         assert (t.cpu().numpy() == np.array(ref)).all()
     log("  20 calls on each of two streams")
+
+
+@pytest.mark.parametrize("M,V,ld", [(300, 1001, (1 << 23) + 1), (100, 9001, (1 << 25) + 3)])
+def test_rows_past_32_bits(M, V, ld):
+    uw, torch = _uw(), torch_cuda()
+    x = np.random.default_rng(V).standard_normal((M, V)).astype(np.float32) * 3
+    near = torch.from_numpy(x).cuda().bfloat16()
+    far = torch.empty(M, ld, dtype=torch.bfloat16, device="cuda")
+    far[:, :V] = near
+    u = torch.rand(M, device="cuda")
+    tok = torch.zeros(2, M, dtype=torch.int32, device="cuda")
+    need = uw.sample_workspace(M, V)
+    ws = torch.zeros(max(16, need), dtype=torch.uint8, device="cuda")
+    uw.sample(far, u, tok[0], M, V, ld=ld, d_ws=ws, ws_bytes=need)
+    ref = [_draw(l, float(v))[0] for l, v in zip(near.double().cpu().numpy(), u)]
+    assert (tok[0].cpu().numpy() == np.array(ref)).all()
