@@ -389,3 +389,46 @@ def test_gemm_slices_in_two_graphs_at_once():
         torch.cuda.synchronize()
         for graph, stream, y, x, w, _ in runs:
             _check(y.double().cpu().numpy(), x, w, K, False, "replay")
+
+
+# Sizes that each of the kernel's shapes takes, in one slice and in several where it is cut at all
+LARGER = [(40, 6000, 144), (100, 4100, 144), (24, 4100, 4112), (1030, 1003, 144), (2050, 1003, 144), (130, 515, 9000),
+          (40, 4100, 4112), (520, 8010, 400), (2050, 257, 4112), (2050, 257, 9000), (2050, 6000, 272), (2050, 1003, 4112),
+          (2050, 1003, 9000), (2050, 6000, 1296), (700, 6000, 9000)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", LARGER)
+def test_gemm_larger(M, N, K, out):
+    """The tolerance of the small ones, with operands and reference made on the GPU."""
+    uw, torch = _uw(), torch_cuda()
+    gen = torch.Generator("cuda").manual_seed(M + N + K)
+    rand = lambda *n: torch.randn(*n, device="cuda", generator=gen)
+    G, ld = -(-K // 128), _up(K, 16)
+    qx, qw = (torch.full((n, ld), 0x7F, dtype=torch.uint8, device="cuda") for n in (M, N))
+    sx, sw = torch.exp(rand(G, M)), torch.exp(rand(-(-N // 128), G))
+    spread = lambda s, n: s.repeat_interleave(128, 1)[:n, :K].double()
+    vals = []
+    for q, s in ((qx, sx.t()), (qw, sw.repeat_interleave(128, 0)[:N])):
+        c = (rand(q.shape[0], K) * 40).to(torch.float8_e4m3fn)
+        q[:, :K] = c.view(torch.uint8)
+        vals.append(c.double() * spread(s, q.shape[0]))
+    x, w = vals
+    bf16 = out == "bf16"
+    ref, mag = x @ w.t(), x.abs() @ w.abs().t()
+    tol = (128 + G + 2) * 2.0**-23 * mag
+    if bf16:
+        for k in range(0, K, 128):
+            a, b = x[:, k:k + 128].abs(), w[:, k:k + 128].abs()
+            tol += 2.0**-10 * torch.minimum(a.amax(1)[:, None] * b.amax(1)[None, :], a @ b.t())
+        tol += 2.0**-8 * (ref.abs() + tol)
+    need = uw.fp8_gemm_workspace(M, N, K)
+    for ws in (None, torch.full((max(need, 16),), 0xFF, dtype=torch.uint8, device="cuda")):
+        ldy = N + 1 if ws is None else _up(N, 4)
+        y = torch.full((M + 1, ldy), -77.0, dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")
+        uw.fp8_gemm(qx, sx, qw, sw, y, M, N, K, ldx=ld, ldw=ld, ldy=ldy, d_ws=ws, ws_bytes=need if ws is not None else 0)
+        err = (y[:M, :N].double() - ref).abs()
+        worst = float((err / tol).max())
+        log(f"  M={M} N={N} K={K} {out} workspace {0 if ws is None else need}: worst {worst:.3g} of the tolerance")
+        assert worst <= 1.0
+        assert bool((y[:M, N:] == -77).all()) and bool((y[M] == -77).all()), "outside the matrix"
