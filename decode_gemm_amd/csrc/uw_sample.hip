@@ -26,13 +26,17 @@ namespace uw {
 
 namespace {
 
+// A token's mass is worked out in several places and has to come out the same in all of them.
+#pragma clang fp contract(off)
+
 typedef unsigned long long u64;
 
 constexpr int kBins = 2048;            // 46 per unit of y: the 44 units that have mass fill 2025 of them
-constexpr double kBinsPerUnit = 46.0;
+constexpr double kBinsPerUnit = 46.0, kUnitPerBin = 1.0 / 46.0;
 constexpr double kDeepest = -44.0;     // 2^43 * 2^y rounds to 0 from here down
 constexpr int kList = 2048;            // tokens that are sorted in LDS
 constexpr uint32_t kAim = 256;         // tokens that the gathered beginning of the order has at least
+constexpr uint32_t kCrowd = 255;       // most tokens of a sort bin that are compared with one another
 constexpr int kShort = 512;            // largest k that it is made to hold
 constexpr u64 kOne = u64{1} << 43;     // mass of the row's largest token
 
@@ -57,22 +61,43 @@ __device__ __forceinline__ float value(const uint16_t* x, int i) { return __uint
 constexpr double kRound = 6755399441055744.0;  // 3 * 2^51
 __device__ __forceinline__ int low_bits(double v) { return static_cast<int>(__double_as_longlong(v)); }
 
-// 2^43 * 2^y for y in (-44, 0]: 2^f for the fraction f in [-0.5, 0.5] as 1 + f q(f), q the polynomial
-// that meets (2^f - 1) / f at the eight Chebyshev points; within 2.2e-12 of the value, and exact at 0.
-// The whole part goes into the exponent bits.
+// Bin b holds the y nearest to -b / 46; the sum's low bits are b.
+__device__ __forceinline__ double bin_sum(double y) { return __builtin_fma(y, -kBinsPerUnit, kRound); }
+__device__ __forceinline__ int bin_of(double y) { return low_bits(bin_sum(y)); }
+
+// 2^43 * 2^y for y in (-44.5, 0] is that of the bin's middle times 2^d for the distance d from it; both
+// are polynomials 1 + f q(f) where q meets (2^f - 1) / f at Chebyshev points (nine for |f| <= 1/2 with
+// the whole part in the exponent bits, four for |d| <= 1/92), together within 7e-14 of the value, and
+// exact at 0. Over whole rows the middles come from a table in LDS: the pass of 256 rows of 131072
+// takes 28 us, 32 with one long polynomial for all of y.
+__device__ __forceinline__ double middle(int b)
+{
+    const double y = static_cast<double>(b) * -kUnitPerBin, t = y + kRound, f = y - (t - kRound);
+    double q = 0x1.b63880a30ec15p-24;
+    q = __builtin_fma(q, f, 0x1.63d136366db24p-20);
+    q = __builtin_fma(q, f, 0x1.ffcb9515a8013p-17);
+    q = __builtin_fma(q, f, 0x1.4308ac85aa947p-13);
+    q = __builtin_fma(q, f, 0x1.5d87fe86fe88ep-10);
+    q = __builtin_fma(q, f, 0x1.3b2ab7181b755p-7);
+    q = __builtin_fma(q, f, 0x1.c6b08d7047e52p-5);
+    q = __builtin_fma(q, f, 0x1.ebfbdff823cedp-3);
+    q = __builtin_fma(q, f, 0x1.62e42fefa39efp-1);
+    const u64 v = static_cast<u64>(__double_as_longlong(__builtin_fma(q, f, 1.0)));
+    return __longlong_as_double(static_cast<long long>(v + (static_cast<u64>(static_cast<uint32_t>(low_bits(t) + 43) << 20) << 32)));
+}
+__device__ __forceinline__ double weight(double y, double bin, double mid)
+{
+    const double d = __builtin_fma(bin - kRound, kUnitPerBin, y);
+    double q = 0x1.3b2ade109790cp-7;
+    q = __builtin_fma(q, d, 0x1.c6b0e2036dc06p-5);
+    q = __builtin_fma(q, d, 0x1.ebfbdff829fbbp-3);
+    q = __builtin_fma(q, d, 0x1.62e42fef9e814p-1);
+    return mid * __builtin_fma(q, d, 1.0);
+}
 __device__ __forceinline__ double weight(double y)
 {
-    const double t = y + kRound, f = y - (t - kRound);
-    double q = 0x1.63b2d796f0517p-20;
-    q = __builtin_fma(q, f, 0x1.00c0e4e1521c8p-16);
-    q = __builtin_fma(q, f, 0x1.4308c7183d81ep-13);
-    q = __builtin_fma(q, f, 0x1.5d877598350f3p-10);
-    q = __builtin_fma(q, f, 0x1.3b2ab70ad2565p-7);
-    q = __builtin_fma(q, f, 0x1.c6b08da70cce3p-5);
-    q = __builtin_fma(q, f, 0x1.ebfbdff82a734p-3);
-    q = __builtin_fma(q, f, 0x1.62e42fef9cc69p-1);
-    const u64 b = static_cast<u64>(__double_as_longlong(__builtin_fma(q, f, 1.0)));
-    return __longlong_as_double(static_cast<long long>(b + (static_cast<u64>(static_cast<uint32_t>(low_bits(t) + 43) << 20) << 32)));
+    const double bin = bin_sum(y);
+    return weight(y, bin, middle(low_bits(bin)));
 }
 
 // Nearest whole number (ties to even) of 0 <= w < 2^52.
@@ -93,9 +118,6 @@ struct Scale {
     }
 };
 
-// Bin b holds the y nearest to -b / 46.
-__device__ __forceinline__ int bin_of(double y) { return low_bits(__builtin_fma(y, -kBinsPerUnit, kRound)); }
-
 // Sort key of (logit, index): ascending keys are the order. -0 and +0 are equal logits.
 __device__ __forceinline__ uint32_t order_bits(float l)
 {
@@ -112,16 +134,20 @@ struct Marks {
     u64 Z;              // mass of the row
     float from[4], to[4];
     uint32_t by_k;      // top-k cuts, in bin b1, before which are c1 tokens
+    uint32_t by_p, by_m;  // top-p and min-p may decide
     int32_t b1;
     uint32_t c1;
-    int32_t q0, q1;     // bins of min-p's cut
-    uint32_t take[kBins / 32];  // all these bins
+    int32_t q0;         // first bin of min-p's cut
+    uint32_t take[kBins / 32];    // all these bins
+    uint32_t before[kBins / 32];  // how many of them lie before each word's
+    uint32_t bins;                // and in all
 };
 
 template <int NT>
 struct Shared {
     u64 H[kBins + 1];       // mass before each bin (while the histogram is made: mass of it)
     uint32_t C[kBins + 1];  // tokens before each bin, likewise
+    double mid[kBins];      // middle(b), filled where a row's masses are summed
     u64 list[kList];
     u64 upto[kList];        // mass up to and with each token of the sorted list; scratch before that
     Marks marks;
@@ -198,13 +224,13 @@ __device__ __forceinline__ float block_max(Shared<NT>& S, float v)
     return v;
 }
 
-// test(logit) for the logits i0 .. i1-1 of a row, once each, by all threads of the workgroup, and
-// act(logit, index) for those that pass (NaN must not). 16-byte loads between the 16-byte boundaries, up
-// to 32 logits on the way per thread. What passes is noted in a mask and acted on in one loop: most
-// code here runs once or twice per launch, and fetching instructions costs more than running them, so
-// only the test is unrolled.
+// test(logit) for the logits i0 .. i1-1 of a row, once each, by all threads of the workgroup (NaN must
+// not pass). 16-byte loads between the 16-byte boundaries, up to 32 logits on the way per thread. What
+// passes is noted in a mask, which goes to act(mask, index) by the batch, index(b) being the place of
+// the logit that bit b stands for: most code here runs once or twice per launch, and fetching
+// instructions costs more than running them, so only the test is unrolled.
 template <int NT, int L, class T, class Test, class Act>
-__device__ __forceinline__ void each_if(const T* x, int i0, int i1, Test test, Act act)
+__device__ __forceinline__ void each_batch(const T* x, int i0, int i1, Test test, Act act)
 {
     constexpr int W = 16 / sizeof(T), U = L / W;  // logits per load, loads on the way
     static_assert(L <= 32 && U >= 1, "mask");
@@ -233,25 +259,63 @@ __device__ __forceinline__ void each_if(const T* x, int i0, int i1, Test test, A
                     passed |= test(__uint_as_float(q[e][c] & 0xFFFF0000u)) ? 1u << (W * e + 2 * c + 1) : 0u;
                 }
             }
-        while (passed) {
-            const int b = __ffs(passed) - 1;
-            passed &= passed - 1;
-            const int at = a + W * (j0 + b / W * NT + tid) + b % W;
-            act(value(x, at), at);
-        }
+        act(passed, [&](int b) { return a + W * (j0 + b / W * NT + tid) + b % W; });
     }
-    if (tid < head + (i1 - tail)) {
-        const int at = tid < head ? i0 + tid : tail + tid - head;
-        const float l = value(x, at);
-        if (test(l)) act(l, at);
-    }
+    // the logits beside the boundaries
+    const bool mine = tid < head + (i1 - tail);
+    const int at = tid < head ? i0 + tid : tail + tid - head;
+    if (head + (i1 - tail) > 0) act(mine && test(value(x, at)) ? 1u : 0u, [&](int) { return at; });
 }
 
-// f(logit) for the logits of a whole row that have mass, with their y.
-template <int NT, class T, class F>
-__device__ __forceinline__ void each_mass(const T* x, int V, const Scale& sc, F f)
+// act(logit, index) for those that pass.
+template <int NT, int L, class T, class Test, class Act>
+__device__ __forceinline__ void each_if(const T* x, int i0, int i1, Test test, Act act)
 {
-    each_if<NT, 8>(x, 0, V, [&](float l) { return sc.y(l) > kDeepest; }, [&](float l, int) { f(l, sc.y(l)); });
+    each_batch<NT, L>(x, i0, i1, test, [&](uint32_t passed, auto index) {
+        while (passed) {
+            const int at = index(__ffs(passed) - 1);
+            passed &= passed - 1;
+            act(value(x, at), at);
+        }
+    });
+}
+
+// The indexes of those that pass go to the list, counted in S.n, which may pass kList. A wave reserves
+// room for its batch at once; the logits are read again behind that (to_keys), all at the same time.
+template <int NT, int L, class T, class Test>
+__device__ __forceinline__ void collect(Shared<NT>& S, const T* x, int i0, int i1, Test test)
+{
+    each_batch<NT, L>(x, i0, i1, test, [&](uint32_t passed, auto index) {
+        if (!__any(passed)) return;
+        const uint32_t c = __popc(passed), upto = wave_sums(c);
+        uint32_t at = 0;
+        if ((threadIdx.x & 63) == 63) at = atomicAdd(&S.n, upto);
+        at = __builtin_amdgcn_readlane(at, 63) + upto - c;
+        while (passed) {
+            if (at < kList) S.list[at] = static_cast<u64>(index(__ffs(passed) - 1));
+            at++;
+            passed &= passed - 1;
+        }
+    });
+}
+
+template <int NT>
+__device__ __forceinline__ void fill_middles(Shared<NT>& S)
+{
+    for (int b = threadIdx.x; b < kBins; b += NT) S.mid[b] = middle(b);
+}
+
+// f(logit, bin, mass) for the logits of a whole row that have mass (with S.mid filled).
+template <int NT, class T, class F>
+__device__ __forceinline__ void each_mass(const Shared<NT>& S, const T* x, int V, const Scale& sc, F f)
+{
+    each_if<NT, 8>(
+        x, 0, V, [&](float l) { return sc.y(l) > kDeepest; },
+        [&](float l, int) {
+            const double y = sc.y(l), bin = bin_sum(y);
+            const int b = low_bits(bin);
+            f(l, b, whole(weight(y, bin, S.mid[b])));
+        });
 }
 
 // A row's settings, brought into range.
@@ -301,6 +365,20 @@ __device__ int find_mass(Shared<NT>& S, u64 t, int slot)
         if (S.H[b] < t && t <= S.H[b + 1]) S.found[slot] = b;
     __syncthreads();
     return S.found[slot];
+}
+
+// The same for two masses at once.
+template <int NT>
+__device__ void find_two(Shared<NT>& S, u64 t, u64 u, int& f, int& g)
+{
+    for (int b = threadIdx.x; b < kBins; b += NT) {
+        const u64 from = S.H[b], to = S.H[b + 1];
+        if (from < t && t <= to) S.found[1] = b;
+        if (from < u && u <= to) S.found[2] = b;
+    }
+    __syncthreads();
+    f = S.found[1];
+    g = S.found[2];
 }
 
 // H and (counts) C from contents of bins to sums before each bin.
@@ -370,44 +448,63 @@ __device__ float reached_by(Shared<NT>& S, float mine, const Scale& sc, uint32_t
     return b < 0 ? -INFINITY : below_bin(sc, b);
 }
 
-template <int NT>
-__device__ __forceinline__ void append(Shared<NT>& S, float l, int i)
+// Keys in place of the indexes in the list.
+template <int NT, class T>
+__device__ __forceinline__ void to_keys(Shared<NT>& S, const T* x, int n)
 {
-    const uint32_t at = atomicAdd(&S.n, 1u);
-    if (at < kList) S.list[at] = key_of(l, i);
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const int at = static_cast<int>(S.list[i]);
+        S.list[i] = key_of(value(x, at), at);
+    }
+    __syncthreads();
 }
 
-// The tokens of i0 .. i1-1 that reach tau go to the list (counted in S.n, which may pass kList); with
-// `masses` all tokens' masses go to the histogram.
+// The indexes of the tokens of i0 .. i1-1 that reach tau go to the list (those that have no mass only
+// if they come within the rounding of its end); with `masses` all tokens' masses go to the histogram.
 template <int NT, class T>
 __device__ void gather(Shared<NT>& S, const T* x, int i0, int i1, const Scale& sc, float tau, bool masses)
 {
-    auto act = [&](float l, int i) {
-        if (sc.y(l) > kDeepest) append(S, l, i);
-    };
     const double top = static_cast<double>(sc.top);
-    const float end = below_bin(sc, static_cast<int>(-kDeepest * kBinsPerUnit));
+    const float end = fmaxf(below_bin(sc, static_cast<int>(-kDeepest * kBinsPerUnit)), -FLT_MAX);
+    tau = fmaxf(tau, end);
     if (masses)
-        each_if<NT, 16>(
-            x, i0, i1,
+        collect<NT, 16>(
+            S, x, i0, i1,
             [&](float l) {
                 // Without branches, so that the exponentials of several logits overlap: what has no mass (NaN
                 // too) adds to a place of its lane's own. (The largest logit is finite here, and masses
                 // a little below the end are 0.)
-                const double y = fmax((static_cast<double>(l) - top) * sc.c, kDeepest - 0.49);
-                atomicAdd(l > end ? &S.H[bin_of(y)] : &S.upto[threadIdx.x & 63], whole(weight(y)));
+                const double y = fmax((static_cast<double>(l) - top) * sc.c, kDeepest - 0.49), bin = bin_sum(y);
+                const int b = low_bits(bin);
+                atomicAdd(l >= end ? &S.H[b] : &S.upto[threadIdx.x & 63], whole(weight(y, bin, S.mid[b])));
                 return l >= tau;
-            },
-            act);
+            });
     else
-        each_if<NT, 32>(x, i0, i1, [&](float l) { return l >= tau; }, act);
+        collect<NT, 32>(S, x, i0, i1, [&](float l) { return l >= tau; });
+}
+
+// The place of a token's bin among the marked ones, drawn out to `sub` sort bins each by its place
+// within it. A token of no marked bin, there by rounding alone, goes before the next one.
+template <int NT>
+__device__ __forceinline__ int marked_place(const Shared<NT>& S, const Scale& sc, u64 key, int sub)
+{
+    const Marks& K = S.marks;
+    const double v = fmin(sc.y(key_value(key)) * -kBinsPerUnit, kBins - 1.0);  // -inf and the like of y too
+    const int b = low_bits(v + kRound);
+    const uint32_t w = K.take[b >> 5], bit = 1u << (b & 31);
+    int at = static_cast<int>(K.before[b >> 5] + __popc(w & (bit - 1))) * sub;
+    if (w & bit) {
+        const int f = static_cast<int>((v - b + 0.5) * sub);
+        at += f < sub - 1 ? f : sub - 1;
+    }
+    return at < kBins - 1 ? at : kBins - 1;
 }
 
 // Sort the n (1 .. kList) tokens of the list: into bins that share out the range between its largest
-// and smallest logit, then by comparing within a bin. Lists that crowd a bin (ties) go through a
-// bitonic network instead. Uses C.
+// and smallest logit (or, of marked bins, those), then by comparing within a bin. Lists that crowd a bin
+// (ties) go through a bitonic network instead: 512 tokens in 10 us. Uses C.
 template <int NT>
-__device__ void sort_list(Shared<NT>& S, int n)
+__device__ void sort_list(Shared<NT>& S, const Scale& sc, int n, bool marked)
 {
     const int tid = threadIdx.x;
     uint32_t lo = ~0u, hi = 0;
@@ -417,31 +514,41 @@ __device__ void sort_list(Shared<NT>& S, int n)
         S.crowd = 0;
     }
     clear_bins(S, false, true);
-    for (int i = tid; i < n; i += NT) {
-        const uint32_t o = static_cast<uint32_t>(S.list[i] >> 32);
-        lo = o < lo ? o : lo;
-        hi = o > hi ? o : hi;
-    }
+    float top = 0.f, scale = 0.f;
+    int sub = 0;
+    if (marked) {
+        sub = kBins / static_cast<int>(S.marks.bins);
+    } else {
+        for (int i = tid; i < n; i += NT) {
+            const uint32_t o = static_cast<uint32_t>(S.list[i] >> 32);
+            lo = o < lo ? o : lo;
+            hi = o > hi ? o : hi;
+        }
 #pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const uint32_t a = __shfl_xor(lo, d), b = __shfl_xor(hi, d);
-        lo = a < lo ? a : lo;
-        hi = b > hi ? b : hi;
+        for (int d = 32; d; d >>= 1) {
+            const uint32_t a = __shfl_xor(lo, d), b = __shfl_xor(hi, d);
+            lo = a < lo ? a : lo;
+            hi = b > hi ? b : hi;
+        }
+        __syncthreads();
+        if ((tid & 63) == 0) {
+            atomicMin(&S.first, lo);
+            atomicMax(&S.last, hi);
+        }
     }
     __syncthreads();
-    if ((tid & 63) == 0) {
-        atomicMin(&S.first, lo);
-        atomicMax(&S.last, hi);
+    if (!marked) {
+        top = order_value(S.first);
+        const float span = top - order_value(S.last);
+        scale = span > 0.f && span < INFINITY ? (kBins - 1) / span : 0.f;
     }
-    __syncthreads();
-    const float top = order_value(S.first), span = top - order_value(S.last);
-    const float scale = span > 0.f && span < INFINITY ? (kBins - 1) / span : 0.f;
     auto bin = [&](u64 k) {
+        if (marked) return marked_place(S, sc, k, sub);
         const int b = scale > 0.f ? static_cast<int>((top - key_value(k)) * scale) : 0;
         return b < kBins - 1 ? b : kBins - 1;
     };
     for (int i = tid; i < n; i += NT)
-        if (atomicAdd(&S.C[bin(S.list[i])], 1u) == 31) S.crowd = 1;
+        if (atomicAdd(&S.C[bin(S.list[i])], 1u) == kCrowd) S.crowd = 1;
     __syncthreads();
     if (!S.crowd) {
         bins_to_sums(S, false, true);
@@ -479,10 +586,13 @@ __device__ void sort_list(Shared<NT>& S, int n)
         }
 }
 
-__device__ __forceinline__ u64 mass_of(const Scale& sc, u64 key) { return whole(weight(sc.y(key_value(key)))); }
+// y of a token of the list, and its mass: 0 from kDeepest down, where weight() ends.
+__device__ __forceinline__ double listed_y(const Scale& sc, u64 key) { return fmax(sc.y(key_value(key)), kDeepest - 0.49); }
+__device__ __forceinline__ u64 mass_of(const Scale& sc, u64 key) { return whole(weight(listed_y(sc, key))); }
 
 // upto[] of the sorted list: masses summed within the list (rows == false), or over the row by the
-// sums in H, where the list holds whole bins (H of those bins is used up). Returns the place of the
+// sums in H, where the list holds whole bins (H of those bins is used up; tokens of other bins, there
+// by rounding alone, get sums between those of the marked bins around them). Returns the place of the
 // first token of bin b1 in the list (rows only).
 template <int NT>
 __device__ int sum_list(Shared<NT>& S, int n, const Scale& sc, bool rows, int b1)
@@ -499,7 +609,7 @@ __device__ int sum_list(Shared<NT>& S, int n, const Scale& sc, bool rows, int b1
     if (tid == 0) S.found[3] = 0;
     block_sums(S, total, 0, before, unused);
     u64 m = before;
-    auto bin = [&](int i) { return bin_of(sc.y(key_value(S.list[i]))); };
+    auto bin = [&](int i) { return bin_of(listed_y(sc, S.list[i])); };
     for (int i = from; i < to; i++) {
         if (rows) {
             const int b = bin(i);
@@ -532,23 +642,41 @@ __device__ __forceinline__ int first_that(int n, F reached)
     return from + __ffsll(static_cast<long long>(b)) - 1;
 }
 
-// Answer from the sorted beginning of the order (n tokens; all: every token with mass is in it; Z: the
+// Whether the list that tau gives has every token with mass.
+__device__ __forceinline__ bool holds_all(const Scale& sc, float tau) { return tau == -INFINITY || sc.top == INFINITY; }
+
+// Whether min-p's cut is above tau by a margin in y.
+__device__ __forceinline__ bool cuts_above(const Row& r, const Scale& sc, float tau, double margin)
+{
+    return r.only_first || sc.y(tau) < log2(static_cast<double>(r.least)) - margin;
+}
+
+// Whether the masses of all tokens are needed beside the list that tau gives.
+__device__ __forceinline__ bool needs_masses(const Row& r, const Scale& sc, float tau)
+{
+    if (r.by_k || holds_all(sc, tau)) return false;  // the list answers, or from_row counts for itself
+    if (r.by_p || !r.by_m) return true;
+    return !cuts_above(r, sc, tau, 0.01);  // min-p alone, and its cut lies in the list
+}
+
+// Answer from the beginning of the order (n tokens, those that reach tau; all: every token with mass is in it; Z: the
 // row's mass, 0 if not known). Leaves the token in S.drawn and returns the mass kept; 0 if a
 // question reaches past the list.
 template <int NT>
-__device__ u64 from_list(Shared<NT>& S, const Row& r, const Scale& sc, int n, bool all, u64 Z)
+__device__ u64 from_list(Shared<NT>& S, const Row& r, const Scale& sc, int n, float tau, u64 Z)
 {
-    if (Z && !r.by_m) {
-        // without min-p the first question decides: does it reach past the list?
+    const bool all = holds_all(sc, tau);
+    if (Z && !(r.by_m && cuts_above(r, sc, tau, -0.01))) {
+        // the first question decides: does it reach past the list? (min-p does unless it cuts in the list)
         u64 m = 0, before;
         uint32_t unused;
         for (int i = threadIdx.x; i < n; i += NT) m += mass_of(sc, S.list[i]);
         block_sums(S, m, 0, before, unused);
         if (threadIdx.x == NT - 1) S.mass[0] = before + m;
         __syncthreads();
-        if ((r.by_p ? r.p_target(Z) : r.u_target(Z)) > S.mass[0]) return 0;
+        if ((r.by_p ? r.p_target(Z) : r.by_m ? Z : r.u_target(Z)) > S.mass[0]) return 0;
     }
-    sort_list(S, n);
+    sort_list(S, sc, n, false);
     sum_list(S, n, sc, false, 0);
     if (threadIdx.x < 64) {
         const u64 L = S.upto[n - 1];
@@ -605,12 +733,12 @@ __device__ u64 search_row(Shared<NT>& S, const T* x, int V, const Scale& sc, int
             dc[threadIdx.x] = 0;
         }
         __syncthreads();
-        each_mass<NT>(x, V, sc, [&](float l, double y) {
-            if (bin_of(y) != b) return;
+        each_mass<NT>(S, x, V, sc, [&](float l, int bin, u64 mass) {
+            if (bin != b) return;
             const uint32_t o = order_bits(l);
             if (level && (o >> (shift + 8)) != prefix) return;
             const uint32_t d = (o >> shift) & 255u;
-            atomicAdd(&dm[d], whole(weight(y)));
+            atomicAdd(&dm[d], mass);
             atomicAdd(&dc[d], 1u);
         });
         __syncthreads();
@@ -657,10 +785,10 @@ __device__ void count_row(Shared<NT>& S, const T* x, int V, const Scale& sc)
 {
     __syncthreads();
     clear_bins(S, true, true);
+    fill_middles(S);
     __syncthreads();
-    each_mass<NT>(x, V, sc, [&](float, double y) {
-        const int b = bin_of(y);
-        atomicAdd(&S.H[b], whole(weight(y)));
+    each_mass<NT>(S, x, V, sc, [&](float, int b, u64 mass) {
+        atomicAdd(&S.H[b], mass);
         atomicAdd(&S.C[b], 1u);
     });
     bins_to_sums(S, true, true);
@@ -690,7 +818,7 @@ __device__ void mark_bins(Shared<NT>& S, const Row& r, const Scale& sc)
     auto mark = [&](int w, int f, int g) {
         for (int b = f + tid; b <= g; b += NT) atomicOr(&K.take[b >> 5], 1u << (b & 31));
         if (tid == 0) {
-            K.from[w] = below_bin(sc, g);
+            K.from[w] = fmaxf(below_bin(sc, g), -FLT_MAX);
             const float t = f ? below_bin(sc, f - 1) : INFINITY;
             K.to[w] = f ? t + fabsf(t) * 0x1p-20f + 3 * FLT_MIN : INFINITY;
         }
@@ -708,53 +836,65 @@ __device__ void mark_bins(Shared<NT>& S, const Row& r, const Scale& sc)
             K.c1 = S.C[b1];
         }
     }
-    if (r.by_p) {
-        const int f = find_mass(S, r.p_target(lo), 1), g = find_mass(S, r.p_target(hi), 2);
-        lo = S.H[f] < 1 ? 1 : S.H[f];
-        hi = S.H[g + 1] < hi ? S.H[g + 1] : hi;
-        mark(1, f, g);
+    // of top-p and min-p, one that surely keeps no less than the other decides nothing
+    bool by_p = r.by_p, by_m = r.by_m;
+    int f1 = 0, g1 = 0, q0 = 0, q1 = 0;
+    if (by_p) {
+        find_two(S, r.p_target(lo), r.p_target(hi), f1, g1);
     }
-    if (r.by_m) {
+    if (by_m) {
         const int c = bin_of(log2(static_cast<double>(r.least)));
-        const int q0 = c > 0 ? c - 1 : 0, q1 = c + 1 < kBins - 1 ? c + 1 : kBins - 1;
+        q0 = c > 0 ? c - 1 : 0;
+        q1 = c + 1 < kBins - 1 ? c + 1 : kBins - 1;
+        if (by_p && S.H[q0] >= S.H[g1 + 1]) by_m = false;
+        if (by_p && S.H[q1 + 1] <= S.H[f1] && S.H[q1 + 1] >= kOne) by_p = false;
+    }
+    if (by_p) {
+        lo = S.H[f1] < 1 ? 1 : S.H[f1];
+        hi = S.H[g1 + 1] < hi ? S.H[g1 + 1] : hi;
+        mark(1, f1, g1);
+    }
+    if (by_m) {
         if (S.H[q0] < lo) lo = S.H[q0] < 1 ? 1 : S.H[q0];
         hi = S.H[q1 + 1] < hi ? S.H[q1 + 1] : hi;
         mark(2, q0, q1);
-        if (tid == 0) {
-            K.q0 = q0;
-            K.q1 = q1;
-        }
+    }
+    if (tid == 0) {
+        K.by_p = by_p;
+        K.by_m = by_m;
+        K.q0 = q0;
     }
     __syncthreads();
-    const int f = find_mass(S, r.u_target(lo), 1), g = find_mass(S, r.u_target(hi), 2);
+    int f, g;
+    find_two(S, r.u_target(lo), r.u_target(hi), f, g);
     mark(3, f, g);
+    __syncthreads();
+    if (tid < kBins / 32) {
+        static_assert(kBins / 32 == 64, "one wave");
+        const uint32_t c = __popc(K.take[tid]), upto = wave_sums(c);
+        K.before[tid] = upto - c;
+        if (tid == 63) K.bins = upto;
+    }
     __syncthreads();
 }
 
-// The tokens of the marked bins among i0 .. i1-1 go to the list (counted in S.n, which may pass kList).
-// Most are outside by their logits alone: that is tested without branches, for the draw's range
-// alone, or top-p's too, or all.
+// The tokens of the marked bins go to the list (counted in S.n, which may pass kList), told by their
+// logits: the draw's range alone, or top-p's or min-p's too, or all.
 template <int NT, class T>
-__device__ void gather_marked(Shared<NT>& S, const T* x, int i0, int i1, const Row& r, const Scale& sc)
+__device__ void gather_marked(Shared<NT>& S, const T* x, int V)
 {
     const Marks& K = S.marks;
-    auto check = [&](float l, int i) {
-        const double y = sc.y(l);
-        if (!(y > kDeepest)) return;
-        const int b = bin_of(y);
-        if ((K.take[b >> 5] >> (b & 31)) & 1u) append(S, l, i);
-    };
     const float f0 = K.from[0], f1 = K.from[1], f2 = K.from[2], f3 = K.from[3];
     const float t0 = K.to[0], t1 = K.to[1], t2 = K.to[2], t3 = K.to[3];
-    if (K.by_k || r.by_m)
-        each_if<NT, 32>(
-            x, i0, i1,
-            [&](float l) { return ((l >= f0) & (l <= t0)) | ((l >= f1) & (l <= t1)) | ((l >= f2) & (l <= t2)) | ((l >= f3) & (l <= t3)); },
-            check);
-    else if (r.by_p)
-        each_if<NT, 32>(x, i0, i1, [&](float l) { return ((l >= f1) & (l <= t1)) | ((l >= f3) & (l <= t3)); }, check);
+    const float fa = K.by_p ? f1 : f2, ta = K.by_p ? t1 : t2;
+    if (K.by_k || (K.by_p && K.by_m))
+        collect<NT, 32>(S, x, 0, V, [&](float l) {
+            return ((l >= f0) & (l <= t0)) | ((l >= f1) & (l <= t1)) | ((l >= f2) & (l <= t2)) | ((l >= f3) & (l <= t3));
+        });
+    else if (K.by_p || K.by_m)
+        collect<NT, 32>(S, x, 0, V, [&](float l) { return ((l >= fa) & (l <= ta)) | ((l >= f3) & (l <= t3)); });
     else
-        each_if<NT, 32>(x, i0, i1, [&](float l) { return (l >= f3) & (l <= t3); }, check);
+        collect<NT, 32>(S, x, 0, V, [&](float l) { return (l >= f3) & (l <= t3); });
     __syncthreads();
 }
 
@@ -769,16 +909,17 @@ __device__ u64 from_marked(Shared<NT>& S, const T* x, int V, const Row& r, const
     const bool by_k = K.by_k;
     __syncthreads();
     if (n <= kList) {
-        sort_list(S, n);
-        const u64 before_m = r.by_m ? S.H[K.q0] : 0;  // mass before min-p's bins
+        to_keys(S, x, n);
+        sort_list(S, sc, n, true);
+        const u64 before_m = K.by_m ? S.H[K.q0] : 0;  // mass before min-p's bins
         const int before_b1 = sum_list(S, n, sc, true, by_k ? K.b1 : -2);
         if (tid < 64) {
             u64 kept = by_k ? S.upto[r.k - 1 - K.c1 + before_b1] : K.Z;
-            if (r.by_p) {
+            if (K.by_p) {
                 const u64 t = r.p_target(kept);
                 kept = S.upto[first_that(n, [&](int i) { return S.upto[i] >= t; })];
             }
-            if (r.by_m) {
+            if (K.by_m) {
                 u64 m = kOne;  // the first token is never left out
                 if (!r.only_first) {
                     const u64 w = r.least_mass();
@@ -800,18 +941,17 @@ __device__ u64 from_marked(Shared<NT>& S, const T* x, int V, const Row& r, const
     }
     u64 kept = K.Z;
     if (by_k) kept = search_row(S, x, V, sc, K.b1, true, static_cast<u64>(r.k), false);
-    if (r.by_p) {
+    if (K.by_p) {
         const u64 t = r.p_target(kept);
         __syncthreads();
         const int b = find_mass(S, t, 1);
         kept = search_row(S, x, V, sc, b, false, t, false);
     }
-    if (r.by_m) {
+    if (K.by_m) {
         const u64 w = r.least_mass();
         u64 m = 0;
-        each_mass<NT>(x, V, sc, [&](float, double y) {
-            const u64 v = whole(weight(y));
-            if (v >= w) m += v;
+        each_mass<NT>(S, x, V, sc, [&](float, int, u64 mass) {
+            if (mass >= w) m += mass;
         });
         if (tid == 0) S.mass[2] = 0;
         __syncthreads();
@@ -835,19 +975,8 @@ __device__ u64 from_row(Shared<NT>& S, const T* x, int V, const Row& r, const Sc
     if (!have_masses) count_row(S, x, V, sc);
     __syncthreads();
     mark_bins(S, r, sc);
-    gather_marked(S, x, 0, V, r, sc);
+    gather_marked(S, x, V);
     return from_marked(S, x, V, r, sc, static_cast<int>(S.n));
-}
-
-// Whether the list that tau gives has every token with mass.
-__device__ __forceinline__ bool holds_all(const Scale& sc, float tau) { return tau == -INFINITY || sc.top == INFINITY; }
-
-// Whether the masses of all tokens are needed beside the list that tau gives.
-__device__ __forceinline__ bool needs_masses(const Row& r, const Scale& sc, float tau)
-{
-    if (r.by_k || holds_all(sc, tau)) return false;  // the list answers, or from_row counts for itself
-    if (r.by_p || !r.by_m) return true;
-    return !(sc.y(tau) < log2(static_cast<double>(r.least)) - 0.01);  // min-p alone, and its cut lies in the list
 }
 
 __device__ __forceinline__ void write_row(const SampleArgs& a, int64_t row, int32_t token, float prob)
@@ -887,12 +1016,12 @@ __device__ __forceinline__ U got(const U* p)
 // workgroup that is the row's last. put() writes through to memory, and every wave's writes are there
 // before its barrier; so the last workgroup finds all of them (a fence would write back the whole
 // L2: with 512 workgroups that took 10 us).
-template <int NT>
-__device__ bool hand_over(Shared<NT>& S, u64* list, uint32_t* n, uint32_t* arrived, uint32_t parts)
+template <int NT, class T>
+__device__ bool hand_over(Shared<NT>& S, const T* x, u64* list, uint32_t* n, uint32_t* arrived, uint32_t parts)
 {
     const uint32_t mine = S.n < kList ? S.n : kList;
     if (threadIdx.x == 0) S.found[0] = static_cast<int>(atomicAdd(n, S.n));
-    __syncthreads();
+    to_keys(S, x, static_cast<int>(mine));
     const uint32_t at = static_cast<uint32_t>(S.found[0]);
     for (uint32_t i = threadIdx.x; i < mine; i += NT)
         if (at + i < kList) put(&list[at + i], S.list[i]);
@@ -935,6 +1064,7 @@ __global__ void __launch_bounds__(NT) sample_rows(SampleArgs a)
         tau = reached_by(S, mine, sc, r.by_k ? (r.k > 32 ? static_cast<uint32_t>(r.k) : 32u) : kAim);
         masses = needs_masses(r, sc, tau);
         clear_bins(S, masses, false);
+        if (masses) fill_middles(S);
         if (threadIdx.x == 0) S.n = 0;
         __syncthreads();
         gather(S, x, 0, a.V, sc, tau, masses);
@@ -943,7 +1073,10 @@ __global__ void __launch_bounds__(NT) sample_rows(SampleArgs a)
     const int n = listed ? static_cast<int>(S.n) : 0;
     if (masses) bins_to_sums(S, true, false);
     u64 kept = 0;
-    if (listed && n <= kList) kept = from_list(S, r, sc, n, holds_all(sc, tau), masses ? S.H[kBins] : 0);
+    if (listed && n <= kList) {
+        to_keys(S, x, n);
+        kept = from_list(S, r, sc, n, tau, masses ? S.H[kBins] : 0);
+    }
     if (!kept) kept = from_row(S, x, a.V, r, sc, masses);
     write_drawn(a, row, sc, S.drawn, kept);
 }
@@ -1011,6 +1144,7 @@ __global__ void __launch_bounds__(NT) sample_parts(SampleArgs a, RowSpace* space
     const bool listed = !r.by_k || r.short_k();
     const bool masses = needs_masses(r, sc, tau);
     clear_bins(S, masses, false);
+    if (masses) fill_middles(S);
     if (tid == 0) S.n = 0;
     __syncthreads();
     if (listed) gather(S, x, part_begin(a.V, part, parts), part_begin(a.V, part + 1, parts), sc, tau, masses);
@@ -1026,29 +1160,33 @@ __global__ void __launch_bounds__(NT) sample_parts(SampleArgs a, RowSpace* space
         m = wave_sums(m);
         if (lane == 63) atomicAdd(&R.Z, m);
     }
-    if (!hand_over(S, R.list, &R.n, &R.arrived, parts)) return;
+    if (!hand_over(S, x, R.list, &R.n, &R.arrived, parts)) return;
     const uint32_t n = got(&R.n);
     const u64 Z = got(&R.Z);
     u64 kept = 0;
     if (listed && n <= kList) {
         for (uint32_t i = tid; i < n; i += NT) S.list[i] = got(&R.list[i]);
         __syncthreads();
-        kept = from_list(S, r, sc, static_cast<int>(n), holds_all(sc, tau), Z);
+        kept = from_list(S, r, sc, static_cast<int>(n), tau, Z);
     }
     if (!kept) {
         if (masses) {
             __syncthreads();
-            for (int b = tid; b < kBins; b += NT) {
-                u64 m = 0;
-                for (uint32_t s = 0; s < parts; s += 8) {  // eight loads on the way at a time
-                    u64 v[8];
+            constexpr int B = kBins / NT, E = 16 / B;
+            u64 m[B] = {};
+            for (uint32_t s = 0; s < parts; s += E) {  // 16 loads on the way at a time
+                u64 v[E][B];
 #pragma unroll
-                    for (uint32_t e = 0; e < 8; e++) v[e] = got(&H[(s + e < parts ? s + e : s) * kBins + b]);
+                for (uint32_t e = 0; e < E; e++)
 #pragma unroll
-                    for (uint32_t e = 0; e < 8; e++) m += s + e < parts ? v[e] : 0;
-                }
-                S.H[b] = m;
+                    for (int b = 0; b < B; b++) v[e][b] = s + e < parts ? got(&H[(s + e) * kBins + b * NT + tid]) : 0;
+#pragma unroll
+                for (uint32_t e = 0; e < E; e++)
+#pragma unroll
+                    for (int b = 0; b < B; b++) m[b] += v[e][b];
             }
+#pragma unroll
+            for (int b = 0; b < B; b++) S.H[b * NT + tid] = m[b];
             bins_to_sums(S, true, false);
         }
         kept = from_row(S, x, a.V, r, sc, masses);
