@@ -165,8 +165,10 @@ __device__ __forceinline__ void store4(const F8Args& a, int64_t m, int64_t n, co
 
 // ------------------------------------------------------------------------- skinny
 // Few rows of X: 16 RT rows of W x 16 CT rows of X per workgroup, whose NW waves take the
-// groups in turn and meet in LDS. Each wave keeps U groups of both
-// operands in flight in registers. Bound by HBM (W once), so it takes the exact sums always.
+// groups in turn and meet in LDS. Each wave keeps U groups of both operands in flight in registers; many
+// small workgroups serve better than deep queues per wave, as W streams past once and the rest is the
+// launch and the last loads' latency. Bound by HBM, so it takes the exact sums always: M = 1, N = 14336,
+// K = 4096 (59 MB) 14.0 us, 11.4 of them at the rate of a large copy; the same with 16 x 16 tiles 15.0.
 template <int CT, int RT, int U, int NW>
 __global__ void __launch_bounds__(64 * NW) fp8_skinny(F8Args a)
 {
@@ -435,6 +437,14 @@ __device__ __forceinline__ void wait_transfers()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// M = 4096, N = 14336, K = 4096 into bf16: 244 to 255 us, 1.89 to 1.97 PFLOP/s with 256 x 256 tiles (278
+// with 256 x 128, 310 with 128 x 128). What bounds it there is power as much as feeding: the same launch
+// takes 230 us on operands that are all zero, 183 us as a timing copy without products and sums, 225 us
+// without transfers. Into fp32 435 us (1.1 PFLOP/s; a bf16 product's rate, whose matrix instruction it
+// takes, with the conversions beside it). Small products are bound by the launch, the pipeline's first
+// loads and the joining of K slices: M = 64, N = 4096, K = 14336 into fp32 19.3 us with 128 x 64 tiles and
+// eight slices, about 5 of them joining (30 without slices).
+//
 // One barrier per step, placed where every fragment of the
 // step is in registers: behind it the stage takes the step NST ahead, and the next step's
 // fragments of X replace this step's as the last MFMAs let go of them, so the matrix cores do not
@@ -607,9 +617,9 @@ hipError_t launch_tile(const F8Args& a, hipStream_t s)
 // ------------------------------------------------------------------------- choice
 // Kernel shapes and what a launch of them takes. The time of a launch is modelled as
 //   fixed + max(rounds of workgroups, bytes from HBM, bytes into the CUs) [+ joining K slices]
-// with constants fitted to 24000 launches measured on MI355X (M 1 to 4096, 12 pairs of N and K from
-// 128 to 28672, K slices 1 to 16): over those sizes the shape that the model picks takes 2.2% longer
-// than the fastest one on average, and 11% longer for one size in twenty.
+// with constants fitted to 22600 launches measured on MI355X (M 1 to 4096, 15 pairs of N and K from
+// 64 to 28672, K slices 1 to 16): over those sizes the shape that the model picks takes 1.6% longer
+// than the fastest one on average, and 8% longer or more for one size in twenty.
 struct Shape {
     int bn, bm, waves_k;  // rows of W and X per workgroup; waves that share a group out (tiles: 1)
     int per_cu;           // workgroups that fit a CU
@@ -620,26 +630,28 @@ struct Shape {
     float hbm, cu;     // TB/s from memory, into the CUs
     float again;       // share of W read again for every further tile along M
 };
-constexpr float kJoinFixed = 2.2f, kJoinRate = 2.7f;  // us; TB/s of partial sums written and read
+constexpr float kJoinFixed = 3.4f, kJoinRate = 2.7f;  // us; TB/s of partial sums written and read
 
 const Shape kSums[] = {
-    {256, 256, 1, 1, launch_tile<256, 256, 2, 4, 2, 2, false>, 6.31f, 1.75f, 1.41f, 1.41f, 4.06f, 8.94f, 0.81f},
-    {256, 128, 1, 1, launch_tile<256, 128, 4, 2, 3, 2, false>, 6.37f, 0.0f, 0.858f, 0.858f, 5.78f, 11.7f, 0.64f},
-    {128, 128, 1, 2, launch_tile<128, 128, 4, 2, 2, 1, false>, 4.32f, 0.517f, 0.599f, 1.04f, 5.71f, 14.1f, 0.75f},
-    {128, 64, 1, 2, launch_tile<128, 64, 4, 2, 3, 1, false>, 4.01f, 1.03f, 0.373f, 0.738f, 6.31f, 16.9f, 0.46f},
-    {128, 32, 1, 2, launch_tile<128, 32, 4, 1, 3, 1, false>, 3.43f, 1.61f, 0.354f, 0.527f, 6.15f, 19.2f, 0.32f},
-    {16, 16, 8, 8, launch_skinny<1, 1, 1, 8>, 3.12f, 0.37f, 0.578f, 4.15f, 6.0f, 10.0f, 0.31f},
-    {16, 16, 16, 2, launch_skinny<1, 1, 1, 16>, 2.96f, 0.49f, 1.13f, 2.32f, 4.64f, 9.28f, 0.3f},
-    {32, 16, 16, 2, launch_skinny<1, 2, 1, 16>, 3.0f, 0.32f, 1.96f, 4.83f, 5.04f, 8.66f, 0.3f},
-    {32, 32, 16, 1, launch_skinny<2, 2, 1, 16>, 2.89f, 0.285f, 2.96f, 2.96f, 3.57f, 8.19f, 0.31f},
-    {32, 64, 8, 2, launch_skinny<4, 2, 1, 8>, 3.5f, 0.25f, 2.0f, 3.85f, 3.13f, 9.34f, 0.3f},
+    {256, 256, 1, 1, launch_tile<256, 256, 2, 4, 2, 2, false>, 3.81f, 1.55f, 1.38f, 1.38f, 4.34f, 9.27f, 0.862f},
+    {256, 128, 1, 1, launch_tile<256, 128, 4, 2, 3, 2, false>, 2.72f, 2.71f, 0.829f, 0.829f, 6.07f, 10.4f, 0.325f},
+    {128, 128, 1, 2, launch_tile<128, 128, 4, 2, 2, 1, false>, 3.57f, 0.391f, 0.582f, 0.994f, 6.09f, 14.0f, 0.759f},
+    {128, 64, 1, 2, launch_tile<128, 64, 4, 2, 3, 1, false>, 3.66f, 0.0f, 0.37f, 0.743f, 7.06f, 30.8f, 0.505f},
+    {128, 32, 1, 2, launch_tile<128, 32, 4, 1, 3, 1, false>, 2.95f, 0.618f, 0.354f, 0.531f, 6.81f, 19.5f, 0.33f},
+    {16, 16, 8, 8, launch_skinny<1, 1, 1, 8>, 2.27f, 0.419f, 0.704f, 4.15f, 5.78f, 9.93f, 0.3f},
+    {32, 16, 16, 2, launch_skinny<1, 2, 1, 16>, 2.34f, 0.346f, 2.26f, 4.62f, 4.99f, 8.56f, 0.3f},
+    {32, 32, 16, 1, launch_skinny<2, 2, 1, 16>, 2.56f, 0.274f, 3.11f, 3.11f, 3.64f, 8.01f, 0.301f},
+    {32, 64, 8, 2, launch_skinny<4, 2, 1, 8>, 2.74f, 0.256f, 2.24f, 4.11f, 2.96f, 8.85f, 0.59f},
 };
 const Shape kExact[] = {
-    {256, 128, 1, 1, launch_tile<256, 128, 4, 2, 3, 1, true>, 4.36f, 0.927f, 1.69f, 1.69f, 3.46f, 6.54f, 0.65f},
-    {128, 128, 1, 2, launch_tile<128, 128, 4, 2, 2, 1, true>, 3.73f, 1.09f, 1.02f, 2.13f, 3.19f, 7.19f, 0.78f},
-    {128, 64, 1, 2, launch_tile<128, 64, 4, 2, 3, 1, true>, 4.0f, 0.63f, 0.674f, 1.21f, 4.79f, 10.3f, 0.62f},
-    {128, 32, 1, 2, launch_tile<128, 32, 4, 1, 3, 1, true>, 3.38f, 1.37f, 0.511f, 0.752f, 5.41f, 13.5f, 0.43f},
-    kSums[5], kSums[6], kSums[7], kSums[8], kSums[9],
+    {256, 128, 1, 1, launch_tile<256, 128, 4, 2, 3, 1, true>, 2.91f, 1.26f, 1.66f, 1.66f, 3.6f, 6.49f, 0.734f},
+    {128, 128, 1, 2, launch_tile<128, 128, 4, 2, 2, 1, true>, 3.11f, 0.947f, 1.02f, 2.06f, 3.3f, 7.33f, 0.777f},
+    {128, 64, 1, 2, launch_tile<128, 64, 4, 2, 3, 1, true>, 3.7f, 0.0f, 0.671f, 1.15f, 5.17f, 10.7f, 0.594f},
+    {128, 32, 1, 2, launch_tile<128, 32, 4, 1, 3, 1, true>, 3.06f, 0.431f, 0.513f, 0.754f, 6.03f, 17.7f, 0.402f},
+    {16, 16, 8, 8, launch_skinny<1, 1, 1, 8>, 2.22f, 0.424f, 0.703f, 4.14f, 17.1f, 9.95f, 0.3f},
+    {32, 16, 16, 2, launch_skinny<1, 2, 1, 16>, 2.29f, 0.347f, 2.26f, 4.62f, 5.0f, 8.56f, 0.337f},
+    {32, 32, 16, 1, launch_skinny<2, 2, 1, 16>, 2.51f, 0.275f, 3.11f, 3.11f, 3.65f, 7.98f, 0.301f},
+    {32, 64, 8, 2, launch_skinny<4, 2, 1, 8>, 2.69f, 0.248f, 2.24f, 4.17f, 2.98f, 8.89f, 0.64f},
 };
 constexpr uint32_t kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16};
 

@@ -1037,7 +1037,9 @@ __device__ __forceinline__ int part_begin(int V, uint32_t part, uint32_t parts)
     return static_cast<int>(static_cast<int64_t>(V) * part / parts);
 }
 
-// One workgroup per row.
+// One workgroup per row. 256 rows of 131072 (134 MB) take 77 us: 18 the first pass (7.4 TB/s), 6 the beginning's
+// lower end, 14 the second pass or, with masses, 28 (bound by the 64-bit operations and LDS atomics),
+// 5 the list, and 17 to 20 in rows whose answers lie past it.
 template <class T, int NT>
 __global__ void __launch_bounds__(NT) sample_rows(SampleArgs a)
 {
@@ -1085,7 +1087,11 @@ __global__ void __launch_bounds__(NT) sample_rows(SampleArgs a)
 // a logit that enough of its threads reach. The second gathers the beginning of the order and, where
 // it is needed, the histogram; the workgroup that is last to do so for a row answers, from the list or
 // with passes over the whole row. (A third launch that shared those passes out over the CUs took
-// longer than it saved: 64 rows of 50257 50 us with it and 44 without, 256 of 131072 100 and 88.)
+// longer than it saved, 14% at 64 rows of 50257 and at 256 of 131072.)
+// What bounds it is latency: 64 rows of 50257 take 34 to 39 us by their settings, of which the loads of
+// the two launches are 4; a row answered from the beginning of the order is through 15 us after the
+// second launch starts, one that needs the marked bins 12 to 14 us later (joining the histograms 2.6,
+// marking 2.5, the pass over the row 5, sorting 2.5, sums and search 2.5).
 template <class T, int NT>
 __global__ void __launch_bounds__(NT) sample_tops(SampleArgs a, RowSpace* space, uint32_t parts)
 {
@@ -1195,9 +1201,9 @@ __global__ void __launch_bounds__(NT) sample_parts(SampleArgs a, RowSpace* space
 }
 
 // How a call is launched: workgroups per row and their threads. With few rows 512 threads pass their
-// barriers sooner (1 row of 131072: 15.7 us, 17.5 with 1024 threads); with more rows 1024 threads and
-// one workgroup for each of 256 CUs win (16 rows: 45 us, 54 with 512 threads and two; 64 rows of
-// 50257: 49 and 56 us). No part has less than 2048 logits.
+// barriers sooner (1 row of 131072: 15.5 us, 17.9 with 1024 threads); with more rows 1024 threads and
+// one workgroup for each of 256 CUs win (64 rows of 131072: 44 us, 50 with 512 threads or with two
+// workgroups; 64 rows of 50257: 36, 39 and 49 us). No part has less than 2048 logits.
 struct Launch {
     uint32_t parts, threads;
 };

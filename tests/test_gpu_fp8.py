@@ -362,15 +362,21 @@ def test_rows_past_32_bits():
 
 
 def test_gemm_slices_in_two_graphs_at_once():
-    """K in slices through a workspace, two captured products with one each, replayed on two streams."""
+    """Two captured products replayed on two streams, each with a workspace of its own; of the two sizes
+    the longer one is cut into K slices."""
     uw, torch = _uw(), torch_cuda()
-    M, N, K = 40, 512, 8192
+    sizes = ((40, 512, 8192), (64, 2048, 14336))
+    assert max(uw.fp8_gemm_workspace(*size) for size in sizes) > 0
+    for size in sizes:
+        _two_graphs(uw, torch, *size)
+
+
+def _two_graphs(uw, torch, M, N, K):
     need = uw.fp8_gemm_workspace(M, N, K)
-    assert need > 0
     runs = []
     for i in range(2):
         ld, (qx, sx, x), (qw, sw, w) = _operands(uw, np.random.default_rng(30 + i), M, N, K)
-        y, ws = torch.zeros(M, N, device="cuda"), torch.empty(need, dtype=torch.uint8, device="cuda")
+        y, ws = torch.zeros(M, N, device="cuda"), torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
         stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
         call = lambda: uw.fp8_gemm(qx, sx, qw, sw, y, M, N, K, ldx=ld, ldw=ld, d_ws=ws, ws_bytes=need)
         call()
