@@ -560,7 +560,7 @@ size_t uw_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K);
  * top_p or min_p leaves the step out; u is held to [0, 1), NaN counts as 0. Logits that are
  * NaN or -inf are never drawn and count nowhere (masks); where some are +inf they share the
  * mass. A row with nothing to draw gets token -1 and probability 0. Masses are integers, multiples
- * of 2^-43 of the largest token's (from a 64-bit exponential, within 2.2e-12), so results are the
+ * of 2^-43 of the largest token's (from a 64-bit exponential, within 7e-14), so results are the
  * same for every run and order; tokens below half of that weigh nothing and are never drawn.
  * Settings are device arrays of M, so that a captured graph can be replayed with others; NULL
  * leaves a step out (T = 1).
