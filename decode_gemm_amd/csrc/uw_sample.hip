@@ -34,7 +34,7 @@ typedef unsigned long long u64;
 constexpr int kBins = 2048;            // 46 per unit of y: the 44 units that have mass fill 2025 of them
 constexpr double kBinsPerUnit = 46.0, kUnitPerBin = 1.0 / 46.0;
 constexpr double kDeepest = -44.0;     // 2^43 * 2^y rounds to 0 from here down
-constexpr int kList = 2048;            // tokens that are sorted in LDS
+constexpr int kList = 4096;            // tokens that are sorted in LDS
 constexpr uint32_t kAim = 256;         // tokens that the gathered beginning of the order has at least
 constexpr uint32_t kCrowd = 255;       // most tokens of a sort bin that are compared with one another
 constexpr int kShort = 512;            // largest k that it is made to hold
@@ -137,7 +137,7 @@ struct Marks {
     uint32_t by_p, by_m;  // top-p and min-p may decide
     int32_t b1;
     uint32_t c1;
-    int32_t q0;         // first bin of min-p's cut
+    int32_t q0, q1;     // bins that min-p's cut may be in
     uint32_t take[kBins / 32];    // all these bins
     uint32_t before[kBins / 32];  // how many of them lie before each word's
     uint32_t bins;                // and in all
@@ -154,6 +154,7 @@ struct Shared {
     u64 wsum[NT / 64];
     uint32_t wcnt[NT / 64];
     float wmax[NT / 64];
+    uint32_t spare[64];  // where lanes add what counts nowhere
     uint32_t n, first, last, crowd;
     int found[4];
     u64 mass[4];
@@ -305,19 +306,6 @@ __device__ __forceinline__ void fill_middles(Shared<NT>& S)
     for (int b = threadIdx.x; b < kBins; b += NT) S.mid[b] = middle(b);
 }
 
-// f(logit, bin, mass) for the logits of a whole row that have mass (with S.mid filled).
-template <int NT, class T, class F>
-__device__ __forceinline__ void each_mass(const Shared<NT>& S, const T* x, int V, const Scale& sc, F f)
-{
-    each_if<NT, 8>(
-        x, 0, V, [&](float l) { return sc.y(l) > kDeepest; },
-        [&](float l, int) {
-            const double y = sc.y(l), bin = bin_sum(y);
-            const int b = low_bits(bin);
-            f(l, b, whole(weight(y, bin, S.mid[b])));
-        });
-}
-
 // A row's settings, brought into range.
 struct Row {
     bool by_k, by_p, by_m;
@@ -431,6 +419,28 @@ __device__ __forceinline__ float below_bin(const Scale& sc, int b)
     return t - fabsf(t) * 0x1p-22f - FLT_MIN;  // a little less, for the roundings; -inf where all logits weigh the same
 }
 
+// A logit at or above the upper end of bin b.
+__device__ __forceinline__ float above_bin(const Scale& sc, int b)
+{
+    if (b == 0) return INFINITY;
+    const float t = below_bin(sc, b - 1);
+    return t + fabsf(t) * 0x1p-20f + 3 * FLT_MIN;
+}
+
+// f(logit, bin, mass) for the logits of a row in the bins b0 .. b1 (with S.mid filled).
+template <int NT, class T, class F>
+__device__ __forceinline__ void each_mass(const Shared<NT>& S, const T* x, int V, const Scale& sc, int b0, int b1, F f)
+{
+    const float from = fmaxf(below_bin(sc, b1), -FLT_MAX), to = above_bin(sc, b0);
+    each_if<NT, 32>(
+        x, 0, V, [&](float l) { return (l >= from) & (l <= to); },
+        [&](float l, int) {
+            const double y = sc.y(l), bin = bin_sum(y);
+            const int b = low_bits(bin);
+            if (y > kDeepest && b >= b0 && b <= b1) f(l, b, whole(weight(y, bin, S.mid[b])));
+        });
+}
+
 // A logit that at least q of the threads' maxima `mine` reach; -inf if fewer than q have mass.
 template <int NT>
 __device__ float reached_by(Shared<NT>& S, float mine, const Scale& sc, uint32_t q)
@@ -459,26 +469,43 @@ __device__ __forceinline__ void to_keys(Shared<NT>& S, const T* x, int n)
     __syncthreads();
 }
 
-// The indexes of the tokens of i0 .. i1-1 that reach tau go to the list (those that have no mass only
-// if they come within the rounding of its end); with `masses` all tokens' masses go to the histogram.
-template <int NT, class T>
-__device__ void gather(Shared<NT>& S, const T* x, int i0, int i1, const Scale& sc, float tau, bool masses)
+// The masses of all tokens of i0 .. i1-1 go to the histogram (COUNT: and their number), and the indexes of
+// those that reach tau to the list. Without branches, so that the exponentials of several logits
+// overlap: what has no mass (NaN too) adds to a place of its lane's own, and masses a little below
+// the end are 0.
+template <int NT, bool COUNT, class T>
+__device__ __forceinline__ void add_masses(Shared<NT>& S, const T* x, int i0, int i1, const Scale& sc, float end, float tau)
 {
     const double top = static_cast<double>(sc.top);
-    const float end = fmaxf(below_bin(sc, static_cast<int>(-kDeepest * kBinsPerUnit)), -FLT_MAX);
+    collect<NT, 16>(S, x, i0, i1, [&](float l) {
+        double y = fmax((static_cast<double>(l) - top) * sc.c, kDeepest - 0.49);
+        if (COUNT && l == sc.top) y = 0.0;  // an infinite one too
+        const double bin = bin_sum(y);
+        const int b = low_bits(bin);
+        atomicAdd(l >= end ? &S.H[b] : &S.upto[threadIdx.x & 63], whole(weight(y, bin, S.mid[b])));
+        if (COUNT) atomicAdd(((l >= end) & (y > kDeepest)) ? &S.C[b] : &S.spare[threadIdx.x & 63], 1u);
+        return l >= tau;
+    });
+}
+
+// What has no mass ends below this logit.
+__device__ __forceinline__ float mass_end(const Scale& sc)
+{
+    return fmaxf(below_bin(sc, static_cast<int>(-kDeepest * kBinsPerUnit)), -FLT_MAX);
+}
+
+// The indexes of the tokens of i0 .. i1-1 that reach tau go to the list (those that have no mass only
+// if they come within the rounding of its end); with `masses` all tokens' masses go to the histogram,
+// with `counts` their numbers too.
+template <int NT, class T>
+__device__ void gather(Shared<NT>& S, const T* x, int i0, int i1, const Scale& sc, float tau, bool masses, bool counts)
+{
+    const float end = mass_end(sc);
     tau = fmaxf(tau, end);
-    if (masses)
-        collect<NT, 16>(
-            S, x, i0, i1,
-            [&](float l) {
-                // Without branches, so that the exponentials of several logits overlap: what has no mass (NaN
-                // too) adds to a place of its lane's own. (The largest logit is finite here, and masses
-                // a little below the end are 0.)
-                const double y = fmax((static_cast<double>(l) - top) * sc.c, kDeepest - 0.49), bin = bin_sum(y);
-                const int b = low_bits(bin);
-                atomicAdd(l >= end ? &S.H[b] : &S.upto[threadIdx.x & 63], whole(weight(y, bin, S.mid[b])));
-                return l >= tau;
-            });
+    if (counts)
+        add_masses<NT, true>(S, x, i0, i1, sc, end, tau);
+    else if (masses)
+        add_masses<NT, false>(S, x, i0, i1, sc, end, tau);
     else
         collect<NT, 32>(S, x, i0, i1, [&](float l) { return l >= tau; });
 }
@@ -654,7 +681,8 @@ __device__ __forceinline__ bool cuts_above(const Row& r, const Scale& sc, float 
 // Whether the masses of all tokens are needed beside the list that tau gives.
 __device__ __forceinline__ bool needs_masses(const Row& r, const Scale& sc, float tau)
 {
-    if (r.by_k || holds_all(sc, tau)) return false;  // the list answers, or from_row counts for itself
+    if (holds_all(sc, tau)) return false;  // the list answers, or from_row counts for itself
+    if (r.by_k) return !r.short_k();
     if (r.by_p || !r.by_m) return true;
     return !cuts_above(r, sc, tau, 0.01);  // min-p alone, and its cut lies in the list
 }
@@ -733,8 +761,7 @@ __device__ u64 search_row(Shared<NT>& S, const T* x, int V, const Scale& sc, int
             dc[threadIdx.x] = 0;
         }
         __syncthreads();
-        each_mass<NT>(S, x, V, sc, [&](float l, int bin, u64 mass) {
-            if (bin != b) return;
+        each_mass<NT>(S, x, V, sc, b, b, [&](float l, int, u64 mass) {
             const uint32_t o = order_bits(l);
             if (level && (o >> (shift + 8)) != prefix) return;
             const uint32_t d = (o >> shift) & 255u;
@@ -787,10 +814,7 @@ __device__ void count_row(Shared<NT>& S, const T* x, int V, const Scale& sc)
     clear_bins(S, true, true);
     fill_middles(S);
     __syncthreads();
-    each_mass<NT>(S, x, V, sc, [&](float, int b, u64 mass) {
-        atomicAdd(&S.H[b], mass);
-        atomicAdd(&S.C[b], 1u);
-    });
+    gather(S, x, 0, V, sc, INFINITY, true, true);
     bins_to_sums(S, true, true);
 }
 
@@ -819,8 +843,7 @@ __device__ void mark_bins(Shared<NT>& S, const Row& r, const Scale& sc)
         for (int b = f + tid; b <= g; b += NT) atomicOr(&K.take[b >> 5], 1u << (b & 31));
         if (tid == 0) {
             K.from[w] = fmaxf(below_bin(sc, g), -FLT_MAX);
-            const float t = f ? below_bin(sc, f - 1) : INFINITY;
-            K.to[w] = f ? t + fabsf(t) * 0x1p-20f + 3 * FLT_MIN : INFINITY;
+            K.to[w] = above_bin(sc, f);
         }
     };
     if (by_k) {
@@ -843,9 +866,10 @@ __device__ void mark_bins(Shared<NT>& S, const Row& r, const Scale& sc)
         find_two(S, r.p_target(lo), r.p_target(hi), f1, g1);
     }
     if (by_m) {
-        const int c = bin_of(log2(static_cast<double>(r.least)));
-        q0 = c > 0 ? c - 1 : 0;
-        q1 = c + 1 < kBins - 1 ? c + 1 : kBins - 1;
+        // where a mass is r.least to within the rounding to whole ones
+        const double y = log2(static_cast<double>(r.least)), d = 1e-6 + 1.5 / static_cast<double>(r.least_mass());
+        q0 = bin_of(fmin(y + d, 0.0));
+        q1 = bin_of(fmax(y - d, kDeepest));
         if (by_p && S.H[q0] >= S.H[g1 + 1]) by_m = false;
         if (by_p && S.H[q1 + 1] <= S.H[f1] && S.H[q1 + 1] >= kOne) by_p = false;
     }
@@ -863,6 +887,7 @@ __device__ void mark_bins(Shared<NT>& S, const Row& r, const Scale& sc)
         K.by_p = by_p;
         K.by_m = by_m;
         K.q0 = q0;
+        K.q1 = q1;
     }
     __syncthreads();
     int f, g;
@@ -950,10 +975,10 @@ __device__ u64 from_marked(Shared<NT>& S, const T* x, int V, const Row& r, const
     if (K.by_m) {
         const u64 w = r.least_mass();
         u64 m = 0;
-        each_mass<NT>(S, x, V, sc, [&](float, int, u64 mass) {
+        each_mass<NT>(S, x, V, sc, K.q0, K.q1, [&](float, int, u64 mass) {
             if (mass >= w) m += mass;
         });
-        if (tid == 0) S.mass[2] = 0;
+        if (tid == 0) S.mass[2] = S.H[K.q0];
         __syncthreads();
         if (m) atomicAdd(&S.mass[2], m);
         __syncthreads();
@@ -994,10 +1019,10 @@ __device__ __forceinline__ void write_drawn(const SampleArgs& a, int64_t row, co
 }
 
 constexpr uint32_t kMostParts = 32;
-struct RowSpace {
+struct alignas(16) RowSpace {
     uint32_t n;        // tokens in the list
     uint32_t arrived;  // workgroups done with the row
-    u64 Z;             // mass of the row
+    u64 Z[kMostParts];  // the parts' masses
     float top[kMostParts], tau[kMostParts];
     u64 list[kList];
 };
@@ -1005,7 +1030,11 @@ static_assert(sizeof(RowSpace) % 16 == 0, "layout");
 
 // Data that workgroups of one launch hand to another: written through to, and read from, where all of
 // the device sees it.
-__device__ __forceinline__ void put(u64* p, u64 v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+template <class U>
+__device__ __forceinline__ void put(U* p, U v)
+{
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 template <class U>
 __device__ __forceinline__ U got(const U* p)
 {
@@ -1017,19 +1046,46 @@ __device__ __forceinline__ U got(const U* p)
 // before its barrier; so the last workgroup finds all of them (a fence would write back the whole
 // L2: with 512 workgroups that took 10 us).
 template <int NT, class T>
-__device__ bool hand_over(Shared<NT>& S, const T* x, u64* list, uint32_t* n, uint32_t* arrived, uint32_t parts)
+__device__ bool hand_over(Shared<NT>& S, const T* x, RowSpace& R, uint32_t part, uint32_t parts, bool masses)
 {
     const uint32_t mine = S.n < kList ? S.n : kList;
-    if (threadIdx.x == 0) S.found[0] = static_cast<int>(atomicAdd(n, S.n));
+    if (threadIdx.x == 0) S.found[0] = static_cast<int>(atomicAdd(&R.n, S.n));
     to_keys(S, x, static_cast<int>(mine));
     const uint32_t at = static_cast<uint32_t>(S.found[0]);
     for (uint32_t i = threadIdx.x; i < mine; i += NT)
-        if (at + i < kList) put(&list[at + i], S.list[i]);
+        if (at + i < kList) put(&R.list[at + i], S.list[i]);
+    if (masses && threadIdx.x == 0) {
+        u64 m = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 64; w++) m += S.wsum[w];
+        put(&R.Z[part], m);
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (threadIdx.x == 0) S.found[1] = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == parts;
+    if (threadIdx.x == 0) S.found[1] = __hip_atomic_fetch_add(&R.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == parts;
     __syncthreads();
     return S.found[1];
+}
+
+// The parts' bins, summed; 16 loads on the way at a time.
+template <int NT, class U>
+__device__ __forceinline__ void join_parts(U* to, const U* from, uint32_t parts)
+{
+    constexpr int B = kBins / NT, E = 16 / B;
+    U m[B] = {};
+    for (uint32_t s = 0; s < parts; s += E) {
+        U v[E][B];
+#pragma unroll
+        for (uint32_t e = 0; e < E; e++)
+#pragma unroll
+            for (int b = 0; b < B; b++) v[e][b] = s + e < parts ? got(&from[(s + e) * kBins + b * NT + threadIdx.x]) : 0;
+#pragma unroll
+        for (uint32_t e = 0; e < E; e++)
+#pragma unroll
+            for (int b = 0; b < B; b++) m[b] += v[e][b];
+    }
+#pragma unroll
+    for (int b = 0; b < B; b++) to[b * NT + threadIdx.x] = m[b];
 }
 
 __device__ __forceinline__ int part_begin(int V, uint32_t part, uint32_t parts)
@@ -1059,21 +1115,17 @@ __global__ void __launch_bounds__(NT) sample_rows(SampleArgs a)
     if (top == -INFINITY) return write_row(a, row, -1, 0.0f);  // nothing to draw
     const Scale sc = r.scale(top);
     const bool listed = !r.by_k || r.short_k();
-    float tau = 0.f;
-    bool masses = false;
-    if (listed) {
-        // room for the tokens that share the last one's bin
-        tau = reached_by(S, mine, sc, r.by_k ? (r.k > 32 ? static_cast<uint32_t>(r.k) : 32u) : kAim);
-        masses = needs_masses(r, sc, tau);
-        clear_bins(S, masses, false);
-        if (masses) fill_middles(S);
-        if (threadIdx.x == 0) S.n = 0;
-        __syncthreads();
-        gather(S, x, 0, a.V, sc, tau, masses);
-        __syncthreads();
-    }
-    const int n = listed ? static_cast<int>(S.n) : 0;
-    if (masses) bins_to_sums(S, true, false);
+    // room for the tokens that share the last one's bin
+    const float tau = listed ? reached_by(S, mine, sc, r.by_k ? (r.k > 32 ? static_cast<uint32_t>(r.k) : 32u) : kAim) : INFINITY;
+    const bool masses = needs_masses(r, sc, tau), counts = masses && !listed;
+    clear_bins(S, masses, counts);
+    if (masses) fill_middles(S);
+    if (threadIdx.x == 0) S.n = 0;
+    __syncthreads();
+    if (listed || masses) gather(S, x, 0, a.V, sc, tau, masses, counts);
+    __syncthreads();
+    const int n = static_cast<int>(S.n);
+    if (masses) bins_to_sums(S, true, counts);
     u64 kept = 0;
     if (listed && n <= kList) {
         to_keys(S, x, n);
@@ -1118,7 +1170,6 @@ __global__ void __launch_bounds__(NT) sample_tops(SampleArgs a, RowSpace* space,
         if (part == 0) {
             RowSpace& R = space[row];
             R.n = R.arrived = 0;
-            R.Z = 0;
         }
     }
 }
@@ -1148,27 +1199,34 @@ __global__ void __launch_bounds__(NT) sample_parts(SampleArgs a, RowSpace* space
     // no part had enough tokens: all of them (tau is +inf also where the largest logits are)
     if (tau == INFINITY && top < INFINITY) tau = -INFINITY;
     const bool listed = !r.by_k || r.short_k();
-    const bool masses = needs_masses(r, sc, tau);
-    clear_bins(S, masses, false);
+    const bool masses = needs_masses(r, sc, tau), counts = masses && !listed;
+    clear_bins(S, masses, counts);
     if (masses) fill_middles(S);
     if (tid == 0) S.n = 0;
     __syncthreads();
-    if (listed) gather(S, x, part_begin(a.V, part, parts), part_begin(a.V, part + 1, parts), sc, tau, masses);
+    if (listed || masses)
+        gather(S, x, part_begin(a.V, part, parts), part_begin(a.V, part + 1, parts), sc, listed ? tau : INFINITY, masses, counts);
     __syncthreads();
     // this part's tokens, mass and histogram go to the row's space
     u64* const H = hist + row * parts * kBins;
+    uint32_t* const C = reinterpret_cast<uint32_t*>(hist + a.M * parts * kBins) + row * parts * kBins;
     if (masses) {
         u64 m = 0;
         for (int b = tid; b < kBins; b += NT) {
             put(&H[part * kBins + b], S.H[b]);
+            if (counts) put(&C[part * kBins + b], S.C[b]);
             m += S.H[b];
         }
         m = wave_sums(m);
-        if (lane == 63) atomicAdd(&R.Z, m);
+        if (lane == 63) S.wsum[tid >> 6] = m;
     }
-    if (!hand_over(S, x, R.list, &R.n, &R.arrived, parts)) return;
+    if (!hand_over(S, x, R, part, parts, masses)) return;
     const uint32_t n = got(&R.n);
-    const u64 Z = got(&R.Z);
+    u64 Z = 0;
+    if (masses) {
+        Z = wave_sums(lane < static_cast<int>(parts) ? got(&R.Z[lane]) : u64{0});
+        Z = __shfl(Z, 63);
+    }
     u64 kept = 0;
     if (listed && n <= kList) {
         for (uint32_t i = tid; i < n; i += NT) S.list[i] = got(&R.list[i]);
@@ -1178,22 +1236,9 @@ __global__ void __launch_bounds__(NT) sample_parts(SampleArgs a, RowSpace* space
     if (!kept) {
         if (masses) {
             __syncthreads();
-            constexpr int B = kBins / NT, E = 16 / B;
-            u64 m[B] = {};
-            for (uint32_t s = 0; s < parts; s += E) {  // 16 loads on the way at a time
-                u64 v[E][B];
-#pragma unroll
-                for (uint32_t e = 0; e < E; e++)
-#pragma unroll
-                    for (int b = 0; b < B; b++) v[e][b] = s + e < parts ? got(&H[(s + e) * kBins + b * NT + tid]) : 0;
-#pragma unroll
-                for (uint32_t e = 0; e < E; e++)
-#pragma unroll
-                    for (int b = 0; b < B; b++) m[b] += v[e][b];
-            }
-#pragma unroll
-            for (int b = 0; b < B; b++) S.H[b * NT + tid] = m[b];
-            bins_to_sums(S, true, false);
+            join_parts<NT>(S.H, H, parts);
+            if (counts) join_parts<NT>(S.C, C, parts);
+            bins_to_sums(S, true, counts);
         }
         kept = from_row(S, x, a.V, r, sc, masses);
     }
@@ -1262,7 +1307,7 @@ size_t uw_sample_workspace(int64_t M, int64_t V)
 {
     if (M < 1 || V < 1 || V > UW_SAMPLE_MAX_V || M > kRowsMost) return 0;
     const Launch l = plan_launch(M, V);
-    return l.parts == 1 ? 0 : static_cast<size_t>(M) * (sizeof(RowSpace) + l.parts * kBins * sizeof(u64));
+    return l.parts == 1 ? 0 : static_cast<size_t>(M) * (sizeof(RowSpace) + l.parts * kBins * (sizeof(u64) + sizeof(uint32_t)));
 }
 
 uw_status uw_sample(const uw_sample_args* args, void* stream)

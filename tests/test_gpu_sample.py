@@ -310,3 +310,16 @@ def test_rows_past_32_bits(M, V, ld):
     uw.sample(far, u, tok[0], M, V, ld=ld, d_ws=ws, ws_bytes=need)
     ref = [_draw(l, float(v))[0] for l, v in zip(near.double().cpu().numpy(), u)]
     assert (tok[0].cpu().numpy() == np.array(ref)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,V", [(2, 40000), (3, 3000), (40, 9000)])
+def test_large_k_and_wide_distributions(M, V, dtype):
+    """k past what is gathered, alone and with the other steps, and distributions whose answers lie deep."""
+    uw = _uw()
+    rng = np.random.default_rng(M + V)
+    u = rng.random(M).astype(np.float32)
+    for spread, T in ((3.0, 1.0), (1.0, 1.0), (2.0, 3.0), (0.05, 1.0), (0.0, 1.0)):
+        x = (rng.standard_normal((M, V)) * spread).astype(np.float32)
+        for k, p, least in ((600, 1.0, 0.0), (2500, 0.7, 0.0), (V - 1, 0.999, 1e-3), (0, 0.9, 0.0), (0, 1.0, 1e-3), (0, 0.6, 0.02)):
+            _compare(uw, x, u, f"spread {spread}", dtype=dtype, temperature=[T] * M, top_k=[k] * M, top_p=[p] * M, min_p=[least] * M)
