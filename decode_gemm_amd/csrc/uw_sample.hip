@@ -416,7 +416,8 @@ __device__ __forceinline__ float below_bin(const Scale& sc, int b)
 {
     if (sc.top == INFINITY) return INFINITY;
     const float t = static_cast<float>(static_cast<double>(sc.top) - (static_cast<double>(b) + 0.5) / kBinsPerUnit / sc.c);
-    return t - fabsf(t) * 0x1p-22f - FLT_MIN;  // a little less, for the roundings; -inf where all logits weigh the same
+    // a little less, for the roundings (of the difference, too); -inf where all logits weigh the same
+    return t - fabsf(t) * 0x1p-22f - fabsf(sc.top) * 0x1p-48f - FLT_MIN;
 }
 
 // A logit at or above the upper end of bin b.
@@ -424,7 +425,7 @@ __device__ __forceinline__ float above_bin(const Scale& sc, int b)
 {
     if (b == 0) return INFINITY;
     const float t = below_bin(sc, b - 1);
-    return t + fabsf(t) * 0x1p-20f + 3 * FLT_MIN;
+    return t + fabsf(t) * 0x1p-20f + fabsf(sc.top) * 0x1p-46f + 3 * FLT_MIN;
 }
 
 // f(logit, bin, mass) for the logits of a row in the bins b0 .. b1 (with S.mid filled).

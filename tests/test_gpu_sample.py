@@ -42,15 +42,15 @@ def _draw(l, u, T=1.0, k=0, p=1.0, least=0.0):
             w = np.exp(np.where(d == 0, 0.0, d / T))
     if 0 < k < ids.size:
         w = w[:k]
-    mass = np.rint(w * ONE).astype(np.int64)
+    mass = np.rint(w * ONE).astype(np.uint64)  # 2^20 tokens of 2^43 are 2^63
     if p < 1:
-        before = np.concatenate([[0], np.cumsum(mass)[:-1]])
-        mass = mass[: max(1, int(np.count_nonzero(before < max(1, math.ceil(max(float(p), 0.0) * float(mass.sum()))))))]
+        before = np.cumsum(mass) - mass
+        mass = mass[: max(1, int(np.count_nonzero(before < np.uint64(max(1, math.ceil(max(float(p), 0.0) * float(mass.sum())))))))]
     if least > 0:
         mass = mass[: max(1, int(np.count_nonzero(w[: mass.size] >= least)))]
     c = np.cumsum(mass)
     u = 0.0 if not u > 0 else min(float(u), 1 - 2.0**-24)
-    j = int(np.searchsorted(c, int(u * float(c[-1])), side="right"))
+    j = int(np.searchsorted(c, np.uint64(int(u * float(c[-1]))), side="right"))
     return int(ids[j]), float(w[j] * ONE / float(c[-1]))
 
 
@@ -323,3 +323,33 @@ def test_large_k_and_wide_distributions(M, V, dtype):
         x = (rng.standard_normal((M, V)) * spread).astype(np.float32)
         for k, p, least in ((600, 1.0, 0.0), (2500, 0.7, 0.0), (V - 1, 0.999, 1e-3), (0, 0.9, 0.0), (0, 1.0, 1e-3), (0, 0.6, 0.02)):
             _compare(uw, x, u, f"spread {spread}", dtype=dtype, temperature=[T] * M, top_k=[k] * M, top_p=[p] * M, min_p=[least] * M)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_largest_vocabulary(dtype):
+    """2^20 logits: all equal, all at the type's lowest value, flat, masked to a few, an infinite one among them."""
+    uw = _uw()
+    V = 1 << 20
+    rng = np.random.default_rng(20)
+    x = np.zeros((5, V), np.float32)
+    x[1] = np.finfo(np.float32).min if dtype == "f32" else -float.fromhex("0x1.fep127")
+    x[2] = rng.standard_normal(V)
+    x[3] = -np.inf
+    x[3, rng.integers(0, V, 30)] = rng.standard_normal(30)
+    x[4] = rng.standard_normal(V)
+    x[4, [7, V - 1]] = np.inf
+    for k, p, least, T in ((0, 1.0, 0.0, 1.0), (0, 0.9, 0.0, 1.0), (100000, 0.5, 0.01, 2.0), (0, 1.0, 0.3, 1.0), (400, 0.9, 0.0, 1.0)):
+        u = rng.random(5).astype(np.float32)
+        _compare(uw, x, u, dtype=dtype, temperature=[T] * 5, top_k=[k] * 5, top_p=[p] * 5, min_p=[least] * 5)
+
+
+def test_large_logits():
+    """Logits far from 0 against their spread, and temperatures that make up for it."""
+    uw = _uw()
+    rng = np.random.default_rng(22)
+    M, V = 6, 30000
+    x = (rng.standard_normal((M, V)) * np.array([[1e6], [3e30], [1e-30], [1.0], [100.0], [1e-3]])).astype(np.float32)
+    x[3] += np.float32(2e5)
+    T = [1e6, 1e30, 1e-30, 1.0, 0.01, 1e-3]
+    for k, p, least in ((0, 1.0, 0.0), (0, 0.9, 0.001), (700, 0.99, 0.0), (50, 0.9, 0.0)):
+        _compare(uw, x, rng.random(M).astype(np.float32), temperature=T, top_k=[k] * M, top_p=[p] * M, min_p=[least] * M)
