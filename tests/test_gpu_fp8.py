@@ -438,3 +438,33 @@ def test_gemm_larger(M, N, K, out):
         log(f"  M={M} N={N} K={K} {out} workspace {0 if ws is None else need}: worst {worst:.3g} of the tolerance")
         assert worst <= 1.0
         assert bool((y[:M, N:] == -77).all()) and bool((y[M] == -77).all()), "outside the matrix"
+
+
+def test_swiglu_over_the_range_of_g():
+    """One value per row, so that the scales tell |h| in fp32. silu is within 2.5 steps of 2^-23, product
+    and scale round by half a step each: 3.5 * 2^-23."""
+    uw, torch = _uw(), torch_cuda()
+    g = np.concatenate([np.linspace(-87, 90, 5000), -np.logspace(-30, 1, 500), np.logspace(-30, 30, 500)]).astype(np.float32)
+    odd = np.array([0.0, -0.0, -100.0, -1e4, -3e38, np.inf, -np.inf, np.nan], np.float32)
+    y = np.zeros((g.size + odd.size, 8), np.float32)
+    y[:, 0], y[:, 4] = np.concatenate([g, odd]), 2.0**30
+    M = y.shape[0]
+    d = torch.from_numpy(y).cuda()
+    q = torch.zeros(M, 16, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(1, M, device="cuda")
+    uw.fp8_swiglu(d, d[:, 4:], q, s, M, 1, ldg=8, ldu=8, ldq=16)
+    sh, qh = s[0].cpu().numpy().astype(np.float64), q[:, 0].cpu().numpy()
+    g64 = g.astype(np.float64)
+    with np.errstate(over="ignore"):
+        h = g64 / (1 + np.exp(-g64)) * 2.0**30
+    fits = np.abs(h) <= np.finfo(np.float32).max  # 10^30 * 2^30 is infinite in fp32: a NaN code, scale 1
+    assert (sh[: g.size][~fits] == 1).all() and (qh[: g.size][~fits] & 0x7F == 0x7F).all()
+    ref = np.maximum(np.abs(h) / 448, 2.0**-126)
+    assert (np.abs(sh[: g.size] - ref) <= 3.5 * 2.0**-23 * ref)[fits].all()
+    big = fits & (np.abs(h) / 448 > 2.0**-125)
+    assert (qh[: g.size][big] == np.where(h[big] < 0, 0xFE, 0x7E)).all()  # +-448 at the scale
+    assert (qh[g.size + np.array([0, 1, 3, 4])] & 0x7F == 0).all() and (qh[g.size + 5 :] & 0x7F == 0x7F).all()
+    # e^-100 is 26.5 of the smallest fp32 steps, known to one of them: a value all the same, and not 0
+    tiny = 100 * np.exp(-100.0) * 2.0**30
+    assert qh[g.size + 2] == 0xFE and abs(sh[g.size + 2] * 448 - tiny) <= tiny / 26
+    assert (sh[g.size + 5 :] == 1).all()
