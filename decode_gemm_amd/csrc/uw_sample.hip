@@ -37,7 +37,13 @@ constexpr double kDeepest = -44.0;     // 2^43 * 2^y rounds to 0 from here down
 constexpr int kList = 4096;            // tokens that are sorted in LDS
 constexpr uint32_t kAim = 256;         // tokens that the gathered beginning of the order has at least
 constexpr uint32_t kCrowd = 255;       // most tokens of a sort bin that are compared with one another
-constexpr int kShort = 512;            // largest k that it is made to hold
+// Largest k that it is made to hold, for `parts` workgroups of nt threads: of s = parts * nt maxima the q-th
+// largest is reached by s ln(s / (s - q)) tokens or so, which leaves three tenths of the list free. (k = 1000
+// of 131072: 1 row 20 us from the list, 51 by counting all tokens; 850 in 256 rows 59 and 87.)
+__host__ __device__ constexpr int64_t short_most(uint32_t parts, int nt)
+{
+    return parts == 1 ? 7 * nt / 8 : parts * nt / 2 < kList / 2 ? parts * nt / 2 : kList / 2;
+}
 constexpr u64 kOne = u64{1} << 43;     // mass of the row's largest token
 
 struct SampleArgs {
@@ -309,12 +315,13 @@ __device__ __forceinline__ void fill_middles(Shared<NT>& S)
 // A row's settings, brought into range.
 struct Row {
     bool by_k, by_p, by_m;
+    bool short_k;  // the beginning of the order answers top-k: then no masses of other tokens are needed
     int64_t k;
     float temp;  // 1 for the greedy choice, which is k = 1
     float p, least, u;
     bool only_first;  // min-p above 1
 
-    __device__ __forceinline__ Row(const SampleArgs& a, int64_t row)
+    __device__ __forceinline__ Row(const SampleArgs& a, int64_t row, int64_t most)
     {
         const float t = a.temperature ? a.temperature[row] : 1.0f;
         const int32_t kk = a.top_k ? a.top_k[row] : 0;
@@ -324,6 +331,7 @@ struct Row {
         temp = greedy ? 1.0f : t;
         k = greedy ? 1 : kk;
         by_k = k > 0 && k < a.V;
+        short_k = by_k && k <= most;
         by_p = p < 1.0f;
         by_m = m > 0.0f && m >= 0x1p-44f;
         only_first = m > 1.0f;
@@ -340,8 +348,6 @@ struct Row {
     __device__ __forceinline__ u64 u_target(u64 m) const { return static_cast<u64>(static_cast<double>(u) * static_cast<double>(m)) + 1; }
     // the least whole mass that min-p keeps
     __device__ __forceinline__ u64 least_mass() const { return static_cast<u64>(ceil(static_cast<double>(least) * static_cast<double>(kOne))); }
-    // whether the beginning of the order answers top-k: then no masses of other tokens are needed
-    __device__ __forceinline__ bool short_k() const { return by_k && k <= kShort; }
     __device__ __forceinline__ Scale scale(float top) const { return Scale{top, 1.4426950408889634074 / static_cast<double>(temp)}; }
 };
 
@@ -683,7 +689,7 @@ __device__ __forceinline__ bool cuts_above(const Row& r, const Scale& sc, float 
 __device__ __forceinline__ bool needs_masses(const Row& r, const Scale& sc, float tau)
 {
     if (holds_all(sc, tau)) return false;  // the list answers, or from_row counts for itself
-    if (r.by_k) return !r.short_k();
+    if (r.by_k) return !r.short_k;
     if (r.by_p || !r.by_m) return true;
     return !cuts_above(r, sc, tau, 0.01);  // min-p alone, and its cut lies in the list
 }
@@ -1103,7 +1109,7 @@ __global__ void __launch_bounds__(NT) sample_rows(SampleArgs a)
     __shared__ Shared<NT> S;
     const int64_t row = blockIdx.x;
     const T* const x = static_cast<const T*>(a.x) + row * a.ld;
-    const Row r(a, row);
+    const Row r(a, row, short_most(1, NT));
     float mine = -INFINITY;
     each_if<NT, 32>(
         x, 0, a.V,
@@ -1115,7 +1121,7 @@ __global__ void __launch_bounds__(NT) sample_rows(SampleArgs a)
     const float top = block_max(S, mine);
     if (top == -INFINITY) return write_row(a, row, -1, 0.0f);  // nothing to draw
     const Scale sc = r.scale(top);
-    const bool listed = !r.by_k || r.short_k();
+    const bool listed = !r.by_k || r.short_k;
     // room for the tokens that share the last one's bin
     const float tau = listed ? reached_by(S, mine, sc, r.by_k ? (r.k > 32 ? static_cast<uint32_t>(r.k) : 32u) : kAim) : INFINITY;
     const bool masses = needs_masses(r, sc, tau), counts = masses && !listed;
@@ -1152,7 +1158,7 @@ __global__ void __launch_bounds__(NT) sample_tops(SampleArgs a, RowSpace* space,
     const int64_t row = blockIdx.x / parts;
     const uint32_t part = blockIdx.x % parts;
     const T* const x = static_cast<const T*>(a.x) + row * a.ld;
-    const Row r(a, row);
+    const Row r(a, row, short_most(parts, NT));
     float mine = -INFINITY;
     each_if<NT, 32>(
         x, part_begin(a.V, part, parts), part_begin(a.V, part + 1, parts),
@@ -1163,7 +1169,7 @@ __global__ void __launch_bounds__(NT) sample_tops(SampleArgs a, RowSpace* space,
         [](float, int) {});
     const float top = block_max(S, mine);
     float tau = -INFINITY;
-    const uint32_t aim = r.short_k() ? static_cast<uint32_t>(r.k) + 32 : kAim;
+    const uint32_t aim = r.short_k ? static_cast<uint32_t>(r.k) + 32 : kAim;
     if (top > -INFINITY) tau = reached_by(S, mine, r.scale(top), (aim + parts - 1) / parts);
     if (threadIdx.x == 0) {
         space[row].top[part] = top;
@@ -1186,7 +1192,7 @@ __global__ void __launch_bounds__(NT) sample_parts(SampleArgs a, RowSpace* space
     RowSpace& R = space[row];
     float top = lane < static_cast<int>(parts) ? R.top[lane] : -INFINITY;
     float tau = lane < static_cast<int>(parts) ? R.tau[lane] : INFINITY;
-    const Row r(a, row);
+    const Row r(a, row, short_most(parts, NT));
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
         top = fmaxf(top, __shfl_xor(top, d));
@@ -1199,7 +1205,7 @@ __global__ void __launch_bounds__(NT) sample_parts(SampleArgs a, RowSpace* space
     const Scale sc = r.scale(top);
     // no part had enough tokens: all of them (tau is +inf also where the largest logits are)
     if (tau == INFINITY && top < INFINITY) tau = -INFINITY;
-    const bool listed = !r.by_k || r.short_k();
+    const bool listed = !r.by_k || r.short_k;
     const bool masses = needs_masses(r, sc, tau), counts = masses && !listed;
     clear_bins(S, masses, counts);
     if (masses) fill_middles(S);

@@ -321,7 +321,7 @@ def test_large_k_and_wide_distributions(M, V, dtype):
     u = rng.random(M).astype(np.float32)
     for spread, T in ((3.0, 1.0), (1.0, 1.0), (2.0, 3.0), (0.05, 1.0), (0.0, 1.0)):
         x = (rng.standard_normal((M, V)) * spread).astype(np.float32)
-        for k, p, least in ((600, 1.0, 0.0), (2500, 0.7, 0.0), (V - 1, 0.999, 1e-3), (0, 0.9, 0.0), (0, 1.0, 1e-3), (0, 0.6, 0.02)):
+        for k, p, least in ((600, 1.0, 0.0), (890, 0.9, 0.0), (900, 1.0, 0.001), (2000, 0.95, 0.0), (2500, 0.7, 0.0), (V - 1, 0.999, 1e-3), (0, 0.9, 0.0), (0, 1.0, 1e-3), (0, 0.6, 0.02)):
             _compare(uw, x, u, f"spread {spread}", dtype=dtype, temperature=[T] * M, top_k=[k] * M, top_p=[p] * M, min_p=[least] * M)
 
 
