@@ -353,3 +353,46 @@ def test_large_logits():
     T = [1e6, 1e30, 1e-30, 1.0, 0.01, 1e-3]
     for k, p, least in ((0, 1.0, 0.0), (0, 0.9, 0.001), (700, 0.99, 0.0), (50, 0.9, 0.0)):
         _compare(uw, x, rng.random(M).astype(np.float32), temperature=T, top_k=[k] * M, top_p=[p] * M, min_p=[least] * M)
+
+
+def test_rows_in_parts_in_a_graph():
+    """Several workgroups per row, captured once and replayed on other logits, numbers and settings, on a
+    stream of its own, with eager calls through another workspace in between."""
+    uw, torch = _uw(), torch_cuda()
+    M, V = 4, 50257
+    need = uw.sample_workspace(M, V)
+    assert need > 0
+    gen = torch.Generator("cuda").manual_seed(5)
+    x = torch.zeros(M, V, device="cuda")
+    u, T, p, least = (torch.zeros(M, device="cuda") for _ in range(4))
+    k = torch.zeros(M, dtype=torch.int32, device="cuda")
+    token, again = (torch.zeros(M, dtype=torch.int32, device="cuda") for _ in range(2))
+    prob = torch.zeros(M, device="cuda")
+    ws = torch.full((2, need), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def call(tok, w):
+        uw.sample(x, u, tok, M, V, d_temperature=T, d_top_k=k, d_top_p=p, d_min_p=least, d_prob=prob, d_ws=w, ws_bytes=need)
+
+    call(token, ws[0])
+    torch.cuda.synchronize()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        call(token, ws[0])
+    for spread, kk, pp, mm in ((3.0, 0, 1.0, 0.0), (1.0, 0, 0.9, 0.0), (4.0, 60, 0.95, 0.0), (1.0, 3000, 0.8, 0.001), (2.0, 0, 1.0, 0.02)):
+        x.copy_(torch.randn(M, V, device="cuda", generator=gen) * spread)
+        u.copy_(torch.rand(M, device="cuda", generator=gen))
+        T.copy_(torch.tensor([0.0, 0.7, 1.0, 1.6]))
+        k.fill_(kk)
+        p.fill_(pp)
+        least.fill_(mm)
+        token.fill_(-7)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graph.replay()
+            graph.replay()
+        torch.cuda.synchronize()
+        call(again, ws[1])
+        l = x.double().cpu().numpy()
+        for m in range(M):
+            t, q = _draw(l[m], float(u[m]), float(T[m]), kk, float(p[m]), float(least[m]))
+            assert int(token[m]) == t and int(again[m]) == t and abs(float(prob[m]) - q) <= 2.0**-23 * q + 2.0**-30
