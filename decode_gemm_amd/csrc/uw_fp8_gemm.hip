@@ -442,8 +442,8 @@ __device__ __forceinline__ void wait_transfers()
 // M = 4096, N = 14336, K = 4096 into bf16: 244 to 258 us, 1.87 to 1.97 PFLOP/s with 256 x 256 tiles (278
 // with 256 x 128, 310 with 128 x 128). What bounds it there is power as much as feeding: the same launch
 // takes 230 us on operands that are all zero, 183 us as a timing copy without products and sums, 225 us
-// without transfers. Into fp32 435 us (1.1 PFLOP/s; a bf16 product's rate, whose matrix instruction it
-// takes, with the conversions beside it). Small products are bound by the launch, the pipeline's first
+// without transfers. Into fp32 447 us (1.08 PFLOP/s, a large bf16 product's rate being 1.37: it takes that
+// matrix instruction, and every wave converts the codes of its operands beside it). Small products are bound by the launch, the pipeline's first
 // loads and the joining of K slices: M = 64, N = 4096, K = 14336 into fp32 19.3 us with 128 x 64 tiles and
 // eight slices, about 5 of them joining (30 without slices).
 //
