@@ -77,7 +77,8 @@ __device__ __forceinline__ float row_max16(float a)
 __device__ __forceinline__ float scale_of(float a) { return a == 0.f ? 1.f : fmaxf(a / kTop, FLT_MIN); }
 
 // Eight codes of v / s. The quotient is the correctly rounded one: r = 1 / s is, and one
-// residual step (x - y s, exact in an fma) corrects y = x r by the last bit where it is off
+// residual step (y s - x, exact in an fma) corrects y = x r by the last bit where it is off (taken
+// that way round, +0 for every zero, it leaves a zero its sign)
 // (s >= 2^-126 keeps r finite; only where the residual itself is below the smallest normal
 // number may the quotient's last fp32 bit stay off). Three operations instead of a division's
 // ten. The one rounding to fewer bits is the conversion's, to nearest even.
@@ -87,8 +88,8 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s, float r)
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const float q = v[i] * r;
-        const float e = __builtin_fmaf(-q, s, v[i]);
-        const float t = __builtin_amdgcn_fmed3f(__builtin_fmaf(e, r, q), -kTop, kTop);
+        const float e = __builtin_fmaf(q, s, -v[i]);
+        const float t = __builtin_amdgcn_fmed3f(__builtin_fmaf(-e, r, q), -kTop, kTop);
         y[i] = fabsf(v[i]) <= FLT_MAX ? t : __uint_as_float(0x7FC00000u);
     }
     uint2 o;
@@ -145,8 +146,8 @@ __device__ __forceinline__ float silu(float g)
     const float d = 1.0f + z, low = z - (d - 1.0f), r = __builtin_amdgcn_rcpf(d);
     const float x = g < 0.0f ? g * e : g;
     const float q = x * r;
-    return __builtin_amdgcn_ldexpf(__builtin_fmaf(__builtin_fmaf(-q, low, __builtin_fmaf(-q, d, x)), r, q),
-                                   g < 0.0f ? static_cast<int>(n) : 0);
+    // (the residual's sign as in codes8, for a g of -0)
+    return __builtin_amdgcn_ldexpf(__builtin_fmaf(-__builtin_fmaf(q, low, __builtin_fmaf(q, d, -x)), r, q), g < 0.0f ? static_cast<int>(n) : 0);
 }
 
 struct LoadSwiglu {

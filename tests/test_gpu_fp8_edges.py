@@ -40,3 +40,33 @@ def test_swiglu_down_to_where_silu_ends():
     assert (off <= 1).all()
     assert (qh[~none] == 0xFE).all()  # -448 at the scale
     assert none[g < -110].all() and not none[g > -107].any()
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_zeros_keep_their_sign(dtype, rows):
+    """-0 / s is -0, code 0x80, beside other values and in a group of zeros alone."""
+    uw, torch = _uw(), torch_cuda()
+    K = 384
+    x = np.random.default_rng(1).standard_normal((5, K)).astype(np.float32)
+    x[:, 3::7] = -0.0
+    x[:, 4::7] = 0.0
+    x[:, 128:256:2], x[:, 129:256:2] = 0.0, -0.0
+    d = torch.from_numpy(x).cuda().to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    q = torch.full((5, K), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.zeros((3, 5) if rows == 1 else (1, 3), device="cuda")
+    uw.fp8_quantize(d, q, s, 5, K, block_rows=rows)
+    zero = x == 0
+    assert (q.cpu().numpy()[zero] == np.where(np.signbit(x[zero]), 0x80, 0)).all()
+
+
+def test_swiglu_zeros_keep_their_sign():
+    """silu(-0) is -0, and so is silu of what underflows; the product's sign is that of both."""
+    uw, torch = _uw(), torch_cuda()
+    g = np.tile(np.array([0.0, -0.0, -300.0, 1.0, -1.0, 2.0, 0.0, -0.0], np.float32), 16)
+    u = np.tile(np.array([1.0, 1.0, 1.0, -0.0, -0.0, 3.0, -1.0, -1.0], np.float32), 16)
+    d = [torch.from_numpy(v).cuda().reshape(1, 128) for v in (g, u)]
+    q = torch.full((1, 128), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(1, 1, device="cuda")
+    uw.fp8_swiglu(d[0], d[1], q, s, 1, 128)
+    assert (q[0].cpu().numpy() == np.tile(np.array([0, 0x80, 0x80, 0x80, 0, 0x7E, 0x80, 0], np.uint8), 16)).all()
