@@ -77,10 +77,10 @@ __device__ __forceinline__ float row_max16(float a)
 __device__ __forceinline__ float scale_of(float a) { return a == 0.f ? 1.f : fmaxf(a / kTop, FLT_MIN); }
 
 // Eight codes of v / s. The quotient is the correctly rounded one: r = 1 / s is, and one
-// residual step (y s - x, exact in an fma) corrects y = x r by the last bit where it is off (taken
-// that way round, +0 for every zero, it leaves a zero its sign)
+// residual step (y s - x, exact in an fma) corrects y = x r by the last bit where it is off
 // (s >= 2^-126 keeps r finite; only where the residual itself is below the smallest normal
-// number may the quotient's last fp32 bit stay off). Three operations instead of a division's
+// number may the quotient's last fp32 bit stay off). Taken that way round the residual of a zero
+// is +0, and the zero keeps its sign. Three operations instead of a division's
 // ten. The one rounding to fewer bits is the conversion's, to nearest even.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s, float r)
 {

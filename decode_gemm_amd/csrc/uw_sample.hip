@@ -430,7 +430,9 @@ __device__ __forceinline__ float below_bin(const Scale& sc, int b)
 __device__ __forceinline__ float above_bin(const Scale& sc, int b)
 {
     if (b == 0) return INFINITY;
-    const float t = below_bin(sc, b - 1);
+    // (-inf where a bin ends within the margin of the lowest number: kept from becoming NaN, which no logit
+    // would reach; the logits there are then looked at for more bins than their own)
+    const float t = fmaxf(below_bin(sc, b - 1), -FLT_MAX);
     return t + fabsf(t) * 0x1p-20f + fabsf(sc.top) * 0x1p-46f + 3 * FLT_MIN;
 }
 
