@@ -471,7 +471,8 @@ def fp8_gemm(d_x, d_sx, d_w, d_sw, d_y, M: int, N: int, K: int, ldx: int | None 
              ldw: int | None = None, ldsw: int | None = None, ldy: int | None = None, y_type: int | None = None,
              d_ws=None, ws_bytes: int = 0, stream=None) -> None:
     """uw_fp8_gemm: Y [M][N] (fp32 or bf16, by the dtype of d_y unless y_type is given) from codes and
-    scales of X and W. d_ws: fp8_gemm_workspace(M, N, K) bytes; without it K is never cut."""
+    scales of X and W. d_ws: fp8_gemm_workspace(M, N, K) bytes; with fewer K is cut into fewer slices,
+    without it never."""
     a = Fp8GemmArgs(M, N, K, _ptr(d_x), K if ldx is None else ldx, _ptr(d_sx), M if ldsx is None else ldsx, _ptr(d_w),
                     K if ldw is None else ldw, _ptr(d_sw), (K + 127) // 128 if ldsw is None else ldsw, _ptr(d_y),
                     N if ldy is None else ldy, _type(d_y, y_type), _ptr(d_ws), ws_bytes)

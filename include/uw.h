@@ -515,10 +515,11 @@ uw_status uw_fp8_swiglu(const float* d_g, int64_t ldg, const float* d_u, int64_t
  * Results do not depend on the run: no atomics, and the order of every sum is fixed by M, N, K
  * and the workspace given. Rows and columns of Y outside M x N are left as they are.
  * Workspace: with d_ws of uw_fp8_gemm_workspace(M, N, K) bytes (16-byte aligned) shapes with
- * few output tiles cut K into slices whose partial sums meet there; with d_ws NULL or
- * ws_bytes smaller they run in one slice (correct, slower). It is free again when the call's
- * work is done; calls that overlap need one each. uw_fp8_gemm_workspace is 0 for arguments
- * that uw_fp8_gemm refuses and where no slices are cut.
+ * few output tiles cut K into slices whose partial sums meet there; with fewer bytes they cut
+ * fewer slices, or none, as with d_ws NULL (correct, slower; other last bits). Nothing past
+ * ws_bytes is touched. It is free again when the call's work is done; calls that overlap need
+ * one each. uw_fp8_gemm_workspace is 0 for arguments that uw_fp8_gemm refuses and where no
+ * slices are cut.
  * Errors: UW_ESHAPE (M < 0, N or K < 1), UW_EINVAL (NULL or misaligned pointers: codes and Y
  * 16 bytes, scales 4; leading dimensions; an unknown type), UW_EUNSUPPORTED (a leading
  * dimension of 2^24 bytes or more, M, N or K of 2^31 or more, an M x N of more tiles than one

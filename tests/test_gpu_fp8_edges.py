@@ -70,3 +70,76 @@ def test_swiglu_zeros_keep_their_sign():
     s = torch.zeros(1, 1, device="cuda")
     uw.fp8_swiglu(d[0], d[1], q, s, 1, 128)
     assert (q[0].cpu().numpy() == np.tile(np.array([0, 0x80, 0x80, 0x80, 0, 0x7E, 0x80, 0], np.uint8), 16)).all()
+
+
+def _up(n, m):
+    return (n + m - 1) // m * m
+
+
+def _exact_operands(M, N, K, seed):
+    """Codes of which every group sum is exact in the matrix unit whichever product it takes, and scales of
+    all sizes. The codes' values are 0 or 1 to 15/8 in steps of 1/8 with either sign: products are multiples of
+    1/64 below 4, so 128 of them need 15 bits and no bit lies below 2^-8 of the largest product. Padding holds
+    NaN codes. Returns ld and (codes, scales, values [n][K] in 64 bits without scales) of X and W."""
+    torch = torch_cuda()
+    gen = torch.Generator("cuda").manual_seed(seed)
+    G, ld = -(-K // 128), _up(K, 16)
+    out = []
+    for n, rows in ((M, 1), (N, 128)):
+        v = 1 + torch.randint(0, 8, (n, K), device="cuda", generator=gen) / 8.0
+        v *= torch.randint(-1, 2, (n, K), device="cuda", generator=gen)
+        q = torch.full((n, ld), 0x7F, dtype=torch.uint8, device="cuda")
+        q[:, :K] = v.to(torch.float8_e4m3fn).view(torch.uint8)
+        s = torch.exp(torch.randn((G, n) if rows == 1 else (-(-n // 128), G), device="cuda", generator=gen))
+        out.append((q, s, v.double()))
+    return ld, out[0], out[1]
+
+
+def _exact_product(M, N, K, x, w):
+    """Y in 64 bits, and the sum of the magnitudes of the groups' terms."""
+    torch = torch_cuda()
+    (_, sx, xv), (_, sw, wv) = x, w
+    y = torch.zeros(M, N, dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(y)
+    for g in range(-(-K // 128)):
+        k = slice(128 * g, min(K, 128 * g + 128))
+        t = xv[:, k] @ wv[:, k].t().contiguous()
+        t *= sx[g].double()[:, None]
+        t *= sw[:, g].double().repeat_interleave(128)[:N][None, :]
+        y += t
+        mag += t.abs_()
+    return y, mag
+
+
+def _check_exact(y, ref, mag, K, slices, what):
+    """The group sums being exact, what is left is the product of the scales, a group's fma and the waves'
+    and slices' additions (16 of each at most), half a step of 2^-23 each and counted whole, and for bf16 the
+    one rounding, 2^-8."""
+    torch = torch_cuda()
+    tol = (2 + -(-K // 128) + 16 + slices) * 2.0**-23 * mag
+    if y.dtype == torch.bfloat16:
+        tol = tol + 2.0**-8 * (ref.abs() + tol)
+    off = (y.double() - ref).abs()
+    worst = float((off / tol.clamp(min=1e-300)).max())
+    log(f"  {what}: worst {worst:.3g} of the tolerance")
+    assert worst <= 1.0, what
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 4096, 14336), (100, 183, 12518), (2050, 257, 9000)])
+def test_gemm_with_part_of_the_workspace(M, N, K):
+    """Less workspace than uw_fp8_gemm_workspace gives fewer slices: right results, the same for every call, and
+    nothing written past the bytes given."""
+    uw, torch = _uw(), torch_cuda()
+    need = uw.fp8_gemm_workspace(M, N, K)
+    assert need > 0
+    ld, x, w = _exact_operands(M, N, K, 5)
+    ref, mag = _exact_product(M, N, K, x, w)
+    for dt in (torch.float32, torch.bfloat16):
+        for given in sorted({0, 15, need // 16, need // 4, 3 * need // 8, need // 2, 5 * need // 8, need - 1, need, need + 4096}):
+            ws = torch.full((_up(given, 16) + 4096,), 0xEE, dtype=torch.uint8, device="cuda")
+            y = [torch.zeros(M, N, dtype=dt, device="cuda") for _ in range(2)]
+            for i in range(2):
+                uw.fp8_gemm(x[0], x[1], w[0], w[1], y[i], M, N, K, ldx=ld, ldw=ld, d_ws=ws, ws_bytes=given)
+            assert bool((ws[given:] == 0xEE).all()), f"{given} of {need} bytes given, written past them"
+            assert torch.equal(y[0], y[1])
+            _check_exact(y[0], ref, mag, K, 16, f"{M}x{N}x{K} {dt} {given} of {need}")
