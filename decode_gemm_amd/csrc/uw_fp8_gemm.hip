@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(64 * WN * WM) fp8_tile(F8Args a)
 {
     using T = Tile<BN, BM, WN, WM>;
     constexpr int TN = T::TN, TM = T::TM, F = TN - P, NL = T::NL;
-    static_assert(F >= 1 && P >= 1 && NST >= 2, "W tiles before and behind the barrier");
+    static_assert(P >= 1 && F >= P && NST >= 2, "W tiles before and behind the barrier");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const T t(a);
     const uint32_t steps = t.steps, lds0 = lds_offset(lds);
@@ -519,10 +519,6 @@ __global__ void __launch_bounds__(64 * WN * WM) fp8_tile(F8Args a)
                 d[c] = e;
             }
             __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (F < P) {
-#pragma unroll
-            for (int i = 0; i < P - F; i++) ar[i] = t.wfrag(S, F + i);
         }
         if (NST > 2 && j + NST - 1 < steps)
             wait_transfers<(NST > 2 ? NST - 2 : 0) * NL>();
