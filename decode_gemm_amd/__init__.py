@@ -23,8 +23,8 @@ __all__ = [
     "expand_direct", "split_count", "run_pipeline_noalloc", "noalloc_scratch_bytes", "bundle_write", "bundle_open",
     "bundle_items", "bundle_plans", "load_bundle", "variant_by_name",
     "DERR_BADCODE", "DERR_CHUNKLEN", "DERR_RAWINDEX", "STATUS", "Proj", "MlpLayer", "proj", "mlp_layers", "mlp_stack_workspace",
-    "mlp_stack_forward", "F32", "BF16", "fp8_quantize", "fp8_swiglu", "fp8_gemm", "fp8_gemm_workspace", "sample",
-    "sample_workspace",
+    "mlp_stack_forward", "F32", "BF16", "fp8_quantize", "fp8_swiglu", "fp8_gemm", "fp8_gemm_workspace", "fp8_gemm_plan",
+    "Fp8Plan", "sample", "sample_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libuw.so")
@@ -122,6 +122,11 @@ class Fp8GemmArgs(ctypes.Structure):
         ("ldw", ctypes.c_int64), ("d_sw", ctypes.c_void_p), ("ldsw", ctypes.c_int64), ("d_y", ctypes.c_void_p),
         ("ldy", ctypes.c_int64), ("y_type", ctypes.c_int32), ("d_ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
     ]
+
+
+class Fp8Plan(ctypes.Structure):
+    """uw_fp8_plan: how an 8-bit product of given sizes runs."""
+    _fields_ = [("tile_n", ctypes.c_int32), ("tile_m", ctypes.c_int32), ("slices", ctypes.c_int32), ("exact", ctypes.c_int32)]
 
 
 class SampleArgs(ctypes.Structure):
@@ -223,6 +228,7 @@ def _load():
         "uw_fp8_swiglu": ([P, i64, P, i64, i64, i64, P, i64, P, i64, P], ctypes.c_int),
         "uw_fp8_gemm": ([ctypes.POINTER(Fp8GemmArgs), P], ctypes.c_int),
         "uw_fp8_gemm_workspace": ([i64, i64, i64], sz),
+        "uw_fp8_gemm_plan": ([i64, i64, i64, i32, sz, ctypes.POINTER(Fp8Plan)], ctypes.c_int),
         "uw_sample": ([ctypes.POINTER(SampleArgs), P], ctypes.c_int),
         "uw_sample_workspace": ([i64, i64], sz),
     }
@@ -465,6 +471,13 @@ def fp8_swiglu(d_g, d_u, d_q, d_s, M: int, K: int, ldg: int | None = None, ldu: 
 
 def fp8_gemm_workspace(M: int, N: int, K: int) -> int:
     return lib.uw_fp8_gemm_workspace(M, N, K)
+
+
+def fp8_gemm_plan(M: int, N: int, K: int, y_type: int, ws_bytes: int = 0) -> Fp8Plan:
+    """uw_fp8_gemm_plan: output tile, K slices and kind of inner sums of fp8_gemm for these sizes."""
+    out = Fp8Plan()
+    _check(lib.uw_fp8_gemm_plan(M, N, K, y_type, ws_bytes, ctypes.byref(out)))
+    return out
 
 
 def fp8_gemm(d_x, d_sx, d_w, d_sw, d_y, M: int, N: int, K: int, ldx: int | None = None, ldsx: int | None = None,

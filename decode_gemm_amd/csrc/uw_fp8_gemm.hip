@@ -745,14 +745,21 @@ bool gemm_sizes_ok(int64_t M, int64_t N, int64_t K)
            (M + 15) / 16 * ((N + 15) / 16) <= INT32_MAX;  // the smallest tiles are 16 x 16
 }
 
+uw_status check_sizes(int64_t M, int64_t N, int64_t K, int32_t y_type)
+{
+    if (M < 0 || N < 1 || K < 1) return fail(UW_ESHAPE, "bad shape M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
+    if (!gemm_sizes_ok(M, N, K)) return fail(UW_EUNSUPPORTED, "M, N or K too large");
+    if (y_type != UW_F32 && y_type != UW_BF16) return fail(UW_EINVAL, "bad y_type %d", y_type);
+    return UW_OK;
+}
+
+size_t usable_workspace(size_t bytes) { return bytes < kWorkspaceMost ? bytes : kWorkspaceMost; }
+
 uw_status check_gemm(const uw_fp8_gemm_args* p)
 {
     if (!p) return fail(UW_EINVAL, "NULL argument");
-    if (p->M < 0 || p->N < 1 || p->K < 1)
-        return fail(UW_ESHAPE, "bad shape M=%lld N=%lld K=%lld", (long long)p->M, (long long)p->N, (long long)p->K);
-    if (!gemm_sizes_ok(p->M, p->N, p->K)) return fail(UW_EUNSUPPORTED, "M, N or K too large");
-    if (p->y_type != UW_F32 && p->y_type != UW_BF16) return fail(UW_EINVAL, "bad y_type %d", p->y_type);
-    if (p->M == 0) return UW_OK;
+    const uw_status st = check_sizes(p->M, p->N, p->K, p->y_type);
+    if (st != UW_OK || p->M == 0) return st;
     if (!p->d_x || !p->d_sx || !p->d_w || !p->d_sw || !p->d_y) return fail(UW_EINVAL, "NULL device pointer");
     if (!aligned(p->d_x, 16) || !aligned(p->d_w, 16) || !aligned(p->d_y, 16))
         return fail(UW_EINVAL, "codes and Y must be 16-byte aligned");
@@ -784,6 +791,19 @@ size_t uw_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K)
     return most;
 }
 
+uw_status uw_fp8_gemm_plan(int64_t M, int64_t N, int64_t K, int32_t y_type, size_t ws_bytes, uw_fp8_plan* out)
+{
+    clear_error();
+    if (!out) return fail(UW_EINVAL, "NULL argument");
+    *out = {};
+    const uw_status st = check_sizes(M, N, K, y_type);
+    if (st != UW_OK || M == 0) return st;
+    const Plan p = plan_for(M, N, K, y_type == UW_BF16, usable_workspace(ws_bytes));
+    if (!p.shape) return fail(UW_EUNSUPPORTED, "M x N too large for one launch");
+    *out = {p.shape->bn, p.shape->bm, static_cast<int32_t>(p.slices), y_type == UW_F32 || p.shape->waves_k > 1};
+    return UW_OK;
+}
+
 uw_status uw_fp8_gemm(const uw_fp8_gemm_args* p, void* stream)
 {
     clear_error();
@@ -806,7 +826,7 @@ uw_status uw_fp8_gemm(const uw_fp8_gemm_args* p, void* stream)
     a.bf16 = p->y_type == UW_BF16;
     a.slices = 1;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const Plan plan = plan_for(a.M, a.N, a.K, a.bf16, p->d_ws ? (p->ws_bytes < kWorkspaceMost ? p->ws_bytes : kWorkspaceMost) : 0);
+    const Plan plan = plan_for(a.M, a.N, a.K, a.bf16, p->d_ws ? usable_workspace(p->ws_bytes) : 0);
     if (!plan.shape) return fail(UW_EUNSUPPORTED, "M x N too large for one launch");
     const hipError_t e = run_plan(a, plan, p->d_ws, s);
     return e == hipSuccess ? UW_OK : fail(UW_EHIP, "GEMM launch failed: %s", hipGetErrorString(e));

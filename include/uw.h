@@ -547,6 +547,19 @@ uw_status uw_fp8_gemm(const uw_fp8_gemm_args* args, void* stream);
 size_t uw_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K);
 
 /*
+ * uw_fp8_gemm_plan (host). What uw_fp8_gemm does for these sizes and this y_type on the current
+ * device, given ws_bytes of workspace (0: NULL). All zero for M = 0. Errors: UW_ESHAPE,
+ * UW_EINVAL (NULL out, an unknown type), UW_EUNSUPPORTED, as those of uw_fp8_gemm.
+ */
+typedef struct {
+    int32_t tile_n, tile_m; /* rows of W and of X per workgroup */
+    int32_t slices;         /* K slices, 1 = not cut */
+    int32_t exact;          /* inner sums: 1 in fp32, 0 by the matrix unit's 8-bit product */
+} uw_fp8_plan;
+
+uw_status uw_fp8_gemm_plan(int64_t M, int64_t N, int64_t K, int32_t y_type, size_t ws_bytes, uw_fp8_plan* out);
+
+/*
  * uw_sample (device). One token per row of logits, e.g. of the Y that the GEMM of a model's
  * output projection writes. Row m, with its own settings:
  *   1. tokens are ordered by logit, the largest first, equal ones by index; w_i = exp((l_i - max) / T)

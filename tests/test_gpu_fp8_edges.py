@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 from tests.gpu_util import log, torch_cuda
+from tests.test_fp8_plans import PLANS, SKINNY, plan_of
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +144,58 @@ def test_gemm_with_part_of_the_workspace(M, N, K):
             assert bool((ws[given:] == 0xEE).all()), f"{given} of {need} bytes given, written past them"
             assert torch.equal(y[0], y[1])
             _check_exact(y[0], ref, mag, K, 16, f"{M}x{N}x{K} {dt} {given} of {need}")
+
+
+def _run_plan(uw, y, slices, M, N, K, ld, x, w, ldx=None, ldw=None):
+    """Y [M][N] by the plan, with rows of Y a little further apart than N, which stay as they are behind it."""
+    torch = torch_cuda()
+    need = uw.fp8_gemm_workspace(M, N, K) if slices > 1 else 0
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda") if need else None
+    out = torch.full((M + 1, N + 3), -77.0, dtype=torch.float32 if y == "f32" else torch.bfloat16, device="cuda")
+    uw.fp8_gemm(x[0], x[1], w[0], w[1], out, M, N, K, ldx=ldx or ld, ldw=ldw or ld, ldy=N + 3, d_ws=ws, ws_bytes=need)
+    assert bool((out[:M, N:] == -77).all()) and bool((out[M] == -77).all()), "outside the matrix"
+    return out[:M, :N]
+
+
+@pytest.mark.parametrize("y,tile,slices,M,N,K", PLANS + [("bf16", (128, 64), 1, 333, 5003, 2000), ("bf16", (256, 256), 1, 2048, 14336, 4096)])
+def test_gemm_of_every_shape(y, tile, slices, M, N, K):
+    """Every kernel shape, in one K slice and in several, K whole groups or not, with operands whose group sums
+    are exact: a scale or a group that is off by more than the output's rounding shows. Then NaN codes
+    and scales, which reach the outputs that they stand for and change no bit of the others."""
+    uw, torch = _uw(), torch_cuda()
+    p = plan_of(y, M, N, K, slices)
+    assert ((p.tile_n, p.tile_m), p.slices) == (tile, slices)
+    ld, x, w = _exact_operands(M, N, K, M + N + K)
+    ref, mag = _exact_product(M, N, K, x, w)
+    clean = _run_plan(uw, y, slices, M, N, K, ld, x, w)
+    _check_exact(clean, ref, mag, K, slices, f"{y} {tile} / {slices}, {M}x{N}x{K}")
+    m, n, G = M // 2, N - 1, -(-K // 128)
+    x[0][m, K - 1] = 0xFF
+    w[0][n, min(K - 1, 7)] = 0x7F
+    x[1][G - 1, M - 1] = float("nan")
+    w[1][0, G // 2] = float("nan")  # the first 128 columns
+    hit = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    hit[m], hit[M - 1], hit[:, n], hit[:, :128] = True, True, True, True
+    got = _run_plan(uw, y, slices, M, N, K, ld, x, w)
+    assert torch.equal(torch.isnan(got), hit)
+    assert torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("y,tile,slices,M,N,K", [p for p in PLANS if p[1] not in SKINNY and p[5] % 128 and p[3] + p[4] < 6000])
+def test_tiles_of_rows_past_32_bits(y, tile, slices, M, N, K):
+    """The tile kernels take a row's place in its tile in 32 bits: rows of X and of W as far apart as they may
+    be (255 of them are just under 2^32 bytes) give the bits that rows side by side give."""
+    uw, torch = _uw(), torch_cuda()
+    ld, x, w = _exact_operands(M, N, K, M)
+    far = (1 << 24) - 16
+    near = _run_plan(uw, y, slices, M, N, K, ld, x, w)
+    for both in (False, True):
+        fx = torch.empty(M, far, dtype=torch.uint8, device="cuda")
+        fx[:, :ld] = x[0]
+        fw, ldw = w[0], ld
+        if both:
+            fw, ldw = torch.empty(N, far, dtype=torch.uint8, device="cuda"), far
+            fw[:, :ld] = w[0]
+        assert torch.equal(_run_plan(uw, y, slices, M, N, K, ld, (fx, x[1]), (fw, w[1]), far, ldw), near)
+        del fx, fw
+        torch.cuda.empty_cache()
