@@ -494,15 +494,32 @@ def fp8_gemm(d_x, d_sx, d_w, d_sw, d_y, M: int, N: int, K: int, ldx: int | None 
 
 def sample_workspace(M: int, V: int) -> int:
     return lib.uw_sample_workspace(M, V)
+def _elements(name: str, t, M: int, whole: bool = False):
+    """Address of an array of M fp32 (whole: int32) numbers, which the kernel reads one after another: other
+    types (torch's default integers, for one) and strided tensors would be misread."""
+    if t is None or isinstance(t, int):
+        return t
+    global _torch
+    if _torch is None:
+        import torch as _torch
+    of = _torch.int32 if whole else _torch.float32
+    if t.dtype is not of or not (M == 1 or t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous tensor of {of}, not of {t.dtype} with strides {t.stride()}")
+    return t.data_ptr()
+
+
 
 
 def sample(d_logits, d_u, d_token, M: int, V: int, ld: int | None = None, type: int | None = None, d_temperature=None,
            d_top_k=None, d_top_p=None, d_min_p=None, d_prob=None, d_ws=None, ws_bytes: int = 0, stream=None) -> None:
     """uw_sample: one token (int32) per row of logits [M][V] (fp32 or bf16, by dtype unless type is
-    given) for the uniform numbers d_u [M]; settings are device arrays of M or None. d_prob (optional)
-    receives the drawn token's probability. d_ws: sample_workspace(M, V) bytes."""
-    a = SampleArgs(M, V, _ptr(d_logits), V if ld is None else ld, _type(d_logits, type), _ptr(d_u), _ptr(d_temperature),
-                   _ptr(d_top_k), _ptr(d_top_p), _ptr(d_min_p), _ptr(d_token), _ptr(d_prob), _ptr(d_ws), ws_bytes)
+    given) for the uniform numbers d_u [M]; settings are device arrays of M (fp32, d_top_k int32) or None.
+    d_prob (fp32, optional) receives the drawn token's probability. d_ws: sample_workspace(M, V) bytes. A
+    ValueError for tensors of other types and strided ones."""
+    a = SampleArgs(M, V, _ptr(d_logits), V if ld is None else ld, _type(d_logits, type), _elements("d_u", d_u, M),
+                   _elements("d_temperature", d_temperature, M), _elements("d_top_k", d_top_k, M, True),
+                   _elements("d_top_p", d_top_p, M), _elements("d_min_p", d_min_p, M), _elements("d_token", d_token, M, True),
+                   _elements("d_prob", d_prob, M), _ptr(d_ws), ws_bytes)
     _launch(d_logits, stream, lib.uw_sample, ctypes.byref(a))
 
 
