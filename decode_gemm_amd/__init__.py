@@ -438,6 +438,8 @@ def _launch(t, stream, call, *args):
     """call(*args, stream) with the device of tensor t current and, without a stream, that device's
     current one. (Two lookups in torch's C layer: at batch size 1 the host's share of a call counts.)"""
     if t is None or isinstance(t, int) or not t.is_cuda:
+        if t is not None and not isinstance(t, int) and not t.is_pinned():
+            raise ValueError("a tensor in host memory that is not pinned: the GPU cannot read it")
         return _check(call(*args, _stream(stream)))
     global _torch
     if _torch is None:
@@ -492,8 +494,6 @@ def fp8_gemm(d_x, d_sx, d_w, d_sw, d_y, M: int, N: int, K: int, ldx: int | None 
     _launch(d_x, stream, lib.uw_fp8_gemm, ctypes.byref(a))
 
 
-def sample_workspace(M: int, V: int) -> int:
-    return lib.uw_sample_workspace(M, V)
 def _elements(name: str, t, M: int, whole: bool = False):
     """Address of an array of M fp32 (whole: int32) numbers, which the kernel reads one after another: other
     types (torch's default integers, for one) and strided tensors would be misread."""
@@ -508,6 +508,8 @@ def _elements(name: str, t, M: int, whole: bool = False):
     return t.data_ptr()
 
 
+def sample_workspace(M: int, V: int) -> int:
+    return lib.uw_sample_workspace(M, V)
 
 
 def sample(d_logits, d_u, d_token, M: int, V: int, ld: int | None = None, type: int | None = None, d_temperature=None,

@@ -40,3 +40,13 @@ def test_what_fits_reaches_the_library():
     with pytest.raises(uw.UwError) as e:
         _sample(d_logits=P + 2, **kw)
     assert e.value.status == uw.EINVAL
+
+
+def test_host_memory_is_refused():
+    x, q, s = torch.zeros(4, 256), torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(2, 4)
+    y = torch.zeros(4, 128)
+    for call in (lambda: uw.fp8_quantize(x, q, s, 4, 256, stream=0), lambda: uw.fp8_swiglu(x, x, q, s, 4, 256, stream=0),
+                 lambda: uw.fp8_gemm(q, s, q, s, y, 4, 128, 256, stream=0),
+                 lambda: _sample(d_logits=torch.zeros(4, 1000), type=None)):
+        with pytest.raises(ValueError, match="host memory"):
+            call()
