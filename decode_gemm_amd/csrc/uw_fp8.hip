@@ -165,7 +165,7 @@ struct LoadSwiglu {
 // reduction and nothing passes through LDS. A workgroup of 256 threads covers ROWS rows x 16 / ROWS
 // groups, one group per 16 lanes: more per thread is slower at every size (2 groups 4%, 4 groups 15%
 // at 4096 x 14336), as the registers then hold fewer waves. HBM-bound: the activation of 4096 x 14336
-// moves 530 MB in 93 us (5.7 TB/s, part of it from the cache behind the L2), bf16 to codes at
+// moves 530 MB in 93 to 95 us (5.6 TB/s, part of it from the cache behind the L2), bf16 to codes at
 // 4096 x 4096 51 MB in 11.2 us.
 template <class Load, int ROWS>
 __global__ void __launch_bounds__(256) quantize_rows(QuantArgs a)
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(256) quantize_rows(QuantArgs a)
 }
 
 // 128 x 128 blocks, one workgroup each: the block stays in registers between the maximum, joined over
-// the waves in LDS, and the codes. HBM-bound: bf16 to codes at 14336 x 4096 moves 176 MB in 38.1 us (4.6
+// the waves in LDS, and the codes. HBM-bound: bf16 to codes at 14336 x 4096 moves 176 MB in 38.0 us (4.6
 // TB/s; 38.8 with 512 threads, 43.2 with 256). A matrix of few blocks waits for one block's loads and
 // barrier: 1000 x 1000 4.1 us, 4.6 with 512 threads, 7.0 with 256.
 constexpr int kBlockThreads = 1024;

@@ -167,8 +167,9 @@ __device__ __forceinline__ void store4(const F8Args& a, int64_t m, int64_t n, co
 // Few rows of X: 16 RT rows of W x 16 CT rows of X per workgroup, whose NW waves take the
 // groups in turn and meet in LDS. Each wave keeps U groups of both operands in flight in registers; many
 // small workgroups serve better than deep queues per wave, as W streams past once and the rest is the
-// launch and the last loads' latency. Bound by HBM, so it takes the exact sums always: M = 1, N = 14336,
-// K = 4096 (59 MB) 14.0 us, 11.4 of them at the rate of a large copy; the same with 16 x 16 tiles 15.0.
+// launch and the last loads' latency. Bound by the stream of W, so it takes the exact sums always: M = 1,
+// N = 14336, K = 4096 (59 MB) takes 14.8 us with W from memory (24 such matrices in turn, 1.4 GB: 4.0 TB/s, where
+// a large copy reaches 5.2 and takes 11.4 us for as much), 14.0 when W stays in the 256 MB cache.
 template <int CT, int RT, int U, int NW>
 __global__ void __launch_bounds__(64 * NW) fp8_skinny(F8Args a)
 {
@@ -440,12 +441,12 @@ __device__ __forceinline__ void wait_transfers()
 }
 
 // M = 4096, N = 14336, K = 4096 into bf16: 244 to 258 us, 1.87 to 1.97 PFLOP/s with 256 x 256 tiles (278
-// with 256 x 128, 310 with 128 x 128). What bounds it there is power as much as feeding: the same launch
-// takes 230 us on operands that are all zero, 183 us as a timing copy without products and sums, 225 us
-// without transfers. Into fp32 447 us (1.08 PFLOP/s, a large bf16 product's rate being 1.37: it takes that
-// matrix instruction, and every wave converts the codes of its operands beside it). Small products are bound by the launch, the pipeline's first
-// loads and the joining of K slices: M = 64, N = 4096, K = 14336 into fp32 19.3 us with 128 x 64 tiles and
-// eight slices, about 5 of them joining (30 without slices).
+// with 256 x 128, 310 with 128 x 128). The matrix cores are busy 96 us of it. No one thing accounts for the rest:
+// the same launch takes 230 us on operands that are all zero (power), and as timing copies 225 us without
+// transfers, 246 without the fmas, 184 without matrix products. Into fp32 446 to 453 us (1.07 PFLOP/s, a
+// large bf16 product's rate being 1.37: it takes that matrix instruction, and every wave converts the codes of
+// its operands beside it). Small products are bound by the launch, the pipeline's first loads and the joining of K slices: M = 64, N = 4096, K = 14336 into fp32 19.3 us with 128 x 64 tiles and
+// eight slices, about 5 of them joining (30 without slices); 23.3 with W from memory.
 //
 // One barrier per step, placed where every fragment of the
 // step is in registers: behind it the stage takes the step NST ahead, and the next step's
@@ -617,7 +618,10 @@ hipError_t launch_tile(const F8Args& a, hipStream_t s)
 //   fixed + max(rounds of workgroups, bytes from HBM, bytes into the CUs) [+ joining K slices]
 // with constants fitted to 22600 launches measured on MI355X (M 1 to 4096, 15 pairs of N and K from
 // 64 to 28672, K slices 1 to 16): over those sizes the shape that the model picks takes 1.6% longer
-// than the fastest one on average, and 8% longer or more for one size in twenty.
+// than the fastest one on average, and 8% longer or more for one size in twenty. The launches took
+// their operands in rotation from 180 MB at most, so W came from the 256 MB cache and `hbm` is the rate from
+// there (17 TB/s where it decided nothing); with W from memory the choice has not been measured. The whole
+// device is meant: on a stream of fewer CUs the choice is the same.
 struct Shape {
     int bn, bm, waves_k;  // rows of W and X per workgroup; waves that share a group out (tiles: 1)
     int per_cu;           // workgroups that fit a CU

@@ -1037,8 +1037,9 @@ struct alignas(16) RowSpace {
 };
 static_assert(sizeof(RowSpace) % 16 == 0, "layout");
 
-// Data that workgroups of one launch hand to another: written through to, and read from, where all of
-// the device sees it.
+// Data that workgroups of one launch hand to another. Atomics of agent scope, so that the compiler marks the
+// accesses (sc1): on gfx950 such a store is written through the XCD's own L2, and such a load does not
+// take what that L2 may hold of an older value.
 template <class U>
 __device__ __forceinline__ void put(U* p, U v)
 {
@@ -1051,9 +1052,12 @@ __device__ __forceinline__ U got(const U* p)
 }
 
 // The part's list (S.n tokens, of which kList at most are there) is added to the row's; true for the
-// workgroup that is the row's last. put() writes through to memory, and every wave's writes are there
-// before its barrier; so the last workgroup finds all of them (a fence would write back the whole
-// L2: with 512 workgroups that took 10 us).
+// workgroup that is the row's last. The order that this needs is gfx950's, not the language's (all atomics here
+// are relaxed): a store that put() made has left the counter vmcnt only when it is where the whole
+// device sees it; every wave waits for that before the barrier, behind which one thread counts the
+// workgroup as arrived; and the last workgroup's got() come behind the barrier that its own count went
+// through. So it finds all that the others put. What they put goes through put() and got() alone. (A release in
+// the language's sense writes back the whole L2, which holds nothing of it: with 512 workgroups 10 us.)
 template <int NT, class T>
 __device__ bool hand_over(Shared<NT>& S, const T* x, RowSpace& R, uint32_t part, uint32_t parts, bool masses)
 {
@@ -1255,9 +1259,12 @@ __global__ void __launch_bounds__(NT) sample_parts(SampleArgs a, RowSpace* space
 }
 
 // How a call is launched: workgroups per row and their threads. With few rows 512 threads pass their
-// barriers sooner (1 row of 131072: 15.5 us, 17.9 with 1024 threads); with more rows 1024 threads and
-// one workgroup for each of 256 CUs win (64 rows of 131072: 44 us, 50 with 512 threads or with two
-// workgroups; 64 rows of 50257: 36, 39 and 49 us). No part has less than 2048 logits.
+// barriers sooner (1 row of 131072: 15.3 us, 17.8 with 1024 threads, 18.7 in one workgroup of those); with more
+// rows 1024 threads and one workgroup for each of 256 CUs do well (64 rows of 131072: 43.5 us, 48.4 with 512
+// threads, 49.5 with two workgroups a row, 52.6 with eight; 64 rows of 50257: 33.5, 32.8, 35.5 and 49.6 us). In
+// between the rule is not the best: 8 rows of 131072 take 42.7 us, with 8 workgroups of 1024 threads each they
+// would take 36.5. No part has less than 2048 logits. The whole device is meant: on a stream of fewer CUs the
+// choice is the same.
 struct Launch {
     uint32_t parts, threads;
 };

@@ -487,7 +487,8 @@ uw_status uw_swiglu(const float* d_g, const float* d_u, int64_t n, uint16_t* d_h
  * uw_fp8_swiglu (device). The activation of uw_swiglu, ending in codes: h = silu(g) * u in
  * fp32 (not rounded to bf16 on the way), quantized as rows. g and u fp32 [M][K] with leading
  * dimensions ldg and ldu (multiples of 4), so that both can be halves of one product with the
- * gate and up weights stacked. d_g, d_u, d_q and d_s must not overlap.
+ * gate and up weights stacked: into fp32, so a bf16 output of uw_fp8_gemm is not taken here. silu
+ * is within 2.5 steps of fp32 over all of its range. d_g, d_u, d_q and d_s must not overlap.
  *
  * Errors: UW_ESHAPE (M < 0, K < 1), UW_EINVAL (NULL or misaligned pointers: 16 bytes, scales
  * 4; a leading dimension too small or not the multiple named; an unknown type or block_rows),
@@ -511,7 +512,9 @@ uw_status uw_fp8_swiglu(const float* d_g, int64_t ldg, const float* d_u, int64_t
  * rows. For fp32 outputs the inner sums are fp32 too. For bf16 outputs at larger M the matrix
  * unit's own 8-bit product takes them, which drops bits below about 2^-18 of a group's
  * largest product (up to 2^-11 of it over a group): below the rounding of the output unless
- * groups cancel. A NaN code or scale reaches the outputs of its own row (or column) only.
+ * groups cancel; which sizes those are uw_fp8_gemm_plan tells. The product of the two scales is
+ * taken first, in fp32, and has to be in its range. A NaN code reaches the outputs of its own row
+ * (or column) only, a NaN scale those of the row or of the 128 columns that it stands for.
  * Results do not depend on the run: no atomics, and the order of every sum is fixed by M, N, K
  * and the workspace given. Rows and columns of Y outside M x N are left as they are.
  * Workspace: with d_ws of uw_fp8_gemm_workspace(M, N, K) bytes (16-byte aligned) shapes with
