@@ -569,7 +569,7 @@ uw_status uw_fp8_gemm_plan(int64_t M, int64_t N, int64_t K, int32_t y_type, size
  *   2. top-k: the first k tokens stay (k <= 0 or k >= V: all)
  *   3. top-p: of these, the shortest beginning stays whose mass (sum of w) is at least p times
  *      the mass of all of them; at least one token (p >= 1: all)
- *   4. min-p: tokens with w_i < min_p leave, the first one never does
+ *   4. min-p: tokens with w_i < min_p leave (compared as masses, below), the first one never does
  *   5. the token drawn is the first in the order whose mass with all before it is more than
  *      u times the mass of what is left
  * d_prob (optional) receives w_token / (mass of what is left). T = 0 takes the first token
