@@ -5,6 +5,7 @@ import pytest
 
 from tests.gpu_util import log, torch_cuda
 from tests.test_fp8_plans import PLANS, SKINNY, plan_of
+from tests.test_gpu_fp8 import _e4m3, _scales, _spread
 
 pytestmark = pytest.mark.gpu
 
@@ -199,3 +200,29 @@ def test_tiles_of_rows_past_32_bits(y, tile, slices, M, N, K):
         assert torch.equal(_run_plan(uw, y, slices, M, N, K, ld, (fx, x[1]), (fw, w[1]), far, ldw), near)
         del fx, fw
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_codes_of_tiny_values(dtype):
+    """Every bf16 value over ten binades beside every largest value of its group, for groups whose scales go from
+    2^-126 to 2^-103: the codes are those of the correctly rounded fp32 quotient, where x is subnormal or the
+    quotient's residual would be, too."""
+    uw, torch = _uw(), torch_cuda()
+    man = np.arange(128, 256) / 128.0
+    e = np.arange(-121, -95)
+    x = np.zeros((128, 10, 2, e.size, 128))  # the group's largest, binades below it, halves of the others, binade of the largest
+    x[..., 0] = (man[:, None] * 2.0**e)[:, None, None, :]
+    v = (man.reshape(2, 64)[None, :, :] * 2.0 ** -np.arange(10)[:, None, None])[None, :, :, None, :] * (2.0**e)[:, None]
+    x[..., 1:65] = np.where(v <= x[..., :1], v, 0)
+    x[..., 65:] = -x[..., 1:64]
+    M, K = 128 * 20, 128 * e.size
+    x = x.reshape(M, K).astype(np.float32)
+    d = torch.from_numpy(x).cuda().to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    x = d.float().cpu().numpy()  # bf16 holds fewer bits of the smallest
+    q = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(K // 128, M, device="cuda")
+    uw.fp8_quantize(d, q, s, M, K)
+    ref = _scales(x, 1)
+    assert (s.cpu().numpy().T == ref).all()
+    off = q.cpu().numpy() != _e4m3(x / _spread(ref, 1, M, K))
+    assert not off.any(), f"{int(off.sum())} of {off.size} codes"
