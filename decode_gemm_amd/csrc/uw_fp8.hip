@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(256) quantize_rows(QuantArgs a)
 }
 
 // 128 x 128 blocks, one workgroup each: the block stays in registers between the maximum, joined over
-// the waves in LDS, and the codes. HBM-bound: bf16 to codes at 14336 x 4096 moves 176 MB in 38.0 us (4.6
+// the waves in LDS, and the codes. HBM-bound: bf16 to codes at 14336 x 4096 moves 176 MB in 37.8 us (4.7
 // TB/s; 38.8 with 512 threads, 43.2 with 256). A matrix of few blocks waits for one block's loads and
 // barrier: 1000 x 1000 4.1 us, 4.6 with 512 threads, 7.0 with 256.
 constexpr int kBlockThreads = 1024;
