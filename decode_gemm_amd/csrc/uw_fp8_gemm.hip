@@ -445,8 +445,9 @@ __device__ __forceinline__ void wait_transfers()
 // the same launch takes 230 us on operands that are all zero (power), and as timing copies 225 us without
 // transfers, 246 without the fmas, 184 without matrix products. Into fp32 446 to 453 us (1.07 PFLOP/s, a
 // large bf16 product's rate being 1.37: it takes that matrix instruction, and every wave converts the codes of
-// its operands beside it). Small products are bound by the launch, the pipeline's first loads and the joining of K slices: M = 64, N = 4096, K = 14336 into fp32 19.3 us with 128 x 64 tiles and
-// eight slices, about 5 of them joining (30 without slices); 23.3 with W from memory.
+// its operands beside it). Small products are bound by the launch, the pipeline's first loads and the joining
+// of K slices: M = 64, N = 4096, K = 14336 into fp32 19.3 us with 128 x 64 tiles and eight slices, about 5 of
+// them joining (30 without slices); 23.3 with W from memory.
 //
 // One barrier per step, placed where every fragment of the
 // step is in registers: behind it the stage takes the step NST ahead, and the next step's
