@@ -24,7 +24,8 @@ __all__ = [
     "bundle_items", "bundle_plans", "load_bundle", "variant_by_name",
     "DERR_BADCODE", "DERR_CHUNKLEN", "DERR_RAWINDEX", "STATUS", "Proj", "MlpLayer", "proj", "mlp_layers", "mlp_stack_workspace",
     "mlp_stack_forward", "F32", "BF16", "fp8_quantize", "fp8_swiglu", "fp8_gemm", "fp8_gemm_workspace", "fp8_gemm_plan",
-    "Fp8Plan", "sample", "sample_workspace",
+    "Fp8Plan", "sample", "sample_workspace", "E4M3", "w4_plane_bytes", "w4_quantize", "w4_expand", "w4_gemm", "w4_gate_up",
+    "w4_gemm_workspace", "NORM_NONE", "NORM_RMS", "NORM_LAYER", "block_norm", "logprobs", "logprobs_workspace",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libuw.so")
@@ -34,7 +35,8 @@ STATUS = {0: "UW_OK", 1: "UW_EINVAL", 2: "UW_ESHAPE", 3: "UW_EFORMAT", 4: "UW_ER
 OK, EINVAL, ESHAPE, EFORMAT, ERANGE, ENOSPACE, EHIP, EUNSUPPORTED, EINTERNAL = range(9)
 W_BF16, W_EXP, W_IDX, W_DIRECT = 0, 1, 2, 3
 PIPE_FULL, PIPE_EXP, PIPE_TRANSCODE, PIPE_DIRECT, PIPE_EXPAND = 0, 1, 2, 3, 4
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 FP8_GROUP = 128
 PIPELINE_NAMES = {0: "full", 1: "exp", 2: "transcode", 3: "direct", 4: "expand"}
 DERR_BADCODE, DERR_CHUNKLEN, DERR_RAWINDEX = 1, 2, 4
@@ -139,6 +141,38 @@ class SampleArgs(ctypes.Structure):
     ]
 
 
+class W4Args(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("group", ctypes.c_int32),
+        ("d_x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("d_plane", ctypes.c_void_p), ("d_up", ctypes.c_void_p),
+        ("d_y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("y_type", ctypes.c_int32), ("d_ws", ctypes.c_void_p),
+        ("ws_bytes", ctypes.c_size_t),
+    ]
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("d_y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+        ("y_type", ctypes.c_int32), ("d_r", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("r_type", ctypes.c_int32),
+        ("d_r_out", ctypes.c_void_p), ("ldr_out", ctypes.c_int64), ("post", ctypes.c_int32), ("pre", ctypes.c_int32),
+        ("d_post_w", ctypes.c_void_p), ("d_post_b", ctypes.c_void_p), ("d_pre_w", ctypes.c_void_p),
+        ("d_pre_b", ctypes.c_void_p), ("d_gate", ctypes.c_void_p), ("gate_rows", ctypes.c_int64),
+        ("ldgate", ctypes.c_int64), ("w_type", ctypes.c_int32), ("w_add", ctypes.c_float), ("scale_y", ctypes.c_float),
+        ("scale_r", ctypes.c_float), ("eps", ctypes.c_float), ("d_h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+        ("h_type", ctypes.c_int32), ("d_s", ctypes.c_void_p), ("lds", ctypes.c_int64),
+    ]
+
+
+class LogprobsArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("V", ctypes.c_int64), ("d_logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+        ("type", ctypes.c_int32), ("d_token", ctypes.c_void_p), ("d_temperature", ctypes.c_void_p),
+        ("d_logprob", ctypes.c_void_p), ("d_rank", ctypes.c_void_p), ("d_entropy", ctypes.c_void_p),
+        ("n_top", ctypes.c_int32), ("d_top_token", ctypes.c_void_p), ("d_top_logprob", ctypes.c_void_p),
+        ("d_ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
+    ]
+
+
 class BundleItem(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("blob", ctypes.c_void_p), ("blob_bytes", ctypes.c_size_t)]
 
@@ -231,6 +265,15 @@ def _load():
         "uw_fp8_gemm_plan": ([i64, i64, i64, i32, sz, ctypes.POINTER(Fp8Plan)], ctypes.c_int),
         "uw_sample": ([ctypes.POINTER(SampleArgs), P], ctypes.c_int),
         "uw_sample_workspace": ([i64, i64], sz),
+        "uw_w4_plane_bytes": ([i64, i64, i32], sz),
+        "uw_w4_quantize": ([P, i32, i64, i64, i64, i32, i32, P, P], ctypes.c_int),
+        "uw_w4_expand": ([P, i64, i64, i32, P, i32, i64, P], ctypes.c_int),
+        "uw_w4_gemm": ([ctypes.POINTER(W4Args), P], ctypes.c_int),
+        "uw_w4_gate_up": ([ctypes.POINTER(W4Args), P], ctypes.c_int),
+        "uw_w4_gemm_workspace": ([i64, i64, i64], sz),
+        "uw_block_norm": ([ctypes.POINTER(BlockNormArgs), P], ctypes.c_int),
+        "uw_logprobs": ([ctypes.POINTER(LogprobsArgs), P], ctypes.c_int),
+        "uw_logprobs_workspace": ([i64, i64, i32], sz),
     }
     for name, (args, res) in sigs.items():
         f = getattr(L, name)
@@ -523,6 +566,125 @@ def sample(d_logits, d_u, d_token, M: int, V: int, ld: int | None = None, type: 
                    _elements("d_top_p", d_top_p, M), _elements("d_min_p", d_min_p, M), _elements("d_token", d_token, M, True),
                    _elements("d_prob", d_prob, M), _ptr(d_ws), ws_bytes)
     _launch(d_logits, stream, lib.uw_sample, ctypes.byref(a))
+
+
+def w4_plane_bytes(N: int, K: int, group: int = 128) -> int:
+    """uw_w4_plane_bytes: bytes of a plane of 4-bit weights; 0 for sizes that the calls refuse."""
+    return lib.uw_w4_plane_bytes(N, K, group)
+
+
+def _plane(name: str, t, N: int, K: int, group: int):
+    """Address of a plane, whose tensor must be as large as the sizes say and in one piece."""
+    if t is None or isinstance(t, int):
+        return t
+    need = lib.uw_w4_plane_bytes(N, K, group)
+    if not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise ValueError(f"{name} must be a contiguous tensor of {need} bytes")
+    return t.data_ptr()
+
+
+def w4_quantize(d_w, d_plane, N: int, K: int, group: int = 128, zeros: bool = False, ldw: int | None = None,
+                w_type: int | None = None, stream=None) -> None:
+    """uw_w4_quantize: the plane (w4_plane_bytes bytes) of W [N][K] in 4 bits with a scale, and with zeros a zero
+    point, per group of 32, 64 or 128 values of a row."""
+    _launch(d_w, stream, lib.uw_w4_quantize, _ptr(d_w), _type(d_w, w_type), N, K, K if ldw is None else ldw, group, int(zeros),
+            _plane("d_plane", d_plane, N, K, group))
+
+
+def w4_expand(d_plane, d_w, N: int, K: int, group: int = 128, ldw: int | None = None, w_type: int | None = None,
+              stream=None) -> None:
+    """uw_w4_expand: the values of a plane as W [N][K] (fp32, exact, or bf16, by the dtype of d_w unless w_type is given)."""
+    _launch(d_w, stream, lib.uw_w4_expand, _plane("d_plane", d_plane, N, K, group), N, K, group, _ptr(d_w), _type(d_w, w_type),
+            K if ldw is None else ldw)
+
+
+def w4_gemm_workspace(M: int, N: int, K: int) -> int:
+    return lib.uw_w4_gemm_workspace(M, N, K)
+
+
+def w4_gemm(d_x, d_plane, d_y, M: int, N: int, K: int, group: int = 128, ldx: int | None = None, ldy: int | None = None,
+            y_type: int | None = None, d_ws=None, ws_bytes: int = 0, stream=None) -> None:
+    """uw_w4_gemm: Y [M][N] (fp32 or bf16, by the dtype of d_y unless y_type is given) = X W^T, X bf16 [M][K], W a plane
+    of 4-bit weights. d_ws: w4_gemm_workspace(M, N, K) bytes; with fewer K is cut into fewer slices, without it never."""
+    a = W4Args(M, N, K, group, _bf16("d_x", d_x), K if ldx is None else ldx, _plane("d_plane", d_plane, N, K, group), None, _ptr(d_y),
+               N if ldy is None else ldy, _type(d_y, y_type), _ptr(d_ws), ws_bytes)
+    _launch(d_x, stream, lib.uw_w4_gemm, ctypes.byref(a))
+
+
+def w4_gate_up(d_x, d_gate, d_up, d_h, M: int, N: int, K: int, group: int = 128, ldx: int | None = None,
+               ldh: int | None = None, d_ws=None, ws_bytes: int = 0, stream=None) -> None:
+    """uw_w4_gate_up: h [M][N] (bf16) = silu(X Wg^T) * (X Wu^T), both weights planes of N x K with the same group. d_ws:
+    w4_gemm_workspace(M, 2 * N, K) bytes, as for w4_gemm."""
+    a = W4Args(M, N, K, group, _bf16("d_x", d_x), K if ldx is None else ldx, _plane("d_gate", d_gate, N, K, group),
+               _plane("d_up", d_up, N, K, group), _bf16("d_h", d_h), N if ldh is None else ldh, BF16, _ptr(d_ws), ws_bytes)
+    _launch(d_x, stream, lib.uw_w4_gate_up, ctypes.byref(a))
+
+
+def _bf16(name: str, t):
+    """Address of bf16 values; a tensor of another type would be misread."""
+    if t is None or isinstance(t, int):
+        return t
+    if _type(t, None) != BF16:
+        raise ValueError(f"{name} must be bf16, not {t.dtype}")
+    return t.data_ptr()
+
+
+def block_norm(d_y, d_r, d_r_out, M: int, K: int, d_h=None, d_q=None, d_s=None, post: int = NORM_RMS, d_post_w=None,
+               d_post_b=None, pre: int = NORM_RMS, d_pre_w=None, d_pre_b=None, d_gate=None, gate_rows: int = 0,
+               scale_y: float = 1.0, scale_r: float = 1.0, w_add: float = 0.0, eps: float = 1e-6, ldy: int | None = None,
+               ldr: int | None = None, ldr_out: int | None = None, ldh: int | None = None, lds: int | None = None,
+               ldgate: int | None = None, y_type: int | None = None, r_type: int | None = None, w_type: int | None = None,
+               h_type: int | None = None, stream=None) -> None:
+    """uw_block_norm: r' = scale_r r + scale_y gate post(y) into d_r_out, and pre(r') into d_h (fp32 or bf16) or, as e4m3
+    codes with row scales, into d_q and d_s (ldh is then that of d_q). d_y, d_r, d_r_out and d_h / d_q may be None. Types
+    follow the tensors unless given; d_r and d_r_out have one, and weights, biases and gate have one."""
+    if d_h is not None and d_q is not None:
+        raise ValueError("d_h and d_q: h is either values or codes")
+    vectors = [v for v in (d_post_w, d_post_b, d_pre_w, d_pre_b, d_gate) if v is not None]
+
+    def kind(name, given, *tensors):
+        types = {_type(t, None) for t in tensors if t is not None and not isinstance(t, int)} if given is None else {given}
+        if len(types) > 1:
+            raise ValueError(f"{name}: tensors of different types")
+        if not types and any(t is not None for t in tensors):
+            _type(None, None)
+        return types.pop() if types else F32
+
+    for name, v in (("d_post_w", d_post_w), ("d_post_b", d_post_b), ("d_pre_w", d_pre_w), ("d_pre_b", d_pre_b)):
+        if v is not None and not isinstance(v, int) and v.stride(-1) != 1 and K > 1:
+            raise ValueError(f"{name} must have its values one after another")
+    h = d_h if d_q is None else d_q
+    if d_q is not None:
+        h_type = E4M3
+        if not isinstance(d_q, int) and d_q.element_size() != 1:
+            raise ValueError(f"d_q must hold bytes, not {d_q.dtype}")
+    a = BlockNormArgs(
+        M, K, _ptr(d_y), K if ldy is None else ldy, kind("d_y", y_type, d_y), _ptr(d_r), K if ldr is None else ldr,
+        kind("d_r and d_r_out", r_type, d_r, d_r_out), _ptr(d_r_out), K if ldr_out is None else ldr_out, post, pre, _ptr(d_post_w),
+        _ptr(d_post_b), _ptr(d_pre_w), _ptr(d_pre_b), _ptr(d_gate), gate_rows, K if ldgate is None else ldgate,
+        kind("weights, biases and gate", w_type, *vectors), w_add, scale_y, scale_r, eps, _ptr(h), K if ldh is None else ldh,
+        kind("d_h", h_type, h), _ptr(d_s), M if lds is None else lds)
+    _launch(d_y if d_y is not None else d_r, stream, lib.uw_block_norm, ctypes.byref(a))
+
+
+def logprobs_workspace(M: int, V: int, n_top: int = 0) -> int:
+    return lib.uw_logprobs_workspace(M, V, n_top)
+
+
+def logprobs(d_logits, M: int, V: int, d_token=None, d_logprob=None, d_rank=None, d_entropy=None, n_top: int = 0,
+             d_top_token=None, d_top_logprob=None, d_temperature=None, ld: int | None = None, type: int | None = None,
+             d_ws=None, ws_bytes: int = 0, stream=None) -> None:
+    """uw_logprobs: per row of logits [M][V] (fp32 or bf16) the log probability (fp32 [M]) and rank (int32 [M]) of d_token
+    (int32 [M]), the entropy (fp32 [M]) and the n_top first tokens (int32 [M][n_top]) with their log probabilities (fp32). Each
+    output may be None. d_ws: logprobs_workspace(M, V, n_top) bytes. A ValueError for tensors of other types and strided ones."""
+    if n_top == 0:  # empty tensors are no lists
+        d_top_token = d_top_logprob = None
+    a = LogprobsArgs(M, V, _ptr(d_logits), V if ld is None else ld, _type(d_logits, type), _elements("d_token", d_token, M, True),
+                     _elements("d_temperature", d_temperature, M), _elements("d_logprob", d_logprob, M),
+                     _elements("d_rank", d_rank, M, True), _elements("d_entropy", d_entropy, M), n_top,
+                     _elements("d_top_token", d_top_token, M * n_top, True), _elements("d_top_logprob", d_top_logprob, M * n_top),
+                     _ptr(d_ws), ws_bytes)
+    _launch(d_logits, stream, lib.uw_logprobs, ctypes.byref(a))
 
 
 def proj(h: Header, d_blob, pipeline: int = PIPE_DIRECT, d_direct=None, variant: int = -1, split_k: int = 0) -> Proj:

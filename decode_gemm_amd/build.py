@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "libuw.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
-HIP_SOURCES = ["uw_decode.hip", "uw_gemm.hip", "uw_runtime.hip", "uw_fp8.hip", "uw_fp8_gemm.hip", "uw_sample.hip"]
+HIP_SOURCES = ["uw_decode.hip", "uw_gemm.hip", "uw_runtime.hip", "uw_fp8.hip", "uw_fp8_gemm.hip", "uw_sample.hip", "uw_w4.hip",
+               "uw_norm.hip", "uw_logprobs.hip"]
 HOST_SOURCES = ["uw_host.cpp", "uw_bundle.cpp"]
 # Packed fp32 VALU forms are kept out of the generated code.
 HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang",

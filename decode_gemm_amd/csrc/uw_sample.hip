@@ -20,6 +20,7 @@
 #include <cmath>
 
 #include "uw_internal.h"
+#include "uw_order.h"
 #include "uw_recon.h"
 
 namespace uw {
@@ -28,8 +29,6 @@ namespace {
 
 // A token's mass is worked out in several places and has to come out the same in all of them.
 #pragma clang fp contract(off)
-
-typedef unsigned long long u64;
 
 constexpr int kBins = 2048;            // 46 per unit of y: the 44 units that have mass fill 2025 of them
 constexpr double kBinsPerUnit = 46.0, kUnitPerBin = 1.0 / 46.0;
@@ -58,9 +57,6 @@ struct SampleArgs {
     int32_t* token;
     float* prob;
 };
-
-__device__ __forceinline__ float value(const float* x, int i) { return x[i]; }
-__device__ __forceinline__ float value(const uint16_t* x, int i) { return __uint_as_float(static_cast<uint32_t>(x[i]) << 16); }
 
 // Adding kRound to a double of less than 2^31 leaves its nearest whole number in the low 32 bits: two
 // additions in place of a rounding and a conversion, which take four times an addition's time each.
@@ -123,16 +119,6 @@ struct Scale {
         return l == top ? 0.0 : (static_cast<double>(l) - static_cast<double>(top)) * c;
     }
 };
-
-// Sort key of (logit, index): ascending keys are the order. -0 and +0 are equal logits.
-__device__ __forceinline__ uint32_t order_bits(float l)
-{
-    const uint32_t b = __float_as_uint(l + 0.0f);
-    return (b & 0x80000000u) ? b : ~(b | 0x80000000u);  // larger logits get smaller bits
-}
-__device__ __forceinline__ float order_value(uint32_t o) { return __uint_as_float((o & 0x80000000u) ? o : ~o & 0x7FFFFFFFu); }
-__device__ __forceinline__ u64 key_of(float l, int i) { return (static_cast<u64>(order_bits(l)) << 32) | static_cast<uint32_t>(i); }
-__device__ __forceinline__ float key_value(u64 key) { return order_value(static_cast<uint32_t>(key >> 32)); }
 
 // Bins in which the answers of a row's questions lie, and the logits of each range of bins (a little
 // widened): 0 top-k, 1 top-p, 2 min-p, 3 the draw.

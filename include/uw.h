@@ -496,7 +496,7 @@ uw_status uw_swiglu(const float* d_g, const float* d_u, int64_t n, uint16_t* d_h
  * must not overlap.
  */
 #define UW_FP8_GROUP 128
-typedef enum { UW_F32 = 0, UW_BF16 = 1 } uw_type;
+typedef enum { UW_F32 = 0, UW_BF16 = 1, UW_E4M3 = 2 /* codes; of uw_block_norm's h only */ } uw_type;
 
 uw_status uw_fp8_quantize(const void* d_x, int32_t x_type, int64_t M, int64_t K, int64_t ldx, int32_t block_rows,
                           uint8_t* d_q, int64_t ldq, float* d_s, int64_t lds, void* stream);
@@ -606,6 +606,173 @@ typedef struct {
 
 uw_status uw_sample(const uw_sample_args* args, void* stream);
 size_t uw_sample_workspace(int64_t M, int64_t V);
+
+/*
+ * 4-bit weights: projections that may lose more than 8-bit codes do. W [N][K] is kept as codes q of
+ * 4 bits with a scale s (fp32 with 20 significant bits) and a zero point z (0..15) for each group of
+ * `group` (32, 64 or 128) values of a row, the last one of a row possibly short; a code stands for
+ * s * (q - z), which is exact in fp32. K is any positive number.
+ *
+ * Plane (uw_w4_plane_bytes bytes, 16-byte aligned): N in T = ceil(N / 16) row tiles, K in J = ceil(K / 128)
+ * tiles. First 1024 bytes of codes for each (t, j), at 1024 * (t * J + j): the little-endian 32-bit word
+ * 4 * (16 * c + r) + p holds the codes of row 16 t + r, k = 128 j + 32 p + 8 c + e for e = 0..7, code e in bits
+ * 4 * (e / 2) + 16 * (e % 2) and up. Then, from 1024 * T * J on, one 32-bit word for each group of a tile and
+ * row, word ((t * J + j) * (128 / group) + g) * 16 + r: the bits of s, whose lowest four are 0, with z there.
+ * Codes and words for rows past N and groups that begin past K are 0. A caller with weights quantized
+ * elsewhere (fp16 and bf16 scales fit s exactly) may fill a plane itself.
+ *
+ * uw_w4_quantize (device). The plane of W (w_type UW_BF16 or UW_F32, ldw elements between 16-byte aligned
+ * rows: a multiple of 8 for bf16, 4 for fp32). Per group, all in exact arithmetic, rounding to nearest even:
+ *   zeros = 0  z = 8, s = max(a / 7, 2^-126) rounded to 20 bits, a the largest |w| (s = 1 where a = 0),
+ *              q = 8 + w / s rounded
+ *   zeros = 1  lo = the least w or 0, hi = the largest or 0; s = max((hi - lo) / 15, 2^-126) rounded to
+ *              20 bits (1 where hi = lo; hi - lo and the quotient in fp64), z = -lo / s rounded, at most 15, and
+ *              q = w / s rounded + z, held at 0..15
+ * A group with a NaN or an infinity gets the scale NaN: all of it comes out as NaN.
+ *
+ * uw_w4_expand (device). The values of a plane, W [N][K] in w_type (bf16: one rounding), as the plain GEMM of
+ * uw_recon_gemm (UW_W_BF16) takes them for large batches; elements behind K in a row are left as they are.
+ *
+ * uw_w4_gemm (device). Y = X * W^T: X bf16 [M][ldx] (16-byte aligned, ldx a multiple of 8; nothing past K is
+ * read), Y [M][ldy] fp32 or bf16 (y_type; one rounding), by
+ *   Y[m][n] = sum over groups g of  s[n][g] * (sum over k in g of x[m][k] q[n][k]  -  z[n][g] * sum over k in g of x[m][k])
+ * with every sum in fp32 and no weight rounded. (The matrix unit takes 1 + q / 16 for q, so that a row's outputs
+ * are NaN where it holds an infinity or a NaN.) Made for few rows, where W's bytes bound it; larger M runs in blocks
+ * of 64 rows that read W again, right but, from a few hundred rows on, slower than uw_w4_expand and
+ * uw_recon_gemm.
+ *
+ * uw_w4_gate_up (device). h = bf16(silu(X Wg^T) * (X Wu^T)) [M][ldh], both planes N x K with the same group: the
+ * two products and the activation of uw_swiglu in one pass over X, the products not rounded on the way.
+ *
+ * Results of both do not depend on the run (no atomics; the order of every sum is fixed by M, N, K, group and the
+ * workspace given). Rows and columns outside M x N are left as they are. Workspace: with d_ws of
+ * uw_w4_gemm_workspace(M, N, K) bytes (uw_w4_gate_up: of 2 N; 16-byte aligned) shapes with few row tiles cut K into slices whose
+ * partial sums meet there; with fewer bytes, or NULL, they cut fewer or none (right, slower, other last bits). It is free again
+ * when the call's work is done; calls that overlap need one each.
+ * Errors: UW_ESHAPE (M < 0, N or K < 1), UW_EINVAL (NULL or misaligned pointers: 16 bytes; d_y and d_h only that of
+ * their elements; a leading dimension too small or not the multiple named; an unknown type or group; zeros not 0 or 1),
+ * UW_EUNSUPPORTED (N or K over 2^24, M over 2^31 - 1, more than one launch takes), UW_EHIP. M = 0 is a no-op. Buffers must not
+ * overlap, but that Wg and Wu may be the same plane.
+ */
+size_t uw_w4_plane_bytes(int64_t N, int64_t K, int32_t group); /* 0 for arguments that the calls refuse */
+uw_status uw_w4_quantize(const void* d_w, int32_t w_type, int64_t N, int64_t K, int64_t ldw, int32_t group, int32_t zeros,
+                         void* d_plane, void* stream);
+uw_status uw_w4_expand(const void* d_plane, int64_t N, int64_t K, int32_t group, void* d_w, int32_t w_type, int64_t ldw,
+                       void* stream);
+typedef struct {
+    int64_t M, N, K;
+    int32_t group;
+    const uint16_t* d_x; /* X bf16 [M][ldx] */
+    int64_t ldx;         /* >= K, a multiple of 8 */
+    const void* d_plane; /* W; of uw_w4_gate_up: Wg */
+    const void* d_up;    /* Wu; unused by uw_w4_gemm */
+    void* d_y;           /* Y or h [M][ldy] */
+    int64_t ldy;         /* >= N */
+    int32_t y_type;      /* uw_type; uw_w4_gate_up: UW_BF16 */
+    void* d_ws;
+    size_t ws_bytes;
+} uw_w4_args;
+
+uw_status uw_w4_gemm(const uw_w4_args* args, void* stream);
+uw_status uw_w4_gate_up(const uw_w4_args* args, void* stream);
+size_t uw_w4_gemm_workspace(int64_t M, int64_t N, int64_t K);
+
+/*
+ * uw_block_norm (device). What lies between a block's output y and the next block's input h: the norm after
+ * the block, its gate and scale, the residual stream, and the norm before the next block, row by row:
+ *   v  = post(y)
+ *   r' = scale_r * r + scale_y * gate * v
+ *   h  = pre(r')                     (of the fp32 r', not of its stored rounding)
+ * A norm is UW_NORM_NONE (the value itself), UW_NORM_RMS (x / sqrt(mean x^2 + eps) * (w + w_add)) or UW_NORM_LAYER
+ * ((x - mean) / sqrt(mean (x - mean)^2 + eps) * (w + w_add) + b), weights w and biases b [K] optional (NULL: w + w_add is
+ * 1 and b 0). The gate multiplies value by value: row m of y takes row m / gate_rows of d_gate, gate_rows = 0: all rows take
+ * the first (NULL: 1). Weights, biases and gate are of w_type. All arithmetic is fp32, sums of a row included; each output
+ * is rounded once. A NaN stays in its row; rows whose sum of squares passes fp32's range are not supported.
+ * d_y NULL: no block (r' = scale_r * r), d_r NULL: no stream (r' = scale_y * gate * v); d_r_out NULL: r' is not
+ * stored; d_h NULL: there is no h. At least one of d_y, d_r and one of d_r_out, d_h are given.
+ * h is bf16, fp32 or, with h_type UW_E4M3, the codes that uw_fp8_quantize makes of the fp32 h with rows of groups:
+ * scales d_s[k / 128][lds] and ldh bytes between rows, a multiple of 16.
+ * d_r_out may be d_r, d_y or of neither; d_h may be d_y or d_r where their types and leading dimensions are the
+ * same (every row is read before any of it is written); else buffers must not overlap. Elements behind K in a row are
+ * neither used nor written.
+ * Errors: UW_ESHAPE (M < 0, K < 1), UW_EINVAL (NULL pointers as above; misaligned ones: 16 bytes, scales 4; leading dimensions below
+ * K or that do not keep rows 16-byte aligned; an unknown type or norm; gate_rows < 0; eps not a finite number >= 0),
+ * UW_EUNSUPPORTED (K > UW_NORM_MAX_K, M >= 2^31), UW_EHIP. M = 0 is a no-op.
+ */
+#define UW_NORM_MAX_K 65536
+typedef enum { UW_NORM_NONE = 0, UW_NORM_RMS = 1, UW_NORM_LAYER = 2 } uw_norm;
+typedef struct {
+    int64_t M, K;
+    const void* d_y;   /* [M][ldy] or NULL */
+    int64_t ldy;
+    int32_t y_type;    /* UW_F32 or UW_BF16 */
+    const void* d_r;   /* [M][ldr] or NULL */
+    int64_t ldr;
+    int32_t r_type;    /* UW_F32 or UW_BF16, of r and r' */
+    void* d_r_out;     /* [M][ldr_out] or NULL */
+    int64_t ldr_out;
+    int32_t post, pre; /* uw_norm */
+    const void* d_post_w; /* [K] or NULL */
+    const void* d_post_b; /* [K] or NULL, UW_NORM_LAYER only */
+    const void* d_pre_w;
+    const void* d_pre_b;
+    const void* d_gate; /* [ceil(M / gate_rows)][ldgate] or NULL */
+    int64_t gate_rows;
+    int64_t ldgate;
+    int32_t w_type;    /* UW_F32 or UW_BF16, of weights, biases and gate */
+    float w_add;
+    float scale_y, scale_r;
+    float eps;
+    void* d_h;         /* [M][ldh] or NULL */
+    int64_t ldh;
+    int32_t h_type;    /* UW_F32, UW_BF16 or UW_E4M3 */
+    float* d_s;        /* UW_E4M3: scales [ceil(K / 128)][lds] */
+    int64_t lds;       /* >= M */
+} uw_block_norm_args;
+
+uw_status uw_block_norm(const uw_block_norm_args* args, void* stream);
+
+/*
+ * uw_logprobs (device). Per row of logits, of the distribution that uw_sample draws from with the temperature T
+ * alone: weights w_i = exp((l_i - max) / T), tokens ordered by logit, the largest first, equal ones by index.
+ *   d_logprob  log(w_t / sum of w) of the row's given token t = d_token[m]
+ *   d_rank     how many tokens come before t in the order
+ *   d_entropy  - sum of p log p, p = w / sum of w
+ *   d_top_token, d_top_logprob  [M][n_top]: the first n_top tokens of the order and their log probabilities
+ * Each output may be NULL (d_top_token and d_top_logprob with n_top = 0; else either). Temperatures, NaN, infinities and masks
+ * are as in uw_sample: T <= 0 or NaN gives the first token of the order all of the mass, an infinite T weighs all
+ * tokens the same; logits that are NaN or -inf have no mass and no place in the order; where some are +inf they share
+ * the mass. A token without a place, or outside 0..V-1 (a padded position), has log probability -inf and rank -1. In the top
+ * lists places past the last token of the order hold -1 and -inf. A row in which no token has a place gets entropy 0.
+ * exp and its sums are fp32 within a few hundred values and fp64 from there on: log probabilities and
+ * entropies are within about 1e-6 (and 2^-23 of their value). Ranks and top tokens come from comparisons
+ * alone and are exact. No result depends on the run.
+ * d_ws: uw_logprobs_workspace(M, V, n_top) bytes, 16-byte aligned; free again when the call's work is done; calls
+ * that overlap need one each. NULL where that is 0.
+ * Errors: UW_ESHAPE (M < 0, V < 1), UW_EINVAL (NULL d_logits; d_logprob or d_rank without d_token; no output; misaligned pointers: that
+ * of their elements; ld < V; an unknown type; n_top < 0), UW_ENOSPACE (workspace), UW_EUNSUPPORTED (V > UW_SAMPLE_MAX_V, M >= 2^22, n_top >
+ * UW_LOGPROBS_MAX_TOP), UW_EHIP. M = 0 is a no-op.
+ */
+#define UW_LOGPROBS_MAX_TOP 128
+typedef struct {
+    int64_t M, V;
+    const void* d_logits;       /* [M][ld] */
+    int64_t ld;                 /* >= V, any */
+    int32_t type;               /* uw_type of the logits */
+    const int32_t* d_token;     /* [M] or NULL */
+    const float* d_temperature; /* [M] or NULL (1) */
+    float* d_logprob;           /* [M] or NULL */
+    int32_t* d_rank;            /* [M] or NULL */
+    float* d_entropy;           /* [M] or NULL */
+    int32_t n_top;
+    int32_t* d_top_token;       /* [M][n_top] or NULL */
+    float* d_top_logprob;       /* [M][n_top] or NULL */
+    void* d_ws;
+    size_t ws_bytes;
+} uw_logprobs_args;
+
+uw_status uw_logprobs(const uw_logprobs_args* args, void* stream);
+size_t uw_logprobs_workspace(int64_t M, int64_t V, int32_t n_top);
 
 /*
  * MLP stack (device). One SwiGLU MLP per layer, layers in order: g = X Wg^T, u = X Wu^T,
