@@ -25,15 +25,18 @@ namespace {
 
 constexpr int kParts = 256;   // shares of a slice whose maxima are compared
 constexpr int kList = 2048;   // tokens that are sorted in LDS
-constexpr int kMostSlices = 32;
+constexpr int kCounted = 256; // as many are ordered by counting
+constexpr int kMostSlices = 8;
 constexpr double kLn2 = 0x1.62e42fefa39efp-1;
 constexpr u64 kNoKey = ~u64{0};
 
-// What one workgroup knows of its slice of a row.
+// What is known of a row or of one workgroup's slice of it.
 struct Part {
-    double S, H;  // relative to `top`
+    double S, H;     // relative to `top`
     float top;
-    int32_t before;  // tokens before the given one
+    float given;     // logit of the given token, -inf where it has no place in the order
+    int32_t before;  // tokens before it
+    int32_t unused;
 };
 
 struct LogprobArgs {
@@ -102,11 +105,6 @@ struct Words {
     }
 };
 
-// Running maximum and sums.
-struct Sums {
-    float top, S, H;
-};
-
 // 2 log2(e) / T, of halved differences, which cannot overflow; 0 where all tokens weigh the same or (T <= 0, NaN)
 // the sums are not used.
 __device__ __forceinline__ float slope(float T)
@@ -115,25 +113,54 @@ __device__ __forceinline__ float slope(float T)
     return static_cast<float>(fmin(2.8853900817779268 / static_cast<double>(T), 3.0e38));
 }
 
-__device__ __forceinline__ double from(float lower, float top, float c2)  // y of `lower` below `top`
+// Sums below a maximum `from` as sums below `top`, in units of its exponential. An infinite maximum leaves what is
+// finite no mass.
+__device__ __forceinline__ void rebase(float& S, float& H, float from, float top, float c2)
 {
-    if (lower == top) return 0.0;
-    const double y = (static_cast<double>(lower) - static_cast<double>(top)) * 0.5 * static_cast<double>(c2);
-    return y > -1100.0 ? y : -1100.0;  // NaN too
+    if (from == top) return;
+    const float y = fmaxf(__builtin_fmaf(from, 0.5f, -0.5f * top) * c2, -200.f);  // NaN too
+    const float f = top == INFINITY ? 0.f : __builtin_amdgcn_exp2f(y);
+    H = f * __builtin_fmaf(y, S, H);
+    S *= f;
 }
 
-// Adds sums below another maximum.
-__device__ __forceinline__ void join(Part& a, double S, double H, float top, float c2)
+// Maximum and sum over the lanes of a wave, the same bits in all of them: rotations within 16 lanes, then across.
+template <int CTRL>
+__device__ __forceinline__ float rotated(float v)
 {
-    const float m = fmaxf(a.top, top);
-    const double ya = a.top == -INFINITY ? 0.0 : from(a.top, m, c2), yb = top == -INFINITY ? 0.0 : from(top, m, c2);
-    const double fa = exp2(ya), fb = exp2(yb);
-    // an infinite maximum leaves what is finite no mass
-    const bool inf = m == INFINITY;
-    const double A = inf && a.top != m ? 0.0 : fa, B = inf && top != m ? 0.0 : fb;
-    a.H = A * (a.H + ya * a.S) + B * (H + yb * S);
-    a.S = A * a.S + B * S;
-    a.top = m;
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double rotated(double v)
+{
+    const long long b = __double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, 0xF, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, 0xF, 0xF, false);
+    return __longlong_as_double(static_cast<long long>(static_cast<u64>(hi) << 32 | lo));
+}
+template <int CTRL>
+__device__ __forceinline__ int rotated(int v)
+{
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+template <class V>
+__device__ __forceinline__ V wave_sum(V v)
+{
+    v += rotated<0x128>(v);
+    v += rotated<0x124>(v);
+    v += rotated<0x122>(v);
+    v += rotated<0x121>(v);
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = fmaxf(v, rotated<0x128>(v));
+    v = fmaxf(v, rotated<0x124>(v));
+    v = fmaxf(v, rotated<0x122>(v));
+    v = fmaxf(v, rotated<0x121>(v));
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
 }
 
 // The greatest number below v (v not NaN or -inf).
@@ -151,11 +178,12 @@ __device__ __forceinline__ double log_share(float l, const Part& p, double logS,
 }
 __device__ __forceinline__ bool greedy(float T) { return !(T > 0.f); }
 
-__device__ __forceinline__ void answer_row(const LogprobArgs& a, int64_t m, const Part& p, double logS, float T, bool placed, float lt)
+__device__ __forceinline__ void answer_row(const LogprobArgs& a, int64_t m, const Part& p, double logS, float T)
 {
+    const bool placed = p.given > -INFINITY;
     if (a.rank) a.rank[m] = placed ? p.before : -1;
     if (a.logprob) {
-        const double v = !placed ? -INFINITY : greedy(T) ? (p.before == 0 ? 0.0 : -INFINITY) : log_share(lt, p, logS, T);
+        const double v = !placed ? -INFINITY : greedy(T) ? (p.before == 0 ? 0.0 : -INFINITY) : log_share(p.given, p, logS, T);
         a.logprob[m] = static_cast<float>(v);
     }
     if (a.entropy) {
@@ -173,120 +201,46 @@ __device__ __forceinline__ void answer_top(const LogprobArgs& a, int64_t m, uint
     }
 }
 
-// The given token of a row: whether it has a place in the order, and its logit.
-template <class T>
-__device__ __forceinline__ bool given(const LogprobArgs& a, const T* x, int64_t m, int& t, float& l)
-{
-    t = a.token ? a.token[m] : -1;
-    l = t >= 0 && t < a.V ? value(x, t) : -INFINITY;
-    return l > -INFINITY;
-}
-
 template <int NT>
 struct Shared {
     u64 list[kList];
     uint32_t share[kParts];
-    uint32_t better[kParts];
     uint32_t hist[256];
     uint16_t flagged[NT];
-    uint32_t n_flagged, n_list, bound_tau;
-    Part part[NT / 64];
+    float top[NT / 64];
+    double S[NT / 64], H[NT / 64];
+    int before[NT / 64];
+    uint32_t n_flagged, n_list;
     u64 prefix;
     uint32_t taken, shift, done;
 };
 
-// The slice's first n keys, in order, into out (kNoKey past the last one); every thread's words are first + tid + NT i
-// below `end`, and `top` is its largest logit.
-template <class T, int NT, class Out>
-__device__ void first_keys(Shared<NT>& sh, const Words<T>& w, int first, int end, float top, int n, Out out)
+template <int NT>
+__device__ __forceinline__ void put(Shared<NT>& sh, float l, int i)
 {
-    constexpr int VEC = Words<T>::VEC, QUAD = NT / kParts;
-    static_assert(QUAD == 1 || QUAD == 2 || QUAD == 4, "threads per share");
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    float share = top;
-    if (QUAD > 1) share = fmaxf(share, __shfl_xor(share, 1));
-    if (QUAD > 2) share = fmaxf(share, __shfl_xor(share, 2));
-    // larger is better; 0 = nothing with a place
-    const uint32_t mine = share > -INFINITY ? ~order_bits(share) : 0u;
-    if (tid % QUAD == 0) sh.share[tid / QUAD] = mine;
-    if (tid < kParts) sh.better[tid] = 0;
+    const uint32_t at = atomicAdd(&sh.n_list, 1u);
+    if (at < kList) sh.list[at] = key_of(l, i);
+}
+
+// Ties made the tokens from tau on too many for the list: the n-th key digit by digit, 8 bits at a time, until
+// what is left up to it fits.
+template <class T, int NT>
+__device__ __noinline__ void search_keys(Shared<NT>& sh, const Words<T>& w, int first, int end, int n)
+{
+    constexpr int VEC = Words<T>::VEC;
+    const int tid = threadIdx.x;
     if (tid == 0) {
-        sh.n_flagged = 0;
-        sh.n_list = 0;
-        sh.bound_tau = 0;
+        sh.prefix = 0;
+        sh.taken = 0;
+        sh.shift = 64;
+        sh.done = 0;
     }
     __syncthreads();
-    {
-        const int p = tid % kParts, q0 = tid / kParts * (kParts / QUAD);
-        const uint32_t own = sh.share[p];
-        uint32_t c = 0;
-        for (int q = q0; q < q0 + kParts / QUAD; q++) {
-            const uint32_t o = sh.share[q];
-            c += o > own || (o == own && q < p);
-        }
-        if (c) atomicAdd(&sh.better[p], c);
-    }
-    __syncthreads();
-    if (tid < kParts && sh.better[tid] == static_cast<uint32_t>(n - 1)) sh.bound_tau = sh.share[tid];
-    __syncthreads();
-    const uint32_t tau = sh.bound_tau;
-    const bool any = top > -INFINITY;
-    if (any && ~order_bits(top) >= tau) sh.flagged[atomicAdd(&sh.n_flagged, 1u)] = static_cast<uint16_t>(tid);
-    __syncthreads();
-    const int nf = static_cast<int>(sh.n_flagged);
-    for (int f = wave; f < nf; f += NT / 64) {
-        const int t = sh.flagged[f];
-        for (int i = first + t + NT * lane; i < end; i += NT * 64) {
-            float v[VEC];
-            w.load(i, v);
-#pragma unroll
-            for (int k = 0; k < VEC; k++)
-                if (v[k] > -INFINITY && ~order_bits(v[k]) >= tau) {
-                    const uint32_t at = atomicAdd(&sh.n_list, 1u);
-                    if (at < kList) sh.list[at] = key_of(v[k], w.first(i) + k);
-                }
-        }
-    }
-    __syncthreads();
-    if (sh.n_list > kList) {
-        // Ties: the n-th key digit by digit, 8 bits at a time, until what is left up to it fits the list.
-        if (tid == 0) {
-            sh.prefix = 0;
-            sh.taken = 0;
-            sh.shift = 64;
-            sh.done = 0;
-        }
-        __syncthreads();
-        while (!sh.done) {
-            const uint32_t shift = sh.shift;
-            const u64 prefix = sh.prefix;
-            if (tid < 256) sh.hist[tid] = 0;
-            __syncthreads();
-            for (int i = first + tid; i < end; i += NT) {
-                float v[VEC];
-                w.load(i, v);
-#pragma unroll
-                for (int k = 0; k < VEC; k++)
-                    if (v[k] > -INFINITY) {
-                        const u64 key = key_of(v[k], w.first(i) + k);
-                        if (shift == 64 || key >> shift == prefix) atomicAdd(&sh.hist[(key >> (shift - 8)) & 255], 1u);
-                    }
-            }
-            __syncthreads();
-            if (tid == 0) {
-                uint32_t c = sh.taken;
-                int d = 0;
-                while (d < 255 && c + sh.hist[d] < static_cast<uint32_t>(n)) c += sh.hist[d++];
-                sh.taken = c;
-                sh.prefix = (shift == 64 ? 0 : prefix << 8) | static_cast<u64>(d);
-                sh.shift = shift - 8;
-                sh.done = c + sh.hist[d] <= kList || shift == 8;
-                sh.n_list = 0;
-            }
-            __syncthreads();
-        }
+    while (!sh.done) {
         const uint32_t shift = sh.shift;
         const u64 prefix = sh.prefix;
+        if (tid < 256) sh.hist[tid] = 0;
+        __syncthreads();
         for (int i = first + tid; i < end; i += NT) {
             float v[VEC];
             w.load(i, v);
@@ -294,32 +248,69 @@ __device__ void first_keys(Shared<NT>& sh, const Words<T>& w, int first, int end
             for (int k = 0; k < VEC; k++)
                 if (v[k] > -INFINITY) {
                     const u64 key = key_of(v[k], w.first(i) + k);
-                    if (key >> shift <= prefix) {
-                        const uint32_t at = atomicAdd(&sh.n_list, 1u);
-                        if (at < kList) sh.list[at] = key;
-                    }
+                    if (shift == 64 || key >> shift == prefix) atomicAdd(&sh.hist[(key >> (shift - 8)) & 255], 1u);
                 }
         }
         __syncthreads();
+        if (tid == 0) {
+            uint32_t c = sh.taken;
+            int d = 0;
+            while (d < 255 && c + sh.hist[d] < static_cast<uint32_t>(n)) c += sh.hist[d++];
+            sh.taken = c;
+            sh.prefix = (shift == 64 ? 0 : prefix << 8) | static_cast<u64>(d);
+            sh.shift = shift - 8;
+            sh.done = c + sh.hist[d] <= kList || shift == 8;
+            sh.n_list = 0;
+        }
+        __syncthreads();
     }
-    // Keys are all different, so a key's place is the number of smaller ones.
-    const int C = static_cast<int>(sh.n_list);
-    for (int c = tid; c < C; c += NT) {
-        const u64 key = sh.list[c];
-        int place = 0;
-        for (int o = 0; o < C; o++) place += sh.list[o] < key;
-        if (place < n) out(place, key);
+    const uint32_t shift = sh.shift;
+    const u64 prefix = sh.prefix;
+    for (int i = first + tid; i < end; i += NT) {
+        float v[VEC];
+        w.load(i, v);
+#pragma unroll
+        for (int k = 0; k < VEC; k++)
+            if (v[k] > -INFINITY && key_of(v[k], w.first(i) + k) >> shift <= prefix) put(sh, v[k], w.first(i) + k);
     }
-    for (int c = C + tid; c < n; c += NT) out(c, kNoKey);
+    __syncthreads();
 }
 
-// One slice of a row (all of it with slices = 1) per workgroup.
+// A number that at least n of the shares' maxima reach, but not many more; -inf where fewer than n have one. By halving, in
+// the order of numbers, each wave for itself: the counts are those of its lanes' comparisons.
+__device__ __forceinline__ float threshold(const uint32_t* share, float top, uint32_t n)
+{
+    constexpr uint32_t kNone = 0x007FFFFFu;  // -inf in that order
+    const int lane = threadIdx.x & 63;
+    uint32_t v[kParts / 64];
+#pragma unroll
+    for (int i = 0; i < kParts / 64; i++) v[i] = share[lane + 64 * i];
+    uint32_t lo = kNone, hi = top > -INFINITY ? ~order_bits(top) : kNone;
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < kParts / 64; i++) c += __popcll(__ballot(v[i] >= mid));
+        if (c < n) {
+            hi = mid - 1;
+        } else {
+            lo = mid;
+            if (c <= n + n / 4) break;
+        }
+    }
+    return lo == kNone ? -INFINITY : order_value(~lo);
+}
+
+// One slice of a row (all of it with slices = 1) per workgroup; thread t has the words first + t + NT i.
 template <class T, int NT>
 __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
 {
     constexpr int VEC = Words<T>::VEC, U = 16 / VEC;  // 16 values per thread and step
+    constexpr int PER = NT / kParts;                  // threads per share
+    static_assert(PER == 1 || PER == 2 || PER == 4, "threads per share");
     __shared__ Shared<NT> sh;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint32_t z = blockIdx.x % a.slices;
     const int64_t m = blockIdx.x / a.slices;
     const T* x = static_cast<const T*>(a.x) + m * a.ld;
@@ -327,15 +318,15 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
     const int per = (w.n + static_cast<int>(a.slices) - 1) / static_cast<int>(a.slices);
     const int first = per * static_cast<int>(z), end = first + per < w.n ? first + per : w.n;
     const float temp = a.temperature ? a.temperature[m] : 1.f, c2 = slope(temp);
-    int t;
-    float lt;
-    const bool placed = given(a, x, m, t, lt);
+    const int t = a.token ? a.token[m] : -1;
+    const float lt = t >= 0 && t < a.V ? value(x, t) : -INFINITY;
+    const bool placed = lt > -INFINITY;
     const float lt_before = placed ? below(lt) : INFINITY, lt_after = placed ? lt : INFINITY;
 
-    Sums s = {-INFINITY, 0.f, 0.f};
+    float top = -INFINITY, S = 0.f, H = 0.f, v[U][VEC];
     int before = 0;
+    const bool counts = a.rank || greedy(temp);
     for (int i = first + tid; i < end; i += NT * U) {
-        float v[U][VEC];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             if (i + u * NT < end) {
@@ -345,137 +336,234 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
                 for (int k = 0; k < VEC; k++) v[u][k] = -INFINITY;
             }
         }
-        float top = s.top;
+        float now = top;
 #pragma unroll
         for (int u = 0; u < U; u++)
 #pragma unroll
-            for (int k = 0; k < VEC; k++) top = fmaxf(top, v[u][k]);
+            for (int k = 0; k < VEC; k++) now = fmaxf(now, v[u][k]);
+        if (now > top) rebase(S, H, top, now, c2);
+        top = now;
         if (top == INFINITY) {
-            float c = s.top == top ? s.S : 0.f;
 #pragma unroll
             for (int u = 0; u < U; u++)
 #pragma unroll
-                for (int k = 0; k < VEC; k++) c += v[u][k] == top ? 1.f : 0.f;
-            s.S = c;
-            s.H = 0.f;
+                for (int k = 0; k < VEC; k++) S += v[u][k] == top ? 1.f : 0.f;
         } else {
             const float half = 0.5f * top;
-            if (top > s.top) {
-                const float y = fmaxf(__builtin_fmaf(s.top, 0.5f, -half) * c2, -200.f), f = __builtin_amdgcn_exp2f(y);
-                s.H = f * __builtin_fmaf(y, s.S, s.H);
-                s.S *= f;
-            }
-            float S = 0.f, H = 0.f;
+            float s = 0.f, h = 0.f;
 #pragma unroll
             for (int u = 0; u < U; u++)
 #pragma unroll
                 for (int k = 0; k < VEC; k++) {
                     const float y = fmaxf(__builtin_fmaf(v[u][k], 0.5f, -half) * c2, -200.f);  // a mask's NaN too
                     const float e = __builtin_amdgcn_exp2f(y);
-                    S += e;
-                    H = __builtin_fmaf(y, e, H);
+                    s += e;
+                    h = __builtin_fmaf(y, e, h);
                 }
-            s.S += S;
-            s.H += H;
+            S += s;
+            H += h;
         }
-        s.top = top;
+        if (counts)
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int e = w.first(i + u * NT);
-            if (e < t && t < e + VEC) {
-#pragma unroll
-                for (int k = 0; k < VEC; k++) before += v[u][k] > (e + k < t ? lt_before : lt_after);
-            } else {
-                const float than = e < t ? lt_before : lt_after;
+            for (int u = 0; u < U; u++) {
+                const float than = w.first(i + u * NT) < t ? lt_before : lt_after;
 #pragma unroll
                 for (int k = 0; k < VEC; k++) before += v[u][k] > than;
             }
+    }
+    {   // In the word that t lies in, but does not begin, tokens that equal it were counted from t on too.
+        const int word = (t + w.skip) / VEC, e = w.first(word) + tid;
+        if (counts && placed && first <= word && word < end && w.first(word) < t && tid < VEC && e >= t && e < a.V) before -= value(x, e) == lt;
+    }
+    // The row's maximum ...
+    const int n = a.n_top;
+    {
+        const float m_wave = wave_max(top);
+        if (lane == 0) sh.top[wave] = m_wave;
+        float share = top;
+        if (PER > 1) share = fmaxf(share, __shfl_xor(share, 1));
+        if (PER > 2) share = fmaxf(share, __shfl_xor(share, 2));
+        if (tid % PER == 0) sh.share[tid / PER] = share > -INFINITY ? ~order_bits(share) : 0u;
+        if (tid == 0) {
+            sh.n_flagged = 0;
+            sh.n_list = 0;
         }
     }
-    // threads, then waves
-    Part p = {s.S, s.H, s.top, before};
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const double S = __shfl_xor(p.S, d), H = __shfl_xor(p.H, d);
-        const float o = __shfl_xor(p.top, d);
-        const int b = __shfl_xor(p.before, d);
-        join(p, S, H, o, c2);
-        p.before += b;
-    }
-    if ((tid & 63) == 0) sh.part[tid >> 6] = p;
     __syncthreads();
-    p = sh.part[0];
-    for (int i = 1; i < NT / 64; i++) {
-        join(p, sh.part[i].S, sh.part[i].H, sh.part[i].top, c2);
-        p.before += sh.part[i].before;
+    Part p{};
+    p.top = sh.top[0];
+#pragma unroll
+    for (int i = 1; i < NT / 64; i++) p.top = fmaxf(p.top, sh.top[i]);
+    p.given = lt;
+    // ... and the sums below that maximum.
+    rebase(S, H, top, p.top, c2);
+    const double dS = wave_sum(static_cast<double>(S)), dH = wave_sum(static_cast<double>(H));
+    before = wave_sum(before);
+    if (lane == 0) {
+        sh.S[wave] = dS;
+        sh.H[wave] = dH;
+        sh.before[wave] = before;
     }
-    if (a.slices > 1) {
-        if (tid == 0) a.part[m * a.slices + z] = p;
-        if (a.n_top) {
-            u64* keys = a.keys + (m * a.slices + z) * a.n_top;
-            first_keys<T, NT>(sh, w, first, end, s.top, a.n_top, [&](int place, u64 key) { keys[place] = key; });
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 64; i++) {
+        p.S += sh.S[i];
+        p.H += sh.H[i];
+        p.before += sh.before[i];
+    }
+    const double logS = a.slices > 1 ? 0.0 : log(p.S);
+    if (tid == 0) {
+        if (a.slices > 1)
+            a.part[m * a.slices + z] = p;
+        else
+            answer_row(a, m, p, logS, temp);
+    }
+    if (n == 0) return;
+    // Tokens from tau on: a number that at least n shares reach and few more, or -inf.
+    const float tau = n == 1 ? p.top : threshold(sh.share, p.top, static_cast<uint32_t>(n));
+    const bool mine = top > -INFINITY && top >= tau;
+    if (end - first <= NT * U) {  // they are in registers still
+        if (mine) {
+#pragma unroll
+            for (int u = 0; u < U; u++)
+#pragma unroll
+                for (int k = 0; k < VEC; k++)
+                    if (v[u][k] > -INFINITY && v[u][k] >= tau) put(sh, v[u][k], w.first(first + tid + u * NT) + k);
         }
-    } else {
-        const double logS = log(p.S);
-        if (tid == 0) answer_row(a, m, p, logS, temp, placed, lt);
-        if (a.n_top)
-            first_keys<T, NT>(sh, w, first, end, s.top, a.n_top, [&](int place, u64 key) { answer_top(a, m, static_cast<uint32_t>(place), key, p, logS, temp); });
+    } else {  // a wave looks through a thread's words
+        if (mine) sh.flagged[atomicAdd(&sh.n_flagged, 1u)] = static_cast<uint16_t>(tid);
+        __syncthreads();
+        const int nf = static_cast<int>(sh.n_flagged);
+        for (int f = wave; f < nf; f += NT / 64)
+            for (int i = first + sh.flagged[f] + NT * lane; i < end; i += NT * 64) {
+                float c[VEC];
+                w.load(i, c);
+#pragma unroll
+                for (int k = 0; k < VEC; k++)
+                    if (c[k] > -INFINITY && c[k] >= tau) put(sh, c[k], w.first(i) + k);
+            }
+    }
+    __syncthreads();
+    if (sh.n_list > kList) search_keys<T, NT>(sh, w, first, end, n);
+    // Keys are all different, so a key's place is the number of smaller ones; many are sorted instead.
+    const int C = static_cast<int>(sh.n_list);
+    u64* keys = a.slices > 1 ? a.keys + (m * a.slices + z) * n : nullptr;
+    if (C > kCounted) {
+        int size = 2 * kCounted;
+        while (size < C) size *= 2;
+        for (int c = C + tid; c < size; c += NT) sh.list[c] = kNoKey;
+        __syncthreads();
+        for (int run = 2; run <= size; run *= 2)
+            for (int d = run / 2; d > 0; d /= 2) {
+                for (int q = tid; q < size / 2; q += NT) {
+                    const int i = 2 * q - (q & (d - 1)), j = i + d;
+                    const u64 x0 = sh.list[i], x1 = sh.list[j];
+                    if ((x0 > x1) == ((i & run) == 0)) {
+                        sh.list[i] = x1;
+                        sh.list[j] = x0;
+                    }
+                }
+                __syncthreads();
+            }
+    }
+    for (int c = tid; c < n || (c < C && C <= kCounted); c += NT) {
+        u64 key = kNoKey;
+        int place = c;
+        if (c < C) {
+            key = sh.list[c];
+            if (C <= kCounted) {
+                place = 0;
+#pragma unroll 4
+                for (int o = 0; o < C; o++) place += sh.list[o] < key;
+            }
+        }
+        if (place >= n) continue;
+        if (keys)
+            keys[place] = key;
+        else
+            answer_top(a, m, static_cast<uint32_t>(place), key, p, logS, temp);
     }
 }
 
 // A row's answers from its slices: sums in slice order, and each key's place among all slices' sorted
-// keys, by a search in each list.
+// keys, the sum of its places in each list.
+constexpr int kJoinThreads = 512;
 template <class T>
-__global__ void __launch_bounds__(256) logprobs_join(LogprobArgs a)
+__global__ void __launch_bounds__(kJoinThreads) logprobs_join(LogprobArgs a)
 {
     __shared__ u64 keys[kMostSlices * UW_LOGPROBS_MAX_TOP];
+    __shared__ int place[kMostSlices * UW_LOGPROBS_MAX_TOP], count;
+    __shared__ uint16_t list[kMostSlices * UW_LOGPROBS_MAX_TOP];
+    static_assert(kMostSlices <= 64, "one lane per slice");
     const int64_t m = blockIdx.x;
-    const int tid = threadIdx.x, n = a.n_top, S = static_cast<int>(a.slices);
-    for (int i = tid; i < n * S; i += 256) keys[i] = a.keys[m * S * n + i];
+    const int tid = threadIdx.x, lane = tid & 63, n = a.n_top, slices = static_cast<int>(a.slices);
+    for (int i = tid; i < n * slices; i += kJoinThreads) {
+        keys[i] = a.keys[m * slices * n + i];
+        place[i] = 0;
+    }
+    if (tid == 0) count = 0;
     const float temp = a.temperature ? a.temperature[m] : 1.f, c2 = slope(temp);
-    Part p = a.part[m * S];
-    for (int z = 1; z < S; z++) {
-        const Part o = a.part[m * S + z];
-        join(p, o.S, o.H, o.top, c2);
-        p.before += o.before;
+    Part p{};
+    p.top = p.given = -INFINITY;
+    if (lane < slices) p = a.part[m * slices + lane];
+    const float top = wave_max(p.top);
+    if (p.top != top) {
+        const double y = fmax((0.5 * p.top - 0.5 * top) * c2, -1100.0);  // NaN too
+        const double f = top == INFINITY ? 0.0 : exp2(y);
+        p.H = f * (p.H + y * p.S);
+        p.S *= f;
     }
+    p.S = wave_sum(p.S);
+    p.H = wave_sum(p.H);
+    p.before = wave_sum(p.before);
+    p.given = __shfl(p.given, 0);
+    p.top = top;
     const double logS = log(p.S);
-    if (tid == 0) {
-        int t;
-        float lt;
-        const bool placed = given(a, static_cast<const T*>(a.x) + m * a.ld, m, t, lt);
-        answer_row(a, m, p, logS, temp, placed, lt);
-    }
+    if (tid == 0) answer_row(a, m, p, logS, temp);
+    if (n == 0) return;
     __syncthreads();
-    for (int i = tid; i < n * S; i += 256) {
-        const u64 key = keys[i];
-        if (key == kNoKey) continue;
-        int place = 0;
-        for (int z = 0; z < S && place < n; z++) {
-            int lo = 0, hi = n;  // keys of list z below this one
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                if (keys[z * n + mid] < key)
-                    lo = mid + 1;
-                else
-                    hi = mid;
-            }
-            place += lo;
+    // Of the lists' q-th keys the r-th smallest has q r >= n keys up to it, and not many more with q near 2 n / slices:
+    // only these are looked at.
+    const int q = 2 * n < slices ? 1 : (2 * n + slices - 1) / slices < n ? (2 * n + slices - 1) / slices : n, r = (n + q - 1) / q;
+    const u64 mine = lane < slices ? keys[lane * n + q - 1] : kNoKey;
+    int below_mine = 0;
+    for (int z = 0; z < slices; z++) {
+        const u64 other = keys[z * n + q - 1];
+        below_mine += other < mine || (other == mine && z < lane);
+    }
+    const u64 at = __ballot(lane < slices && below_mine == r - 1);
+    const u64 most = __shfl(mine, static_cast<int>(__builtin_ctzll(at)));
+    for (int i = tid; i < n * slices; i += kJoinThreads)
+        if (keys[i] <= most && keys[i] != kNoKey) list[atomicAdd(&count, 1)] = static_cast<uint16_t>(i);
+    __syncthreads();
+    const int C = count;
+    for (int i = tid; i < C * slices; i += kJoinThreads) {
+        const int c = list[i / slices], z = i % slices;
+        const u64 key = keys[c];
+        int lo = 0, hi = n;  // keys of list z below this one
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (keys[z * n + mid] < key)
+                lo = mid + 1;
+            else
+                hi = mid;
         }
-        if (place < n) answer_top(a, m, static_cast<uint32_t>(place), key, p, logS, temp);
+        if (lo) atomicAdd(&place[c], lo);
     }
-    // places past the last token of the row
-    __shared__ int have;
-    if (tid == 0) have = 0;
     __syncthreads();
-    int c = 0;
-    for (int i = tid; i < n * S; i += 256) c += keys[i] != kNoKey;
-    if (c) atomicAdd(&have, c);
-    __syncthreads();
-    for (int i = have + tid; i < n; i += 256) answer_top(a, m, static_cast<uint32_t>(i), kNoKey, p, logS, temp);
+    for (int i = tid; i < C; i += kJoinThreads) {
+        const int c = list[i];
+        if (place[c] < n) answer_top(a, m, static_cast<uint32_t>(place[c]), keys[c], p, logS, temp);
+    }
+    // (with fewer than n keys in the row all of them are in the list)
+    for (int i = C + tid; i < n; i += kJoinThreads) answer_top(a, m, static_cast<uint32_t>(i), kNoKey, p, logS, temp);
 }
 
-// Workgroups of NT threads, `slices` of them per row.
+// Workgroups of `threads`, `slices` of them per row. A CU takes about 3 us for 32000 tokens, so a row among few is
+// cut into slices until the second launch (3 us) costs more than they save: 1 x 131072 takes 23.6, 19.9, 15.5 and
+// 13.8 us with 1, 2, 4 and 8 slices, 64 x 131072 27.6, 23.6, 19.2 and 19.6. From a CU's worth of rows on slices only add work
+// (256 x 131072: 34.5 us with two, 30.6 with a whole row per 1024 threads), and with many rows small workgroups, whose ends
+// meet others' beginnings, do best (1024 x 131072: 103 us with 256 threads, 121 with 512, 115 with 1024).
 struct Shape {
     int threads;
     uint32_t slices;
@@ -483,11 +571,11 @@ struct Shape {
 
 Shape shape_of(int64_t M, int64_t V)
 {
-    // slices of 4096 tokens at the shortest, about 1024 workgroups of 256 threads in all
-    int64_t s = (V + 4095) / 4096, want = (1024 + M - 1) / M;
-    if (s > want) s = want;
-    if (s > kMostSlices) s = kMostSlices;
-    return {256, static_cast<uint32_t>(s < 1 ? 1 : s)};
+    if (V <= 4096 || M >= 512) return {256, 1};
+    if (M >= 128) return {1024, 1};
+    int64_t s = (V + 8191) / 8192;  // a step's tokens at the shortest
+    if (s > 256 / M) s = 256 / M;
+    return {512, static_cast<uint32_t>(s < kMostSlices ? s : kMostSlices)};
 }
 
 bool sizes_ok(int64_t M, int64_t V, int32_t n_top)
@@ -530,8 +618,13 @@ template <class T>
 void launch(const LogprobArgs& a, const Shape& h, hipStream_t s)
 {
     const dim3 grid(static_cast<uint32_t>(a.M * h.slices));
-    hipLaunchKernelGGL((logprobs_rows<T, 256>), grid, dim3(256), 0, s, a);
-    if (h.slices > 1) hipLaunchKernelGGL(logprobs_join<T>, dim3(static_cast<uint32_t>(a.M)), dim3(256), 0, s, a);
+    if (h.threads == 256)
+        hipLaunchKernelGGL((logprobs_rows<T, 256>), grid, dim3(256), 0, s, a);
+    else if (h.threads == 512)
+        hipLaunchKernelGGL((logprobs_rows<T, 512>), grid, dim3(512), 0, s, a);
+    else
+        hipLaunchKernelGGL((logprobs_rows<T, 1024>), grid, dim3(1024), 0, s, a);
+    if (h.slices > 1) hipLaunchKernelGGL(logprobs_join<T>, dim3(static_cast<uint32_t>(a.M)), dim3(kJoinThreads), 0, s, a);
 }
 
 }  // namespace
