@@ -293,12 +293,6 @@ __global__ void __launch_bounds__(64 * NW) fp8_skinny(F8Args a)
 // l mod 8, so it fetches chunk (l mod 8) ^ ((rho >> 1) & 7); the eight lanes of a row read its
 // whole 128-byte segment. A fragment read (lane 16 g + r: row 16 t + r, chunks g and 4 + g) hits
 // 16 distinct 16-byte bank groups in every 16 lanes.
-__device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(base)
-                 : "memory");
-}
-
 template <int BN, int BM>
 constexpr int stage_bytes()
 {

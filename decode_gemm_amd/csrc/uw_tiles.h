@@ -25,6 +25,13 @@ __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t voff, uint32
                  : "memory");
 }
 
+// The same of 4 bytes per lane, landing at lds + 4 l.
+__device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(base)
+                 : "memory");
+}
+
 // blockIdx -> (n tile, m tile): consecutive hardware workgroups are dealt round-robin to
 // the 8 XCDs, so first regroup them so each XCD gets a contiguous run of logical tiles,
 // then walk the tiles in groups of 8 n-tiles so that concurrently resident workgroups

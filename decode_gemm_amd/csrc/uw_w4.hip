@@ -17,6 +17,7 @@
 #include "uw_codes.h"
 #include "uw_internal.h"
 #include "uw_recon.h"
+#include "uw_tiles.h"
 
 namespace uw {
 
@@ -25,6 +26,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int64_t kMostNK = int64_t{1} << 24;
+constexpr int64_t kMostLd = int64_t{1} << 26;  // 16 rows of X within 32-bit byte offsets
 
 __host__ __device__ __forceinline__ int64_t tiles16(int64_t n) { return (n + 15) / 16; }
 __host__ __device__ __forceinline__ int64_t tiles128(int64_t k) { return (k + 127) / 128; }
@@ -169,16 +171,23 @@ struct W4Args {
     void* y;
     int64_t M, N, K, ldx, ldy, J, meta;
     int32_t bf16;
+    float* part;      // K slices: partial sums [slice][plane][M][N], in units of 1/16
+    uint32_t slices;  // slice z takes every slices-th turn of the waves
 };
 
 // Four MFMA operands of a lane from its 16 bytes: word p holds the codes of operand p, a pair of them in
-// the halves of each bf16 pair. 1 + q / 16 in bf16 is 0x3F80 | q << 3.
-__device__ __forceinline__ bf16x8 operand(uint32_t w)
-{
-    constexpr uint32_t kMask = 0x00780078u, kOne = 0x3F803F80u;
-    const u32x4 o = {((w << 3) & kMask) | kOne, ((w >> 1) & kMask) | kOne, ((w >> 5) & kMask) | kOne, ((w >> 9) & kMask) | kOne};
-    return __builtin_bit_cast(bf16x8, o);
-}
+// the halves of each bf16 pair. 1 + q / 16 in bf16 is 0x3F80 | q << 3: a shift and an and-or per two codes. The and-or takes
+// both constants from registers, where the compiler, left to itself, would use literals and two operations.
+struct Codes {
+    uint32_t mask = 0x00780078u, one = 0x3F803F80u;
+    __device__ __forceinline__ Codes() { asm volatile("" : "+v"(mask), "+v"(one)); }
+    __device__ __forceinline__ bf16x8 operand(uint32_t w) const
+    {
+        const u32x4 o = {((w << 3) & mask) | one, ((w >> 1) & mask) | one, ((w >> 5) & mask) | one, ((w >> 9) & mask) | one};
+        return __builtin_bit_cast(bf16x8, o);
+    }
+    __device__ __forceinline__ bf16x8 ones() const { return __builtin_bit_cast(bf16x8, u32x4{one, one, one, one}); }
+};
 
 // Eight values of a row of X from k on; what is past K is 0 and not read.
 __device__ __forceinline__ u32x4 load_x(const uint16_t* p, int64_t k, int64_t K)
@@ -191,177 +200,318 @@ __device__ __forceinline__ u32x4 load_x(const uint16_t* p, int64_t k, int64_t K)
     return v;
 }
 
-// 16 RT rows of W (with UP: of each of the two planes) x 16 CT rows of X per workgroup, whose NW waves take the K
-// tiles in turn and meet in LDS. FEW: at most four rows of X, in the operand's rows 0, 4, 8 and 12, so that a
-// lane's first result is the only one that counts.
-template <int CT, int RT, int U, int NW, int PER, bool FEW, bool UP>
+// Sum over k of a tile's values with the codes, by groups, scaled into the accumulators. x[c][p]: operands of X. RES: results of
+// a lane that count.
+template <int RW, int CT, int PER, int RES>
+__device__ __forceinline__ void multiply_tile(const Codes& k, const u32x4 (&x)[CT][4], const u32x4 (&w)[RW], const uint32_t (&meta)[RW][PER], floatx4 (&acc)[RW][CT])
+{
+    constexpr int P = 4 / PER;  // operands per group
+#pragma unroll
+    for (int g = 0; g < PER; g++) {
+        floatx4 sum[CT];
+#pragma unroll
+        for (int c = 0; c < CT; c++) {
+            sum[c] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int p = 0; p < P; p++)
+                sum[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[c][g * P + p]), k.ones(), sum[c], 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < RW; i++) {
+            floatx4 d[CT];
+#pragma unroll
+            for (int c = 0; c < CT; c++) d[c] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int p = 0; p < P; p++) {
+                const bf16x8 b = k.operand(w[i][g * P + p]);
+#pragma unroll
+                for (int c = 0; c < CT; c++) d[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[c][g * P + p]), b, d[c], 0, 0, 0);
+            }
+            const float s = __uint_as_float(meta[i][g] & ~15u), z = __uint_as_float(0x3F800000u | (meta[i][g] & 15u) << 19);
+#pragma unroll
+            for (int c = 0; c < CT; c++)
+#pragma unroll
+                for (int q = 0; q < RES; q++) acc[i][c][q] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[c][q], d[c][q]), acc[i][c][q]);
+        }
+    }
+}
+
+// The pointer in scalar registers, where a transfer's base belongs.
+__device__ __forceinline__ const uint8_t* uniform(const void* p)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v)), hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+    return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ void store_y(const W4Args& a, int64_t m, int64_t n, float v)
+{
+    if (a.bf16)
+        static_cast<uint16_t*>(a.y)[m * a.ldy + n] = static_cast<uint16_t>(f32_to_bf16_rne(v));
+    else
+        static_cast<float*>(a.y)[m * a.ldy + n] = v;
+}
+
+// 16 RT rows of W (with UP: of each of the two planes) x XR rows of X per workgroup, whose NW waves take the K tiles in
+// turn and meet in LDS; U tiles of a wave are on the way, W's in registers and X's, sent there by DMA, in LDS that the wave
+// has for itself. XR is 16 CT, or 4 or 1 rows, which then stand in the operand's rows 0, 4, 8 and 12 (the rows between
+// repeat them), so that a lane's first result is the only one that counts.
+// An X tile in LDS: row i's 16-byte chunk c at 256 i + 16 (c ^ i mod 16), so that 16 lanes that read one chunk of 16 rows hit
+// all banks. Transfer q covers rows 4 q .. 4 q + 3, lane l landing at 16 l.
+// Order: a tile's transfers are issued before its load of W, loads and transfers return in order, so a wait for W (an empty
+// asm that uses it) is one for X; reads of a slot are waited for before it is filled again.
+template <int XR, int RT, int U, int NW, bool UP>
+struct Skinny {
+    static constexpr int RW = UP ? 2 * RT : RT, CT = XR >= 16 ? XR / 16 : 1, RES = XR >= 16 ? 4 : 1;
+    static constexpr int SLOT = XR * 256, RING = NW * U * SLOT, RED = NW * RW * CT * RES * 64 * 4;
+    static constexpr int LDS = RING > RED ? RING : RED, SENDS = XR >= 16 ? XR / 4 : 1;
+};
+
+template <int XR, int RT, int U, int NW, int PER, bool UP>
 __global__ void __launch_bounds__(64 * NW) w4_skinny(W4Args a)
 {
-    static_assert(!FEW || CT == 1, "few rows are one tile");
-    constexpr int RW = UP ? 2 * RT : RT, RES = FEW ? 1 : 4;
-    __shared__ float red[NW][RW * CT][RES][64];
+    typedef Skinny<XR, RT, U, NW, UP> C;
+    constexpr int RW = C::RW, CT = C::CT, RES = C::RES, SLOT = C::SLOT;
+    extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, r = lane & 15, c4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t T = static_cast<uint32_t>(tiles16(a.N)), J = static_cast<uint32_t>(a.J);
     const uint32_t tiles_n = (T + RT - 1) / RT;
     const uint32_t t0 = blockIdx.x % tiles_n * RT;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x / tiles_n) * (FEW ? 4 : 16 * CT);
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x / tiles_n) * XR;
+    const int rows = a.M - m0 < XR ? static_cast<int>(a.M - m0) : XR;  // rows past M repeat the last one
 
     const uint32_t *wp[RW], *sp[RW];
 #pragma unroll
     for (int i = 0; i < RW; i++) {
         const uint32_t* plane = UP && i >= RT ? a.up : a.w;
         const uint32_t t = t0 + i % RT < T ? t0 + i % RT : T - 1;
-        wp[i] = plane + static_cast<int64_t>(t) * J * 256 + 4 * lane;
-        sp[i] = plane + a.meta + static_cast<int64_t>(t) * J * PER * 16 + r;
+        wp[i] = plane + static_cast<int64_t>(t) * J * 256;
+        sp[i] = plane + a.meta + static_cast<int64_t>(t) * J * PER * 16;
     }
-    const uint16_t* xp[CT];
-    bool has[CT];
+    const uint16_t* x0 = a.x + m0 * a.ldx;
+    const Codes k;
+    const uint8_t* xbase = uniform(x0);
+    const uint32_t ring = lds_offset(lds) + static_cast<uint32_t>(wave * U * SLOT);
+    // what a lane sends: one row's chunk per transfer, or with one row a dword of it
+    uint32_t xoff[C::SENDS];
 #pragma unroll
-    for (int c = 0; c < CT; c++) {
-        const int64_t m = FEW ? m0 + (r >> 2) : m0 + 16 * c + r;
-        has[c] = m < a.M && (!FEW || (r & 3) == 0);
-        xp[c] = a.x + (has[c] ? m : 0) * a.ldx + 8 * c4;
+    for (int q = 0; q < C::SENDS; q++) {
+        const int i = 4 * q + (lane >> 4), row = i < rows ? i : rows - 1;
+        xoff[q] = XR == 1 ? 4 * lane : static_cast<uint32_t>(row * a.ldx * 2) + 16 * ((lane & 15) ^ (i & 15));
     }
+    // and reads: row r's chunk 4 p + c4 (of the first 16 rows; the others lie 4096 bytes apart)
+    const int xrow = XR >= 16 ? r : XR == 4 ? r >> 2 : 0;
+    uint32_t rd[4];
+#pragma unroll
+    for (int p = 0; p < 4; p++) rd[p] = 256 * xrow + 16 * ((4 * p + c4) ^ xrow);
+    const uint8_t* mine = lds + wave * U * SLOT;
+
     floatx4 acc[RW][CT];
 #pragma unroll
     for (int i = 0; i < RW; i++)
 #pragma unroll
         for (int c = 0; c < CT; c++) acc[i][c] = floatx4{0.f, 0.f, 0.f, 0.f};
-
-    u32x4 wv[U][RW], xv[U][CT][4];
+    u32x4 wv[U][RW];
     uint32_t sv[U][RW][PER];
     auto load_w = [&](int u, uint32_t j) {
 #pragma unroll
         for (int i = 0; i < RW; i++) {
-            wv[u][i] = *reinterpret_cast<const u32x4*>(wp[i] + static_cast<int64_t>(j) * 256);
+            wv[u][i] = *reinterpret_cast<const u32x4*>(wp[i] + static_cast<int64_t>(j) * 256 + 4 * lane);
 #pragma unroll
-            for (int g = 0; g < PER; g++) sv[u][i][g] = sp[i][(j * PER + g) * 16];
+            for (int g = 0; g < PER; g++) sv[u][i][g] = sp[i][(j * PER + g) * 16 + r];
         }
     };
-    auto load = [&](int u, uint32_t j) {
+    auto issue = [&](int u, uint32_t j) {
+        if constexpr (XR == 1)
+            dma4(xbase, xoff[0] + 256 * j, ring + u * SLOT);
+        else
+#pragma unroll
+            for (int q = 0; q < C::SENDS; q++) dma16(xbase, xoff[q] + 256 * j, ring + u * SLOT + q * 1024);
         load_w(u, j);
+    };
+    auto step = [&](int u) {
+        asm volatile("" : "+v"(wv[u][0])::"memory");  // W has come, and with it X
+        u32x4 x[CT][4];
 #pragma unroll
         for (int c = 0; c < CT; c++)
 #pragma unroll
-            for (int p = 0; p < 4; p++) {
-                xv[u][c][p] = u32x4{0, 0, 0, 0};
-                if (has[c]) xv[u][c][p] = *reinterpret_cast<const u32x4*>(xp[c] + static_cast<int64_t>(j) * 128 + 32 * p);
-            }
-    };
-    auto multiply = [&](int u) {
-        constexpr int P = 4 / PER;  // operands per group
-        const u32x4 kOnes = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-#pragma unroll
-        for (int g = 0; g < PER; g++) {
-            floatx4 sum[CT], d[RW][CT];
-#pragma unroll
-            for (int c = 0; c < CT; c++) {
-                sum[c] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int p = 0; p < P; p++)
-                    sum[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[u][c][g * P + p]),
-                                                                     __builtin_bit_cast(bf16x8, kOnes), sum[c], 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < RW; i++) {
-#pragma unroll
-                for (int c = 0; c < CT; c++) d[i][c] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int p = 0; p < P; p++) {
-                    const bf16x8 b = operand(wv[u][i][g * P + p]);
-#pragma unroll
-                    for (int c = 0; c < CT; c++)
-                        d[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[u][c][g * P + p]), b, d[i][c], 0, 0, 0);
-                }
-                const uint32_t meta = sv[u][i][g];
-                const float s = __uint_as_float(meta & ~15u), z = __uint_as_float(0x3F800000u | (meta & 15u) << 19);
-#pragma unroll
-                for (int c = 0; c < CT; c++)
-#pragma unroll
-                    for (int q = 0; q < RES; q++) acc[i][c][q] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[c][q], d[i][c][q]), acc[i][c][q]);
-            }
-        }
+            for (int p = 0; p < 4; p++) x[c][p] = *reinterpret_cast<const u32x4*>(mine + u * SLOT + c * 4096 + rd[p]);
+        multiply_tile<RW, CT, PER, RES>(k, x, wv[u], sv[u], acc);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     };
     const uint32_t full = static_cast<uint32_t>(a.K / 128);
-    if (static_cast<uint32_t>(wave) < full) {
-        const uint32_t last = full - 1;
+    // tiles first, first + stride, ...: the waves of all slices take neighbouring ones
+    const uint32_t first = blockIdx.z * NW + wave, stride = NW * a.slices;
+    const uint32_t count = full > first ? (full - first + stride - 1) / stride : 0;
+    if (count > 0) {
+        auto tile = [&](uint32_t i) { return first + stride * (i < count ? i : count - 1); };
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const uint32_t j = wave + u * NW;
-            load(u, j < last ? j : last);
-        }
-        for (uint32_t j = wave; j < full; j += U * NW)
+        for (int u = 0; u < U; u++) issue(u, tile(u));
+        uint32_t done = 0;
+        for (; done + U < count; done += U)
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                if (j + u * NW < full) multiply(u);
-                const uint32_t next = j + (u + U) * NW;
-                load(u, next < last ? next : last);
+                step(u);
+                issue(u, tile(done + U + u));
             }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (done + u < count) step(u);
     }
-    if (J > full && full % NW == static_cast<uint32_t>(wave)) {  // the tile that K ends inside
+    if (J > full && full % stride == first) {  // the tile that K ends inside
         load_w(0, full);
+        u32x4 x[CT][4];
 #pragma unroll
         for (int c = 0; c < CT; c++)
 #pragma unroll
             for (int p = 0; p < 4; p++) {
-                xv[0][c][p] = u32x4{0, 0, 0, 0};
-                if (has[c]) xv[0][c][p] = load_x(xp[c] - 8 * c4, static_cast<int64_t>(full) * 128 + 32 * p + 8 * c4, a.K);
+                const int row = 16 * c + xrow < rows ? 16 * c + xrow : rows - 1;
+                x[c][p] = load_x(x0 + static_cast<int64_t>(row) * a.ldx, static_cast<int64_t>(full) * 128 + 32 * p + 8 * c4, a.K);
             }
-        multiply(0);
+        multiply_tile<RW, CT, PER, RES>(k, x, wv[0], sv[0], acc);
     }
+    // every transfer has landed before the ring becomes the waves' meeting place
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
     for (int i = 0; i < RW; i++)
 #pragma unroll
         for (int c = 0; c < CT; c++)
 #pragma unroll
-            for (int q = 0; q < RES; q++) red[wave][i * CT + c][q][lane] = acc[i][c][q];
+            for (int q = 0; q < RES; q++) red[(((wave * RW + i) * CT + c) * RES + q) * 64 + lane] = acc[i][c][q];
     __syncthreads();
     for (int e = threadIdx.x; e < RT * CT * RES * 64; e += 64 * NW) {
-        const int l = e & 63, q = (e >> 6) % RES, tc = (e >> 6) / RES;  // tc = i * CT + c
-        const int64_t n = 16 * (static_cast<int64_t>(t0) + tc / CT) + (l & 15);
-        const int64_t m = FEW ? m0 + (l >> 4) : m0 + 16 * (tc % CT) + 4 * (l >> 4) + q;
-        if (n >= a.N || m >= a.M) continue;
-        float v = red[0][tc][q][l];
+        const int l = e & 63, q = (e >> 6) % RES, c = (e >> 6) / RES % CT, i = (e >> 6) / (RES * CT);
+        const int64_t n = 16 * (static_cast<int64_t>(t0) + i) + (l & 15);
+        const int row = XR >= 16 ? 16 * c + 4 * (l >> 4) + q : l >> 4;
+        if (n >= a.N || row >= rows) continue;
+        float v = 0.f, u = 0.f;
 #pragma unroll
-        for (int w = 1; w < NW; w++) v += red[w][tc][q][l];
-        v *= 16.f;
-        if constexpr (UP) {
-            float u = red[0][RT * CT + tc][q][l];
-#pragma unroll
-            for (int w = 1; w < NW; w++) u += red[w][RT * CT + tc][q][l];
-            v = silu_mul(v, 16.f * u);
+        for (int w = 0; w < NW; w++) {
+            v += red[(((w * RW + i) * CT + c) * RES + q) * 64 + l];
+            if constexpr (UP) u += red[(((w * RW + RT + i) * CT + c) * RES + q) * 64 + l];
         }
-        if (a.bf16)
-            static_cast<uint16_t*>(a.y)[m * a.ldy + n] = static_cast<uint16_t>(f32_to_bf16_rne(v));
-        else
-            static_cast<float*>(a.y)[m * a.ldy + n] = v;
+        if (a.part) {
+            float* part = a.part + (blockIdx.z * (UP ? 2 : 1) * a.M + m0 + row) * a.N + n;
+            part[0] = v;
+            if constexpr (UP) part[a.M * a.N] = u;
+        } else {
+            store_y(a, m0 + row, n, UP ? silu_mul(16.f * v, 16.f * u) : 16.f * v);
+        }
     }
 }
 
-template <int CT, int RT, int U, int NW, bool FEW, bool UP>
-uw_status launch_skinny(const W4Args& a, int32_t group, hipStream_t s)
+// Sum of the K slices' partial results, in slice order.
+template <bool UP>
+__global__ void __launch_bounds__(256) w4_join(W4Args a)
 {
-    const int64_t blocks = ((tiles16(a.N) + RT - 1) / RT) * ((a.M + (FEW ? 4 : 16 * CT) - 1) / (FEW ? 4 : 16 * CT));
-    if (blocks > kThreadsMost / (64 * NW)) return fail(UW_EUNSUPPORTED, "M x N too large for one launch");
-    const dim3 grid(static_cast<uint32_t>(blocks)), block(64 * NW);
-    if (group == 128)
-        hipLaunchKernelGGL((w4_skinny<CT, RT, U, NW, 1, FEW, UP>), grid, block, 0, s, a);
-    else if (group == 64)
-        hipLaunchKernelGGL((w4_skinny<CT, RT, U, NW, 2, FEW, UP>), grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL((w4_skinny<CT, RT, U, NW, 4, FEW, UP>), grid, block, 0, s, a);
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? UW_OK : fail(UW_EHIP, "4-bit product launch failed: %s", hipGetErrorString(e));
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, mn = a.M * a.N;
+    if (e >= mn) return;
+    float v = 0.f, u = 0.f;
+    for (uint32_t z = 0; z < a.slices; z++) {
+        v += a.part[z * (UP ? 2 : 1) * mn + e];
+        if constexpr (UP) u += a.part[(2 * z + 1) * mn + e];
+    }
+    store_y(a, e / a.N, e % a.N, UP ? silu_mul(16.f * v, 16.f * u) : 16.f * v);
+}
+
+template <int XR, int RT, int U, int NW, int PER, bool UP>
+hipError_t launch_skinny(const W4Args& a, uint32_t blocks, hipStream_t s)
+{
+    constexpr size_t lds = Skinny<XR, RT, U, NW, UP>::LDS;
+    static_assert(lds <= 160 * 1024, "LDS");
+    static uint64_t attr_done = 0;  // devices the LDS limit was raised on
+    const auto fn = w4_skinny<XR, RT, U, NW, PER, UP>;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds, attr_done);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(fn, dim3(blocks, 1, a.slices), dim3(64 * NW), lds, s, a);
+    return hipGetLastError();
+}
+
+template <int XR, int RT, int U, int NW, bool UP>
+hipError_t launch_skinny(const W4Args& a, int32_t group, hipStream_t s)
+{
+    const uint32_t blocks = static_cast<uint32_t>(((tiles16(a.N) + RT - 1) / RT) * ((a.M + XR - 1) / XR));
+    return group == 128  ? launch_skinny<XR, RT, U, NW, 1, UP>(a, blocks, s)
+           : group == 64 ? launch_skinny<XR, RT, U, NW, 2, UP>(a, blocks, s)
+                         : launch_skinny<XR, RT, U, NW, 4, UP>(a, blocks, s);
+}
+
+// Row tiles per workgroup and K slices of a product with more than four rows.
+//   Row tiles: more of them read X less often, and leave fewer workgroups. In cold us at K = 4096 (2000 for N = 5003), N = 4096 /
+//   5003 / 14336 with 1, 2 and 4 row tiles: M = 16 4.9 5.8 7.2 / 5.5 5.0 6.2 / 14.4 10.9 10.1, M = 32 6.0 7.1 9.9 / 7.3 6.3 7.7 /
+//   20.3 14.9 12.9, M = 64 9.6 10.1 13.7 / 14.8 9.4 11.9 / 35.9 23.6 17.9. So four where that leaves 192 workgroups or
+//   more, else two where that leaves 144.
+//   Slices: past 16 rows X's bytes, read once per row tile, are what a long K costs, so where four row tiles leave few
+//   workgroups, K is cut among them as long as every wave of eight keeps three tiles: M = 64, N = 4096, K = 14336 takes 22.5 us
+//   in four slices, 30.9 with one row tile per workgroup and none; M = 32 16.9 and 19.6. (At K = 4096 12.8 and 9.6.)
+struct W4Plan {
+    int rt;
+    uint32_t slices;
+};
+
+W4Plan w4_plan(int64_t M, int64_t N, int64_t K, bool up)
+{
+    const int64_t T = tiles16(N), mb = (M + 63) / 64;
+    const int64_t four = (T * (up ? 2 : 1) + 3) / 4 * mb, two = (T * (up ? 2 : 1) + 1) / 2 * mb;
+    if (four >= 192) return {4, 1};
+    if (M > 16 && four <= 128) {
+        int64_t s = 256 / four, most = tiles128(K) / 24;
+        s = s < most ? s : most;
+        if (s > 1) return {4, static_cast<uint32_t>(s < 8 ? s : 8)};
+    }
+    return {two >= 144 ? 2 : 1, 1};
+}
+
+// Bytes of the slices' partial sums.
+size_t w4_part_bytes(int64_t M, int64_t N, bool up, uint32_t slices)
+{
+    return slices > 1 ? static_cast<size_t>(slices) * (up ? 2 : 1) * M * N * sizeof(float) : 0;
+}
+
+template <int XR, int U, bool UP>
+hipError_t launch_planned(const W4Args& a, int rt, int32_t group, hipStream_t s)
+{
+    // (of each of two planes with UP, where two row tiles of one plane are the least)
+    if (rt == 4) return launch_skinny<XR, UP ? 2 : 4, U, 8, UP>(a, group, s);
+    if (!UP && rt == 2) return launch_skinny<XR, UP ? 1 : 2, U, 8, UP>(a, group, s);
+    return launch_skinny<XR, 1, U, 8, UP>(a, group, s);
 }
 
 template <bool UP>
-uw_status run_product(const W4Args& a, int32_t group, hipStream_t s)
+uw_status run_product(W4Args a, int32_t group, void* d_ws, size_t ws_bytes, hipStream_t s)
 {
-    if (a.M <= 4) return launch_skinny<1, 1, 2, 8, true, UP>(a, group, s);
-    if (a.M <= 16) return launch_skinny<1, 1, 2, 8, false, UP>(a, group, s);
-    if (a.M <= 32) return launch_skinny<2, UP ? 1 : 2, 1, 8, false, UP>(a, group, s);
-    return launch_skinny<4, UP ? 1 : 2, 1, 4, false, UP>(a, group, s);
+    hipError_t e;
+    if (tiles16(a.N) * ((a.M + 15) / 16) > kThreadsMost / 1024) return fail(UW_EUNSUPPORTED, "M x N too large for one launch");
+    if (a.M <= 4) {
+        // One row tile per workgroup; with few of those the CU is filled with waves instead. Cold us with 8 and 16 waves: M = 1,
+        // 4096 x 14336 (N x K) 9.7 and 8.5, 14336 x 4096 8.5 and 9.4, gate and up of that 13.6 and 17.2.
+        const bool wide = tiles16(a.N) < 512;
+        if (a.M == 1)
+            e = wide ? launch_skinny<1, 1, 2, 16, UP>(a, group, s) : launch_skinny<1, 1, 2, 8, UP>(a, group, s);
+        else
+            e = wide ? launch_skinny<4, 1, 2, 16, UP>(a, group, s) : launch_skinny<4, 1, 2, 8, UP>(a, group, s);
+    } else {
+        const W4Plan p = w4_plan(a.M, a.N, a.K, UP);
+        int rt = p.rt;
+        a.slices = p.slices;
+        while (a.slices > 1 && (!d_ws || w4_part_bytes(a.M, a.N, UP, a.slices) > ws_bytes)) a.slices--;
+        if (p.slices > 1 && a.slices == 1) rt = 1;
+        a.part = a.slices > 1 ? static_cast<float*>(d_ws) : nullptr;
+        if (a.M <= 16)
+            e = launch_planned<16, 2, UP>(a, rt, group, s);
+        else if (a.M <= 32)
+            e = launch_planned<32, 1, UP>(a, rt, group, s);
+        else
+            e = launch_planned<64, 1, UP>(a, rt, group, s);
+        if (e == hipSuccess && a.slices > 1) {
+            hipLaunchKernelGGL(w4_join<UP>, dim3(static_cast<uint32_t>((a.M * a.N + 255) / 256)), dim3(256), 0, s, a);
+            e = hipGetLastError();
+        }
+    }
+    return e == hipSuccess ? UW_OK : fail(UW_EHIP, "4-bit product launch failed: %s", hipGetErrorString(e));
 }
 
 uw_status check_plane(int64_t N, int64_t K, int32_t group)
@@ -439,6 +589,7 @@ uw_status product(const uw_w4_args* p, bool up, void* stream)
         return fail(UW_EINVAL, "X, planes and workspace must be 16-byte aligned");
     if (!aligned(p->d_y, p->y_type == UW_BF16 ? 2 : 4)) return fail(UW_EINVAL, "d_y must be aligned to its elements");
     if (p->ldx < p->K || p->ldx % 8) return fail(UW_EINVAL, "ldx must be >= K and a multiple of 8");
+    if (p->ldx > kMostLd) return fail(UW_EUNSUPPORTED, "ldx over 2^26");
     if (p->ldy < p->N) return fail(UW_EINVAL, "ldy must be >= N");
     W4Args a{};
     a.x = p->d_x;
@@ -453,8 +604,9 @@ uw_status product(const uw_w4_args* p, bool up, void* stream)
     a.J = tiles128(p->K);
     a.meta = tiles16(p->N) * a.J * 256;
     a.bf16 = p->y_type == UW_BF16;
+    a.slices = 1;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    return up ? run_product<true>(a, p->group, s) : run_product<false>(a, p->group, s);
+    return up ? run_product<true>(a, p->group, p->d_ws, p->ws_bytes, s) : run_product<false>(a, p->group, p->d_ws, p->ws_bytes, s);
 }
 
 }  // namespace
@@ -524,8 +676,6 @@ uw_status uw_w4_gate_up(const uw_w4_args* args, void* stream)
 size_t uw_w4_gemm_workspace(int64_t M, int64_t N, int64_t K)
 {
     clear_error();
-    (void)M;
-    (void)N;
-    (void)K;
-    return 0;
+    if (M < 5 || M > INT32_MAX || check_plane(N, K, 128) != UW_OK) return 0;
+    return w4_part_bytes(M, N, false, w4_plan(M, N, K, false).slices);
 }

@@ -651,8 +651,8 @@ size_t uw_sample_workspace(int64_t M, int64_t V);
  * when the call's work is done; calls that overlap need one each.
  * Errors: UW_ESHAPE (M < 0, N or K < 1), UW_EINVAL (NULL or misaligned pointers: 16 bytes; d_y and d_h only that of
  * their elements; a leading dimension too small or not the multiple named; an unknown type or group; zeros not 0 or 1),
- * UW_EUNSUPPORTED (N or K over 2^24, M over 2^31 - 1, more than one launch takes), UW_EHIP. M = 0 is a no-op. Buffers must not
- * overlap, but that Wg and Wu may be the same plane.
+ * UW_EUNSUPPORTED (N or K over 2^24, M over 2^31 - 1, ldx over 2^26, more than one launch takes), UW_EHIP. M = 0 is a no-op.
+ * Buffers must not overlap, but that Wg and Wu may be the same plane.
  */
 size_t uw_w4_plane_bytes(int64_t N, int64_t K, int32_t group); /* 0 for arguments that the calls refuse */
 uw_status uw_w4_quantize(const void* d_w, int32_t w_type, int64_t N, int64_t K, int64_t ldw, int32_t group, int32_t zeros,

@@ -197,6 +197,43 @@ def test_gemm_of_whole_numbers_is_exact(M, N, K, group, zeros):
             assert torch.equal(y[:M, :N].cpu(), torch.from_numpy(want).to(out))
 
 
+@pytest.mark.parametrize("M,N,K,group", [(17, 40, 6144, 128), (33, 100, 6500, 32), (64, 96, 14336, 128), (64, 4096, 6300, 64), (130, 33, 25000, 128)])
+def test_products_in_slices(M, N, K, group):
+    """K cut among workgroups, in as many slices as the workspace given has room for, none past its end."""
+    torch, uw = torch_cuda(), _uw()
+    rng = np.random.default_rng(M + N + K)
+    x = rng.integers(-2, 3, (M, K)).astype(np.float32)
+    sides = []
+    for _ in range(2):
+        _, q, s, z = _whole(rng, 1, N, K, group, True)
+        sides.append((put_plane(plane_of(q, s, z, N, K, group)), x.astype(np.float64) @ values_of(q, s, z, K).T))
+    ldx = _up(K, 8)
+    d_x = upload(x, torch.bfloat16, ldx)
+    need = uw.w4_gemm_workspace(M, N, K)
+    assert need > 0 and need % (4 * M * N) == 0
+    for given in (need, need - 4, 8 * M * N, 0):
+        ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+        y = torch.full((M, N + 1), 77.0, device="cuda")
+        log(f"  slices {M}x{N}x{K} workspace {given} of {need}")
+        uw.w4_gemm(d_x, sides[0][0], y, M, N, K, group=group, ldx=ldx, ldy=N + 1, d_ws=ws, ws_bytes=given)
+        assert torch.equal(y[:, :N].cpu().double(), torch.from_numpy(sides[0][1])) and (y[:, N] == 77).all()
+        assert (ws[given:] == 255).all()
+    two = uw.w4_gemm_workspace(M, 2 * N, K)
+    g, u = sides[0][1] / 4096, sides[1][1] / 4096
+    d_x = upload(x / 4096, torch.bfloat16, ldx)  # a power of two: the products stay exact
+    want = g / (1 + np.exp(-g)) * u
+    hs = []
+    for given in (two, 0):
+        ws = torch.full((two + 64,), 255, dtype=torch.uint8, device="cuda")
+        h = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+        uw.w4_gate_up(d_x, sides[0][0], sides[1][0], h, M, N, K, group=group, ldx=ldx, d_ws=ws, ws_bytes=given)
+        assert (ws[given:] == 255).all()
+        hs.append(h)
+    assert torch.equal(*hs)
+    err = np.abs(hs[0].double().cpu().numpy() - want)
+    assert (err <= np.abs(want) * (2.0**-8 + 8 * 2.0**-24) + 2.0**-133).all()
+
+
 def _tolerance(x, s, K, group):
     """A = sum of 16 s |x| per output, times the steps of its sums."""
     M, G = x.shape[0], s.shape[1]
