@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import struct
 
 import numpy as np
 
@@ -173,6 +174,20 @@ class LogprobsArgs(ctypes.Structure):
     ]
 
 
+_FORMATS = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "P", ctypes.c_size_t: "N"}
+
+
+def _packer(cls):
+    """Packs a structure's fields, in order, into bytes that a pointer argument takes: a third of the time that filling the
+    ctypes structure costs, on calls whose host share counts. Pointers are ints, 0 for NULL."""
+    p = struct.Struct("@" + "".join(_FORMATS[t] for _, t in cls._fields_))
+    assert p.size <= ctypes.sizeof(cls) < p.size + 8
+    return p.pack
+
+
+_pack_w4, _pack_block_norm, _pack_logprobs = _packer(W4Args), _packer(BlockNormArgs), _packer(LogprobsArgs)
+
+
 class BundleItem(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("blob", ctypes.c_void_p), ("blob_bytes", ctypes.c_size_t)]
 
@@ -268,11 +283,11 @@ def _load():
         "uw_w4_plane_bytes": ([i64, i64, i32], sz),
         "uw_w4_quantize": ([P, i32, i64, i64, i64, i32, i32, P, P], ctypes.c_int),
         "uw_w4_expand": ([P, i64, i64, i32, P, i32, i64, P], ctypes.c_int),
-        "uw_w4_gemm": ([ctypes.POINTER(W4Args), P], ctypes.c_int),
-        "uw_w4_gate_up": ([ctypes.POINTER(W4Args), P], ctypes.c_int),
+        "uw_w4_gemm": ([P, P], ctypes.c_int),
+        "uw_w4_gate_up": ([P, P], ctypes.c_int),
         "uw_w4_gemm_workspace": ([i64, i64, i64], sz),
-        "uw_block_norm": ([ctypes.POINTER(BlockNormArgs), P], ctypes.c_int),
-        "uw_logprobs": ([ctypes.POINTER(LogprobsArgs), P], ctypes.c_int),
+        "uw_block_norm": ([P, P], ctypes.c_int),
+        "uw_logprobs": ([P, P], ctypes.c_int),
         "uw_logprobs_workspace": ([i64, i64, i32], sz),
     }
     for name, (args, res) in sigs.items():
@@ -573,13 +588,22 @@ def w4_plane_bytes(N: int, K: int, group: int = 128) -> int:
     return lib.uw_w4_plane_bytes(N, K, group)
 
 
-def _plane(name: str, t, N: int, K: int, group: int):
-    """Address of a plane, whose tensor must be as large as the sizes say and in one piece."""
+def _at(t) -> int:
+    """Address of a tensor or a raw one, 0 for None."""
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        return t or 0
+
+
+def _plane(name: str, t, N: int, K: int, group: int) -> int:
+    """Address of a plane, whose tensor must be as large as the sizes say (w4_plane_bytes) and in one piece."""
     if t is None or isinstance(t, int):
-        return t
-    need = lib.uw_w4_plane_bytes(N, K, group)
-    if not t.is_contiguous() or t.numel() * t.element_size() < need:
-        raise ValueError(f"{name} must be a contiguous tensor of {need} bytes")
+        return t or 0
+    if group in (32, 64, 128):  # others are the library's to refuse
+        need = (N + 15) // 16 * ((K + 127) // 128) * (1024 + 8192 // group)
+        if t.nbytes < need or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of {need} bytes")
     return t.data_ptr()
 
 
@@ -606,27 +630,53 @@ def w4_gemm(d_x, d_plane, d_y, M: int, N: int, K: int, group: int = 128, ldx: in
             y_type: int | None = None, d_ws=None, ws_bytes: int = 0, stream=None) -> None:
     """uw_w4_gemm: Y [M][N] (fp32 or bf16, by the dtype of d_y unless y_type is given) = X W^T, X bf16 [M][K], W a plane
     of 4-bit weights. d_ws: w4_gemm_workspace(M, N, K) bytes; with fewer K is cut into fewer slices, without it never."""
-    a = W4Args(M, N, K, group, _bf16("d_x", d_x), K if ldx is None else ldx, _plane("d_plane", d_plane, N, K, group), None, _ptr(d_y),
-               N if ldy is None else ldy, _type(d_y, y_type), _ptr(d_ws), ws_bytes)
-    _launch(d_x, stream, lib.uw_w4_gemm, ctypes.byref(a))
+    a = _pack_w4(M, N, K, group, _bf16("d_x", d_x), K if ldx is None else ldx, _plane("d_plane", d_plane, N, K, group), 0, _at(d_y),
+                 N if ldy is None else ldy, _type(d_y, y_type), _at(d_ws), ws_bytes)
+    _launch(d_x, stream, lib.uw_w4_gemm, a)
 
 
 def w4_gate_up(d_x, d_gate, d_up, d_h, M: int, N: int, K: int, group: int = 128, ldx: int | None = None,
                ldh: int | None = None, d_ws=None, ws_bytes: int = 0, stream=None) -> None:
     """uw_w4_gate_up: h [M][N] (bf16) = silu(X Wg^T) * (X Wu^T), both weights planes of N x K with the same group. d_ws:
     w4_gemm_workspace(M, 2 * N, K) bytes, as for w4_gemm."""
-    a = W4Args(M, N, K, group, _bf16("d_x", d_x), K if ldx is None else ldx, _plane("d_gate", d_gate, N, K, group),
-               _plane("d_up", d_up, N, K, group), _bf16("d_h", d_h), N if ldh is None else ldh, BF16, _ptr(d_ws), ws_bytes)
-    _launch(d_x, stream, lib.uw_w4_gate_up, ctypes.byref(a))
+    a = _pack_w4(M, N, K, group, _bf16("d_x", d_x), K if ldx is None else ldx, _plane("d_gate", d_gate, N, K, group),
+                 _plane("d_up", d_up, N, K, group), _bf16("d_h", d_h), N if ldh is None else ldh, BF16, _at(d_ws), ws_bytes)
+    _launch(d_x, stream, lib.uw_w4_gate_up, a)
 
 
-def _bf16(name: str, t):
+def _bf16(name: str, t) -> int:
     """Address of bf16 values; a tensor of another type would be misread."""
     if t is None or isinstance(t, int):
-        return t
+        return t or 0
     if _type(t, None) != BF16:
         raise ValueError(f"{name} must be bf16, not {t.dtype}")
     return t.data_ptr()
+
+
+def _same_type(name: str, given, tensors) -> int:
+    """The uw_type of all tensors, unless given; F32 where there are none."""
+    if given is not None:
+        return given
+    first = None
+    for t in tensors:
+        if t is None:
+            continue
+        of = getattr(t, "dtype", None)
+        if first is None:
+            first, kind = of, _TYPES[of] if of in _TYPES else _type(t, None)
+        elif of is not first and _type(t, None) != kind:
+            raise ValueError(f"{name}: tensors of different types")
+    return F32 if first is None else kind
+
+
+def _vector(name: str, t) -> int:
+    """Address of a vector's values, which lie one after another."""
+    try:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must have its values one after another")
+        return t.data_ptr()
+    except AttributeError:
+        return t or 0
 
 
 def block_norm(d_y, d_r, d_r_out, M: int, K: int, d_h=None, d_q=None, d_s=None, post: int = NORM_RMS, d_post_w=None,
@@ -640,31 +690,21 @@ def block_norm(d_y, d_r, d_r_out, M: int, K: int, d_h=None, d_q=None, d_s=None, 
     follow the tensors unless given; d_r and d_r_out have one, and weights, biases and gate have one."""
     if d_h is not None and d_q is not None:
         raise ValueError("d_h and d_q: h is either values or codes")
-    vectors = [v for v in (d_post_w, d_post_b, d_pre_w, d_pre_b, d_gate) if v is not None]
-
-    def kind(name, given, *tensors):
-        types = {_type(t, None) for t in tensors if t is not None and not isinstance(t, int)} if given is None else {given}
-        if len(types) > 1:
-            raise ValueError(f"{name}: tensors of different types")
-        if not types and any(t is not None for t in tensors):
-            _type(None, None)
-        return types.pop() if types else F32
-
-    for name, v in (("d_post_w", d_post_w), ("d_post_b", d_post_b), ("d_pre_w", d_pre_w), ("d_pre_b", d_pre_b)):
-        if v is not None and not isinstance(v, int) and v.stride(-1) != 1 and K > 1:
-            raise ValueError(f"{name} must have its values one after another")
-    h = d_h if d_q is None else d_q
-    if d_q is not None:
-        h_type = E4M3
+    if d_q is None:
+        h, h_type = d_h, _same_type("d_h", h_type, (d_h,))
+    else:
+        h, h_type = d_q, E4M3
         if not isinstance(d_q, int) and d_q.element_size() != 1:
             raise ValueError(f"d_q must hold bytes, not {d_q.dtype}")
-    a = BlockNormArgs(
-        M, K, _ptr(d_y), K if ldy is None else ldy, kind("d_y", y_type, d_y), _ptr(d_r), K if ldr is None else ldr,
-        kind("d_r and d_r_out", r_type, d_r, d_r_out), _ptr(d_r_out), K if ldr_out is None else ldr_out, post, pre, _ptr(d_post_w),
-        _ptr(d_post_b), _ptr(d_pre_w), _ptr(d_pre_b), _ptr(d_gate), gate_rows, K if ldgate is None else ldgate,
-        kind("weights, biases and gate", w_type, *vectors), w_add, scale_y, scale_r, eps, _ptr(h), K if ldh is None else ldh,
-        kind("d_h", h_type, h), _ptr(d_s), M if lds is None else lds)
-    _launch(d_y if d_y is not None else d_r, stream, lib.uw_block_norm, ctypes.byref(a))
+    w_type = _same_type("weights, biases and gate", w_type, (d_post_w, d_post_b, d_pre_w, d_pre_b, d_gate))
+    a = _pack_block_norm(
+        M, K, _at(d_y), K if ldy is None else ldy, _same_type("d_y", y_type, (d_y,)), _at(d_r), K if ldr is None else ldr,
+        _same_type("d_r and d_r_out", r_type, (d_r, d_r_out)), _at(d_r_out), K if ldr_out is None else ldr_out, post, pre,
+        0 if d_post_w is None else _vector("d_post_w", d_post_w), 0 if d_post_b is None else _vector("d_post_b", d_post_b),
+        0 if d_pre_w is None else _vector("d_pre_w", d_pre_w), 0 if d_pre_b is None else _vector("d_pre_b", d_pre_b), 0 if d_gate is None else _at(d_gate),
+        gate_rows, K if ldgate is None else ldgate, w_type, w_add, scale_y, scale_r, eps, _at(h), K if ldh is None else ldh, h_type,
+        _at(d_s), M if lds is None else lds)
+    _launch(d_y if d_y is not None else d_r, stream, lib.uw_block_norm, a)
 
 
 def logprobs_workspace(M: int, V: int, n_top: int = 0) -> int:
@@ -679,12 +719,12 @@ def logprobs(d_logits, M: int, V: int, d_token=None, d_logprob=None, d_rank=None
     output may be None. d_ws: logprobs_workspace(M, V, n_top) bytes. A ValueError for tensors of other types and strided ones."""
     if n_top == 0:  # empty tensors are no lists
         d_top_token = d_top_logprob = None
-    a = LogprobsArgs(M, V, _ptr(d_logits), V if ld is None else ld, _type(d_logits, type), _elements("d_token", d_token, M, True),
-                     _elements("d_temperature", d_temperature, M), _elements("d_logprob", d_logprob, M),
-                     _elements("d_rank", d_rank, M, True), _elements("d_entropy", d_entropy, M), n_top,
-                     _elements("d_top_token", d_top_token, M * n_top, True), _elements("d_top_logprob", d_top_logprob, M * n_top),
-                     _ptr(d_ws), ws_bytes)
-    _launch(d_logits, stream, lib.uw_logprobs, ctypes.byref(a))
+    a = _pack_logprobs(M, V, _at(d_logits), V if ld is None else ld, _type(d_logits, type), _elements("d_token", d_token, M, True) or 0,
+                       _elements("d_temperature", d_temperature, M) or 0, _elements("d_logprob", d_logprob, M) or 0,
+                       _elements("d_rank", d_rank, M, True) or 0, _elements("d_entropy", d_entropy, M) or 0, n_top,
+                       _elements("d_top_token", d_top_token, M * n_top, True) or 0,
+                       _elements("d_top_logprob", d_top_logprob, M * n_top) or 0, _at(d_ws), ws_bytes)
+    _launch(d_logits, stream, lib.uw_logprobs, a)
 
 
 def proj(h: Header, d_blob, pipeline: int = PIPE_DIRECT, d_direct=None, variant: int = -1, split_k: int = 0) -> Proj:

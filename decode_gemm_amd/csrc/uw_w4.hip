@@ -47,91 +47,150 @@ __device__ __forceinline__ float round20(double v)
     return static_cast<float>(__longlong_as_double(static_cast<long long>(r)));
 }
 
-template <int LANES>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t a)
+// Maximum over 4, 8 or 16 neighbouring lanes: pairs, quads, then mirrored halves and rows.
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t v)
 {
-#pragma unroll
-    for (int d = 1; d < LANES; d *= 2) {
-        const uint32_t o = __shfl_xor(a, d);
-        a = a > o ? a : o;
-    }
-    return a;
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, false));
 }
-template <int LANES>
-__device__ __forceinline__ float lanes_maxf(float a)
+template <int CTRL>
+__device__ __forceinline__ uint32_t larger(uint32_t v)
 {
-#pragma unroll
-    for (int d = 1; d < LANES; d *= 2) a = fmaxf(a, __shfl_xor(a, d));
-    return a;
+    const uint32_t o = moved<CTRL>(v);
+    return v > o ? v : o;
+}
+template <int CTRL>
+__device__ __forceinline__ float larger(float v)
+{
+    return fmaxf(v, __uint_as_float(moved<CTRL>(__float_as_uint(v))));
+}
+template <int LANES, class V>
+__device__ __forceinline__ V lanes_max(V v)
+{
+    v = larger<0xB1>(v);
+    v = larger<0x4E>(v);
+    if constexpr (LANES > 4) v = larger<0x141>(v);
+    if constexpr (LANES > 8) v = larger<0x140>(v);
+    return v;
 }
 
-// w / s rounded to the nearest whole number, ties to even, for s of 20 bits and |w / s| <= 15.5: the product with 1 / s is
-// at most one off, and the residual w - i s, exact, tells.
+// a / 7 to 20 significant bits, the nearest, ties to even, for a >= 2^-100: the product with 1 / 7 rounded to 20 bits is at most
+// one step off, and the residual a - 7 c, exact, tells.
+__device__ __forceinline__ float seventh20(float a)
+{
+    const uint32_t c = (__float_as_uint(a * (1.0f / 7.0f)) + 8) & ~15u;
+    const float v = __uint_as_float(c), u = __uint_as_float((c & 0x7F800000u) - (19u << 23));  // a step of 20 bits
+    const float e = __builtin_fmaf(-7.0f, v, a), h = 3.5f * u;
+    return fabsf(e) > h || (fabsf(e) == h && (c & 16)) ? v + __builtin_copysignf(u, e) : v;
+}
+
+// w / s rounded to fp32 and then, by adding 1.5 * 2^23, to the nearest whole number, ties to even, which is left with that
+// number. The quotient is the correctly rounded one (inv = 1 / s is, and one residual step corrects it; s is not so small that the
+// residual underflows). Rounding twice is no loss: s has 20 bits, so T s is exact for a T halfway between two whole numbers
+// up to 15 and lies on w's grid, and a w beside it is a step of w away, more than half a step of the quotient.
+constexpr float kWhole = 12582912.0f;
 __device__ __forceinline__ float whole_quotient(float w, float s, float inv)
 {
-    const float i = __builtin_rintf(w * inv), e = __builtin_fmaf(-i, s, w), h = 0.5f * s;
-    const bool odd = (static_cast<int>(i) & 1) != 0;
-    return fabsf(e) > h || (fabsf(e) == h && odd) ? i + __builtin_copysignf(1.0f, e) : i;
+    const float q = w * inv;
+    return __builtin_fmaf(__builtin_fmaf(-q, s, w), inv, q) + kWhole;
 }
 
-// One 16 x 128 tile per workgroup, 8 values per thread: row threadIdx / 16, octet threadIdx % 16.
-template <class T, int GROUP, bool ZEROS>
-__global__ void __launch_bounds__(256) w4_quantize_kernel(PlaneArgs a)
+// Eight codes of values v as a plane's word. A word's sum takes over each whole number with the bits of 1.5 * 2^23 above it, the
+// same for every value and taken off at once.
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[8], float s, float inv, float z)
 {
-    constexpr int LANES = GROUP / 8, PER = 128 / GROUP;
-    const int64_t tile = blockIdx.x, t = tile / a.J, j = tile % a.J;
-    const int r = threadIdx.x >> 4, o = threadIdx.x & 15;
-    const int64_t n = 16 * t + r, k = 128 * j + 8 * o;
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = 0.f;
-    if (n < a.N && k < a.K) load8(static_cast<const T*>(a.w) + n * a.ldw, k, a.K, v);
-    uint32_t top = 0;  // of |v|; infinities and NaN are the largest
-    float hi = 0.f, lo = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-        top = top > b ? top : b;
-        hi = fmaxf(hi, v[i]);
-        lo = fmaxf(lo, -v[i]);
-    }
-    top = lanes_max<LANES>(top);
-    float s = 1.f, z = 8.f;
-    if constexpr (ZEROS) {
-        hi = lanes_maxf<LANES>(hi);
-        lo = lanes_maxf<LANES>(lo);
-        const double d = (static_cast<double>(hi) + static_cast<double>(lo)) / 15.0;
-        if (top != 0) s = fmaxf(round20(d), FLT_MIN);
-        z = fminf(whole_quotient(lo, s, 1.0f / s), 15.f);
-    } else {
-        if (top != 0) s = fmaxf(round20(static_cast<double>(__uint_as_float(top)) / 7.0), FLT_MIN);
-    }
-    const bool broken = top >= 0x7F800000u;
-    const float inv = 1.0f / s;
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        const float q = broken ? 0.f : fminf(fmaxf(whole_quotient(v[i], s, inv) + z, 0.f), 15.f);
-        if (n < a.N && k + i < a.K) word |= static_cast<uint32_t>(static_cast<int>(q)) << (4 * (i / 2) + 16 * (i & 1));
+        const int at = 4 * (i / 2) + 16 * (i & 1);
+        word += __float_as_uint(__builtin_amdgcn_fmed3f(whole_quotient(v[i], s, inv) + z, kWhole, kWhole + 15.0f)) << at;
+        word -= 0x4B400000u << at;
     }
-    a.plane[tile * 256 + 4 * (16 * (o & 3) + r) + (o >> 2)] = word;
-    if (o % LANES == 0) {
-        const uint32_t bits = broken ? 0x7FC00000u : __float_as_uint(s);
-        a.plane[a.meta + (tile * PER + o / LANES) * 16 + r] =
-            n < a.N && k < a.K ? bits | static_cast<uint32_t>(broken ? 0 : static_cast<int>(z)) : 0u;
+    return word;
+}
+
+// TJ 16 x 128 tiles, one after another in K, per workgroup, 8 values of each per thread: row threadIdx / 16, octet
+// threadIdx % 16. Bound by HBM: FIGQ
+template <class T, int GROUP, bool ZEROS, int TJ>
+__global__ void __launch_bounds__(256) w4_quantize_kernel(PlaneArgs a)
+{
+    constexpr int LANES = GROUP / 8, PER = 128 / GROUP;
+    const uint32_t runs = static_cast<uint32_t>((a.J + TJ - 1) / TJ);
+    const int64_t t = blockIdx.x / runs, j0 = static_cast<int64_t>(blockIdx.x % runs) * TJ;
+    const int r = threadIdx.x >> 4, o = threadIdx.x & 15;
+    const int64_t n = 16 * t + r;
+    float v[TJ][8];
+#pragma unroll
+    for (int u = 0; u < TJ; u++) {
+        const int64_t k = 128 * (j0 + u) + 8 * o;
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[u][i] = 0.f;
+        if (n < a.N && k < a.K) load8(static_cast<const T*>(a.w) + n * a.ldw, k, a.K, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < TJ; u++) {
+        if (j0 + u >= a.J) break;
+        const int64_t tile = t * a.J + j0 + u, k = 128 * (j0 + u) + 8 * o;
+        uint32_t top = 0;  // of |v|; infinities and NaN are the largest
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const uint32_t b = __float_as_uint(v[u][i]) & 0x7FFFFFFFu;
+            top = top > b ? top : b;
+        }
+        top = lanes_max<LANES>(top);
+        float s = 1.f, z = 8.f, lowest = 0.f;
+        if constexpr (ZEROS) {
+            float hi = 0.f, lo = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                hi = fmaxf(hi, v[u][i]);
+                lo = fmaxf(lo, -v[u][i]);
+            }
+            hi = lanes_max<LANES>(hi);
+            lowest = lo = lanes_max<LANES>(lo);
+            if (top != 0) s = fmaxf(round20((static_cast<double>(hi) + static_cast<double>(lo)) / 15.0), FLT_MIN);
+        } else if (top != 0) {
+            const float a7 = __uint_as_float(top);
+            s = seventh20(a7);
+            if (__builtin_expect(a7 < 0x1p-100f, 0)) s = fmaxf(round20(static_cast<double>(a7) / 7.0), FLT_MIN);
+        }
+        const bool broken = top >= 0x7F800000u;
+        // below 2^-80 all is taken 2^64 times as large, which changes no quotient
+        const bool small = s < 0x1p-80f;
+        const float k64 = small ? 0x1p64f : 1.0f, sk = s * k64, inv = 1.0f / sk;
+        if (__builtin_expect(__any(small), 0))
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[u][i] *= k64;
+        if constexpr (ZEROS) z = fminf(whole_quotient(lowest * k64, sk, inv) - kWhole, 15.f);
+        uint32_t word = broken ? 0u : codes_of(v[u], sk, inv, z);
+        if (n >= a.N || k + 8 > a.K) {  // what is past the matrix is 0
+            uint32_t keep = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (n < a.N && k + i < a.K) keep |= 15u << (4 * (i / 2) + 16 * (i & 1));
+            word &= keep;
+        }
+        a.plane[tile * 256 + 4 * (16 * (o & 3) + r) + (o >> 2)] = word;
+        if (o % LANES == 0) {
+            const uint32_t bits = broken ? 0x7FC00000u : __float_as_uint(s) | static_cast<uint32_t>(static_cast<int>(z));
+            a.plane[a.meta + (tile * PER + o / LANES) * 16 + r] = n < a.N && k < a.K ? bits : 0u;
+        }
     }
 }
 
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ void store_values(uint16_t* w, int64_t k, int64_t K, const float (&v)[8])
 {
-    if (k + 8 <= K) {
-        u32x4 p;
+    u32x4 p;
 #pragma unroll
-        for (int i = 0; i < 4; i++) p[i] = f32_to_bf16_rne(v[2 * i]) | (f32_to_bf16_rne(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; i++) p[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(floatx2{v[2 * i], v[2 * i + 1]}, bf16x2));
+    if (k + 8 <= K) {
         *reinterpret_cast<u32x4*>(w + k) = p;
     } else {
         for (int i = 0; i < 8; i++)
-            if (k + i < K) w[k + i] = static_cast<uint16_t>(f32_to_bf16_rne(v[i]));
+            if (k + i < K) w[k + i] = static_cast<uint16_t>(p[i / 2] >> (16 * (i & 1)));
     }
 }
 __device__ __forceinline__ void store_values(float* w, int64_t k, int64_t K, const float (&v)[8])
@@ -145,23 +204,35 @@ __device__ __forceinline__ void store_values(float* w, int64_t k, int64_t K, con
     }
 }
 
-// s (q - z): a 20-bit number times a 4-bit one, exact in fp32.
-template <class T, int GROUP>
+// s q - z s: z s is a 20-bit number times a 4-bit one, exact in fp32, and so is the difference, rounded by the fma not at all. The
+// same tiles and threads as the quantizer's. FIGE
+template <class T, int GROUP, int TJ>
 __global__ void __launch_bounds__(256) w4_expand_kernel(PlaneArgs a)
 {
     constexpr int PER = 128 / GROUP, LANES = GROUP / 8;
-    const int64_t tile = blockIdx.x, t = tile / a.J, j = tile % a.J;
+    const uint32_t runs = static_cast<uint32_t>((a.J + TJ - 1) / TJ);
+    const int64_t t = blockIdx.x / runs, j0 = static_cast<int64_t>(blockIdx.x % runs) * TJ;
     const int r = threadIdx.x >> 4, o = threadIdx.x & 15;
-    const int64_t n = 16 * t + r, k = 128 * j + 8 * o;
-    if (n >= a.N || k >= a.K) return;
-    const uint32_t word = a.plane[tile * 256 + 4 * (16 * (o & 3) + r) + (o >> 2)];
-    const uint32_t meta = a.plane[a.meta + (tile * PER + o / LANES) * 16 + r];
-    const float s = __uint_as_float(meta & ~15u);
-    const int z = static_cast<int>(meta & 15u);
-    float v[8];
+    const int64_t n = 16 * t + r;
+    if (n >= a.N) return;
+    uint32_t word[TJ], meta[TJ];
 #pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = static_cast<float>(static_cast<int>((word >> (4 * (i / 2) + 16 * (i & 1))) & 15u) - z) * s;
-    store_values(static_cast<T*>(a.out) + n * a.ldw, k, a.K, v);
+    for (int u = 0; u < TJ; u++) {
+        const int64_t tile = t * a.J + (j0 + u < a.J ? j0 + u : a.J - 1);
+        word[u] = a.plane[tile * 256 + 4 * (16 * (o & 3) + r) + (o >> 2)];
+        meta[u] = a.plane[a.meta + (tile * PER + o / LANES) * 16 + r];
+    }
+#pragma unroll
+    for (int u = 0; u < TJ; u++) {
+        const int64_t k = 128 * (j0 + u) + 8 * o;
+        if (k >= a.K) break;
+        const float s = __uint_as_float(meta[u] & ~15u), zs = -static_cast<float>(meta[u] & 15u) * s;
+        const uint32_t even = word[u] & 0x0F0F0F0Fu, odd = (word[u] >> 4) & 0x0F0F0F0Fu;  // values 0 4 1 5 and 2 6 3 7
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = __builtin_fmaf(static_cast<float>(((i & 2 ? odd : even) >> (8 * (i / 4) + 16 * (i & 1))) & 255u), s, zs);
+        store_values(static_cast<T*>(a.out) + n * a.ldw, k, a.K, v);
+    }
 }
 
 // ------------------------------------------------------------------------------ product
@@ -542,36 +613,45 @@ PlaneArgs plane_args(const void* plane, int64_t N, int64_t K, int64_t ldw)
     return a;
 }
 
+// Four tiles per workgroup where there are enough of them (FIGT), else one.
+template <int TJ>
+dim3 plane_grid(const PlaneArgs& a)
+{
+    return dim3(static_cast<uint32_t>(tiles16(a.N) * ((a.J + TJ - 1) / TJ)));
+}
+bool long_runs(const PlaneArgs& a) { return a.J >= 4 && tiles16(a.N) * a.J >= 8192; }
+
+template <class T, int GROUP, bool ZEROS>
+void launch_quantize(const PlaneArgs& a, hipStream_t s)
+{
+    if (long_runs(a))
+        hipLaunchKernelGGL((w4_quantize_kernel<T, GROUP, ZEROS, 4>), plane_grid<4>(a), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((w4_quantize_kernel<T, GROUP, ZEROS, 1>), plane_grid<1>(a), dim3(256), 0, s, a);
+}
 template <class T, int GROUP>
 void launch_quantize(const PlaneArgs& a, bool zeros, hipStream_t s)
 {
-    const dim3 grid(static_cast<uint32_t>(tiles16(a.N) * a.J));
-    if (zeros)
-        hipLaunchKernelGGL((w4_quantize_kernel<T, GROUP, true>), grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((w4_quantize_kernel<T, GROUP, false>), grid, dim3(256), 0, s, a);
+    zeros ? launch_quantize<T, GROUP, true>(a, s) : launch_quantize<T, GROUP, false>(a, s);
 }
 template <class T>
 void launch_quantize(const PlaneArgs& a, int32_t group, bool zeros, hipStream_t s)
 {
-    if (group == 128)
-        launch_quantize<T, 128>(a, zeros, s);
-    else if (group == 64)
-        launch_quantize<T, 64>(a, zeros, s);
-    else
-        launch_quantize<T, 32>(a, zeros, s);
+    group == 128 ? launch_quantize<T, 128>(a, zeros, s) : group == 64 ? launch_quantize<T, 64>(a, zeros, s) : launch_quantize<T, 32>(a, zeros, s);
 }
 
+template <class T, int GROUP>
+void launch_expand(const PlaneArgs& a, hipStream_t s)
+{
+    if (long_runs(a))
+        hipLaunchKernelGGL((w4_expand_kernel<T, GROUP, 4>), plane_grid<4>(a), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((w4_expand_kernel<T, GROUP, 1>), plane_grid<1>(a), dim3(256), 0, s, a);
+}
 template <class T>
 void launch_expand(const PlaneArgs& a, int32_t group, hipStream_t s)
 {
-    const dim3 grid(static_cast<uint32_t>(tiles16(a.N) * a.J));
-    if (group == 128)
-        hipLaunchKernelGGL((w4_expand_kernel<T, 128>), grid, dim3(256), 0, s, a);
-    else if (group == 64)
-        hipLaunchKernelGGL((w4_expand_kernel<T, 64>), grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((w4_expand_kernel<T, 32>), grid, dim3(256), 0, s, a);
+    group == 128 ? launch_expand<T, 128>(a, s) : group == 64 ? launch_expand<T, 64>(a, s) : launch_expand<T, 32>(a, s);
 }
 
 uw_status product(const uw_w4_args* p, bool up, void* stream)
