@@ -5,7 +5,8 @@
 // are read once and r' and h written once, which is all that the step has to move; the sums that a norm needs
 // are reduced over lanes by rotations, over waves in LDS. A layer norm takes the mean first and then the squares of
 // the differences from it (two reductions): the difference of two sums of squares would lose the variance of a
-// row whose mean is large. HBM-bound for many rows, one launch for few.
+// row whose mean is large. HBM-bound for many rows (4096 x 4096 of fp32 y and bf16 r into bf16 r' and h 37.3 us, 168 MB, 4.5 TB/s; into
+// codes 37.4, 151 MB; a large copy reaches 5.1), a launch, the loads and two reductions for few (1 x 4096 4.0 us).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -28,12 +29,48 @@ struct NormArgs {
     float w_add, scale_y, scale_r, eps;
 };
 
-__device__ __forceinline__ void load8(const void* p, int32_t type, int64_t row, int64_t k, int64_t K, float (&v)[8])
+// Eight consecutive values as they lie in memory. Loading is kept apart from reading them, so that the branch on the type
+// has nothing in it that waits, and all of a thread's loads are on the way together (4096 x 4096, 16 values per thread: 37.5 us,
+// 46.0 with the conversion beside each load).
+struct Raw {
+    u32x4 a, b;  // bf16: b is unused
+};
+__device__ __forceinline__ Raw load_raw(const void* p, int32_t type, int64_t row, int64_t k, int64_t K)
 {
-    if (type == UW_BF16)
-        load8(static_cast<const uint16_t*>(p) + row, k, K, v);
-    else
-        load8(static_cast<const float*>(p) + row, k, K, v);
+    Raw w;
+    w.a = w.b = u32x4{0, 0, 0, 0};
+    if (k + 8 <= K) {
+        const uint8_t* at = static_cast<const uint8_t*>(p) + (row + k) * (type == UW_BF16 ? 2 : 4);
+        w.a = *reinterpret_cast<const u32x4*>(at);
+        if (type != UW_BF16) w.b = *reinterpret_cast<const u32x4*>(at + 16);
+    } else if (k < K) {  // values past K are 0 and not read
+        if (type == UW_BF16) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (k + i < K) w.a[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[row + k + i]) << (16 * (i & 1));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (k + i < K) (i < 4 ? w.a : w.b)[i & 3] = static_cast<const uint32_t*>(p)[row + k + i];
+        }
+    }
+    return w;
+}
+__device__ __forceinline__ void read(const Raw& w, int32_t type, float (&v)[8])
+{
+    if (type == UW_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(w.a[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w.a[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[i] = __uint_as_float(w.a[i]);
+            v[4 + i] = __uint_as_float(w.b[i]);
+        }
+    }
 }
 
 __device__ __forceinline__ void store8(void* p, int32_t type, int64_t row, int64_t k, int64_t K, const float (&v)[8])
@@ -87,14 +124,45 @@ __device__ __forceinline__ float row_sum(float a, float* red)
     return a;
 }
 
+// A norm's vectors, on the way beside the row where registers allow it.
+template <int E>
+struct Vectors {
+    const void *w, *b;
+    int32_t type;
+    float add;
+    Raw rw[E], rb[E];
+    __device__ __forceinline__ void load(int64_t k0, int64_t step, int64_t K)
+    {
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            if (w) rw[e] = load_raw(w, type, 0, k0 + e * step, K);
+            if (b) rb[e] = load_raw(b, type, 0, k0 + e * step, K);
+        }
+    }
+    // v <- v (w + add) + b
+    __device__ __forceinline__ void apply(int e, float (&v)[8]) const
+    {
+        if (w) {
+            float x[8];
+            read(rw[e], type, x);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] *= x[i] + add;
+        }
+        if (b) {
+            float x[8];
+            read(rb[e], type, x);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] += x[i];
+        }
+    }
+};
+
 // v <- norm(v); red: two rows of LDS, one for each sum (the next norm's are others).
 template <int WAVES, int E>
-__device__ __forceinline__ void norm(float (&v)[E][8], int kind, const float (&w)[E][8], const float (&b)[E][8], int64_t k0,
-                                     const NormArgs& a, float (*red)[16])
+__device__ __forceinline__ void norm(float (&v)[E][8], int kind, const Vectors<E>& vectors, int64_t k0, const NormArgs& a, float (*red)[16])
 {
     constexpr int STEP = WAVES * 64 * 8;
     const float n = static_cast<float>(a.K);
-    if (kind == UW_NORM_NONE) return;
     if (kind == UW_NORM_LAYER) {
         float s = 0.f;
 #pragma unroll
@@ -112,11 +180,33 @@ __device__ __forceinline__ void norm(float (&v)[E][8], int kind, const float (&w
     for (int e = 0; e < E; e++)
 #pragma unroll
         for (int i = 0; i < 8; i++) s = __builtin_fmaf(v[e][i], v[e][i], s);
-    const float f = 1.0f / sqrtf(row_sum<WAVES>(s, red[1]) / n + a.eps);
+    // 1 / sqrt(ms) in two parts: f and the rest that its residual 1 - ms f^2, in which f^2 counts in two parts too, tells. So a value
+    // times the factor is off by its own rounding alone, not by the factor's as well.
+    const float ms = row_sum<WAVES>(s, red[1]) / n + a.eps;
+    const float f = 1.0f / sqrtf(ms), ff = f * f;
+    const float rest = __builtin_fmaf(-ms, ff, 1.0f) - ms * __builtin_fmaf(f, f, -ff);
+    const float low = fabsf(rest) < 1.0f ? 0.5f * f * rest : 0.f;  // (0, infinities and NaN have none)
 #pragma unroll
-    for (int e = 0; e < E; e++)
+    for (int e = 0; e < E; e++) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[e][i] = __builtin_fmaf(v[e][i] * f, w[e][i], b[e][i]);
+        for (int i = 0; i < 8; i++) v[e][i] = __builtin_fmaf(v[e][i], f, v[e][i] * low);
+        vectors.apply(e, v[e]);
+    }
+}
+
+// Values k .. k + 7 of a row of h; 16 lanes hold a group of 128 values, or nothing of the row.
+__device__ __forceinline__ void store_h(const NormArgs& a, int64_t m, int64_t k, float (&v)[8])
+{
+    if (a.h_type != UW_E4M3) {
+        store8(a.h, a.h_type, m * a.ldh, k, a.K, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = k + i < a.K ? v[i] : 0.f;
+    const float s = scale_of(row_max16(amax8(v)));
+    const uint2 c = codes8(v, s);
+    store8(static_cast<uint8_t*>(a.h) + m * a.ldh, k, a.K, c);
+    if ((threadIdx.x & 15) == 0 && k < a.K) a.s[k / kG * a.lds + m] = s;
 }
 
 // One row per WAVES waves, E times eight values per thread; with WAVES = 1 four rows share a workgroup.
@@ -124,80 +214,78 @@ template <int WAVES, int E>
 __global__ void __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) block_norm_kernel(NormArgs a)
 {
     constexpr int STEP = WAVES * 64 * 8;
+    constexpr bool EARLY = E <= 2;  // vectors are loaded with the row
     __shared__ float red[WAVES > 1 ? 4 : 1][16];
     const int t = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
     const int64_t m = WAVES == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
     if (WAVES == 1 && m >= a.M) return;
     const int64_t k0 = 8 * t;
-    float v[E][8], r[E][8];
+    const bool posts = a.y && a.post != UW_NORM_NONE, pres = a.h && a.pre != UW_NORM_NONE, gates = a.y && a.gate;
+    const int64_t gate_row = gates && a.gate_rows ? static_cast<uint32_t>(m) / a.gate_rows : 0;
+    Raw y[E], r[E], g[E];
+    Vectors<E> post{posts ? a.post_w : nullptr, posts ? a.post_b : nullptr, a.w_type, a.w_add};
+    Vectors<E> pre{pres ? a.pre_w : nullptr, pres ? a.pre_b : nullptr, a.w_type, a.w_add};
+    auto load_gate = [&]() {
 #pragma unroll
-    for (int e = 0; e < E; e++) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[e][i] = r[e][i] = 0.f;
-        if (a.y) load8(a.y, a.y_type, m * a.ldy, k0 + e * STEP, a.K, v[e]);
-        if (a.r) load8(a.r, a.r_type, m * a.ldr, k0 + e * STEP, a.K, r[e]);
-    }
-    // weights and biases: as loaded, so that they are on the way beside the row
-    auto vectors = [&](const void* wp, const void* bp, float (&w)[E][8], float (&b)[E][8]) {
-#pragma unroll
-        for (int e = 0; e < E; e++) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                w[e][i] = 1.f;
-                b[e][i] = 0.f;
-            }
-            if (wp) {
-                load8(wp, a.w_type, 0, k0 + e * STEP, a.K, w[e]);
-#pragma unroll
-                for (int i = 0; i < 8; i++) w[e][i] += a.w_add;
-            }
-            if (bp) load8(bp, a.w_type, 0, k0 + e * STEP, a.K, b[e]);
-        }
+        for (int e = 0; e < E; e++)
+            if (gates) g[e] = load_raw(a.gate, a.w_type, gate_row * a.ldgate, k0 + e * STEP, a.K);
     };
+#pragma unroll
+    for (int e = 0; e < E; e++)
+        if (a.y) y[e] = load_raw(a.y, a.y_type, m * a.ldy, k0 + e * STEP, a.K);
+#pragma unroll
+    for (int e = 0; e < E; e++)
+        if (a.r) r[e] = load_raw(a.r, a.r_type, m * a.ldr, k0 + e * STEP, a.K);
+    if (EARLY) {
+        post.load(k0, STEP, a.K);
+        load_gate();
+        pre.load(k0, STEP, a.K);
+    }
+    float v[E][8];
     if (a.y) {
-        float w[E][8], b[E][8];
-        if (a.post != UW_NORM_NONE) {
-            vectors(a.post_w, a.post_b, w, b);
-            norm<WAVES, E>(v, a.post, w, b, k0, a, red);
+#pragma unroll
+        for (int e = 0; e < E; e++) read(y[e], a.y_type, v[e]);
+        if (posts) {
+            if (!EARLY) post.load(k0, STEP, a.K);
+            norm<WAVES, E>(v, a.post, post, k0, a, red);
         }
-        if (a.gate) {
-            const int64_t row = a.gate_rows ? static_cast<uint32_t>(m) / a.gate_rows : 0;
+        if (gates) {
+            if (!EARLY) load_gate();
 #pragma unroll
             for (int e = 0; e < E; e++) {
-                float g[8];
-                load8(a.gate, a.w_type, row * a.ldgate, k0 + e * STEP, a.K, g);
+                float x[8];
+                read(g[e], a.w_type, x);
 #pragma unroll
-                for (int i = 0; i < 8; i++) v[e][i] *= g[i];
+                for (int i = 0; i < 8; i++) v[e][i] *= x[i];
             }
         }
+#pragma unroll
+        for (int e = 0; e < E; e++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[e][i] *= a.scale_y;
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[e][i] = 0.f;
     }
 #pragma unroll
     for (int e = 0; e < E; e++) {
+        if (a.r) {
+            float x[8];
+            read(r[e], a.r_type, x);
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[e][i] = a.y ? (a.r ? __builtin_fmaf(a.scale_y, v[e][i], a.scale_r * r[e][i]) : a.scale_y * v[e][i]) : a.scale_r * r[e][i];
+            for (int i = 0; i < 8; i++) v[e][i] = a.y ? __builtin_fmaf(a.scale_r, x[i], v[e][i]) : a.scale_r * x[i];
+        }
         if (a.r_out) store8(a.r_out, a.r_type, m * a.ldr_out, k0 + e * STEP, a.K, v[e]);
     }
     if (!a.h) return;
-    if (a.pre != UW_NORM_NONE) {
-        float w[E][8], b[E][8];
-        vectors(a.pre_w, a.pre_b, w, b);
-        norm<WAVES, E>(v, a.pre, w, b, k0, a, red + (WAVES > 1 ? 2 : 0));
+    if (pres) {
+        if (!EARLY) pre.load(k0, STEP, a.K);
+        norm<WAVES, E>(v, a.pre, pre, k0, a, red + (WAVES > 1 ? 2 : 0));
     }
 #pragma unroll
-    for (int e = 0; e < E; e++) {
-        const int64_t k = k0 + e * STEP;
-        if (a.h_type != UW_E4M3) {
-            store8(a.h, a.h_type, m * a.ldh, k, a.K, v[e]);
-        } else {
-            // 16 lanes hold a group of 128 values, or nothing of the row
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[e][i] = k + i < a.K ? v[e][i] : 0.f;
-            const float s = scale_of(row_max16(amax8(v[e])));
-            const uint2 c = codes8(v[e], s);
-            store8(static_cast<uint8_t*>(a.h) + m * a.ldh, k, a.K, c);
-            if ((t & 15) == 0 && k < a.K) a.s[k / kG * a.lds + m] = s;
-        }
-    }
+    for (int e = 0; e < E; e++) store_h(a, m, k0 + e * STEP, v[e]);
 }
 
 template <int WAVES, int E>
@@ -209,6 +297,29 @@ uw_status launch(const NormArgs& a, hipStream_t s)
     hipLaunchKernelGGL((block_norm_kernel<WAVES, E>), dim3(static_cast<uint32_t>(blocks)), dim3(threads), 0, s, a);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? UW_OK : fail(UW_EHIP, "block norm launch failed: %s", hipGetErrorString(e));
+}
+
+// How many waves share a row: with few rows as many as keep eight values per thread, for the latency; with many rows four, and more
+// values per thread, so that more rows are in a CU at once (us, cold, y fp32, r bf16 and h in codes; few- and many-row shape:
+// 1 x 4096 4.0 and 5.0, 64 x 8192 6.6 and 9.5, 512 x 4096 9.2 and 9.1, 4096 x 4096 40.5 and 37.3, 4096 x 8192 100 and 70). Workgroups
+// that stay, keep the vectors and have the next row on the way took 38.1 and 78 for the last two.
+uw_status launch_shape(const NormArgs& a, hipStream_t s)
+{
+    if (a.K <= 512) return launch<1, 1>(a, s);
+    if (a.K <= 1024) return launch<2, 1>(a, s);
+    if (a.K <= 2048) return launch<4, 1>(a, s);
+    if (a.M >= 512) {
+        if (a.K <= 4096) return launch<4, 2>(a, s);
+        if (a.K <= 6144) return launch<4, 3>(a, s);
+        if (a.K <= 8192) return launch<4, 4>(a, s);
+        if (a.K <= 16384) return launch<8, 4>(a, s);
+    } else {
+        if (a.K <= 4096) return launch<8, 1>(a, s);
+        if (a.K <= 8192) return launch<16, 1>(a, s);
+        if (a.K <= 16384) return launch<16, 2>(a, s);
+    }
+    if (a.K <= 32768) return launch<16, 4>(a, s);
+    return launch<16, 8>(a, s);
 }
 
 // The rows [M][K] of `type` at p, `ld` elements apart, start at 16-byte boundaries.
@@ -293,13 +404,5 @@ uw_status uw_block_norm(const uw_block_norm_args* p, void* stream)
     a.scale_y = p->scale_y;
     a.scale_r = p->scale_r;
     a.eps = p->eps;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    if (a.K <= 512) return launch<1, 1>(a, s);
-    if (a.K <= 1024) return launch<2, 1>(a, s);
-    if (a.K <= 2048) return launch<4, 1>(a, s);
-    if (a.K <= 4096) return launch<8, 1>(a, s);
-    if (a.K <= 8192) return launch<16, 1>(a, s);
-    if (a.K <= 16384) return launch<16, 2>(a, s);
-    if (a.K <= 32768) return launch<16, 4>(a, s);
-    return launch<16, 8>(a, s);
+    return launch_shape(a, static_cast<hipStream_t>(stream));
 }

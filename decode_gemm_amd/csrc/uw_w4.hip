@@ -110,7 +110,9 @@ __device__ __forceinline__ uint32_t codes_of(const float (&v)[8], float s, float
 }
 
 // TJ 16 x 128 tiles, one after another in K, per workgroup, 8 values of each per thread: row threadIdx / 16, octet
-// threadIdx % 16. Bound by HBM: FIGQ
+// threadIdx % 16. Bound by HBM: bf16 weights of 14336 x 4096 take 33.1 us with a
+// scale per 128 (148 MB, 4.5 TB/s; 34.9 with one tile per workgroup, which is as good for a matrix of few tiles), 40 with zero
+// points, whose fp64 quotients show; fp32 weights with zero points 42.3 (272 MB).
 template <class T, int GROUP, bool ZEROS, int TJ>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(PlaneArgs a)
 {
@@ -204,35 +206,25 @@ __device__ __forceinline__ void store_values(float* w, int64_t k, int64_t K, con
     }
 }
 
-// s q - z s: z s is a 20-bit number times a 4-bit one, exact in fp32, and so is the difference, rounded by the fma not at all. The
-// same tiles and threads as the quantizer's. FIGE
-template <class T, int GROUP, int TJ>
+// s q - z s: z s is a 20-bit number times a 4-bit one, exact in fp32, and so is the difference: the fma rounds nothing. One tile per
+// workgroup, a thread as in the quantizer. Bound by HBM's writes: 14336 x 4096 to bf16 takes 22.5 us, to fp32 45.7 (148 and 272 MB,
+// part of them in the cache behind the L2); with four tiles per workgroup 23.7 and 48.4.
+template <class T, int GROUP>
 __global__ void __launch_bounds__(256) w4_expand_kernel(PlaneArgs a)
 {
     constexpr int PER = 128 / GROUP, LANES = GROUP / 8;
-    const uint32_t runs = static_cast<uint32_t>((a.J + TJ - 1) / TJ);
-    const int64_t t = blockIdx.x / runs, j0 = static_cast<int64_t>(blockIdx.x % runs) * TJ;
+    const int64_t tile = blockIdx.x, t = tile / a.J, j = tile % a.J;
     const int r = threadIdx.x >> 4, o = threadIdx.x & 15;
-    const int64_t n = 16 * t + r;
-    if (n >= a.N) return;
-    uint32_t word[TJ], meta[TJ];
+    const int64_t n = 16 * t + r, k = 128 * j + 8 * o;
+    if (n >= a.N || k >= a.K) return;
+    const uint32_t word = a.plane[tile * 256 + 4 * (16 * (o & 3) + r) + (o >> 2)];
+    const uint32_t meta = a.plane[a.meta + (tile * PER + o / LANES) * 16 + r];
+    const float s = __uint_as_float(meta & ~15u), zs = -static_cast<float>(meta & 15u) * s;
+    const uint32_t even = word & 0x0F0F0F0Fu, odd = (word >> 4) & 0x0F0F0F0Fu;  // values 0 4 1 5 and 2 6 3 7
+    float v[8];
 #pragma unroll
-    for (int u = 0; u < TJ; u++) {
-        const int64_t tile = t * a.J + (j0 + u < a.J ? j0 + u : a.J - 1);
-        word[u] = a.plane[tile * 256 + 4 * (16 * (o & 3) + r) + (o >> 2)];
-        meta[u] = a.plane[a.meta + (tile * PER + o / LANES) * 16 + r];
-    }
-#pragma unroll
-    for (int u = 0; u < TJ; u++) {
-        const int64_t k = 128 * (j0 + u) + 8 * o;
-        if (k >= a.K) break;
-        const float s = __uint_as_float(meta[u] & ~15u), zs = -static_cast<float>(meta[u] & 15u) * s;
-        const uint32_t even = word[u] & 0x0F0F0F0Fu, odd = (word[u] >> 4) & 0x0F0F0F0Fu;  // values 0 4 1 5 and 2 6 3 7
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = __builtin_fmaf(static_cast<float>(((i & 2 ? odd : even) >> (8 * (i / 4) + 16 * (i & 1))) & 255u), s, zs);
-        store_values(static_cast<T*>(a.out) + n * a.ldw, k, a.K, v);
-    }
+    for (int i = 0; i < 8; i++) v[i] = __builtin_fmaf(static_cast<float>(((i & 2 ? odd : even) >> (8 * (i / 4) + 16 * (i & 1))) & 255u), s, zs);
+    store_values(static_cast<T*>(a.out) + n * a.ldw, k, a.K, v);
 }
 
 // ------------------------------------------------------------------------------ product
@@ -613,21 +605,14 @@ PlaneArgs plane_args(const void* plane, int64_t N, int64_t K, int64_t ldw)
     return a;
 }
 
-// Four tiles per workgroup where there are enough of them (FIGT), else one.
-template <int TJ>
-dim3 plane_grid(const PlaneArgs& a)
-{
-    return dim3(static_cast<uint32_t>(tiles16(a.N) * ((a.J + TJ - 1) / TJ)));
-}
-bool long_runs(const PlaneArgs& a) { return a.J >= 4 && tiles16(a.N) * a.J >= 8192; }
-
 template <class T, int GROUP, bool ZEROS>
 void launch_quantize(const PlaneArgs& a, hipStream_t s)
 {
-    if (long_runs(a))
-        hipLaunchKernelGGL((w4_quantize_kernel<T, GROUP, ZEROS, 4>), plane_grid<4>(a), dim3(256), 0, s, a);
+    const int64_t T16 = tiles16(a.N);
+    if (T16 * a.J >= 8192)
+        hipLaunchKernelGGL((w4_quantize_kernel<T, GROUP, ZEROS, 4>), dim3(static_cast<uint32_t>(T16 * ((a.J + 3) / 4))), dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((w4_quantize_kernel<T, GROUP, ZEROS, 1>), plane_grid<1>(a), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((w4_quantize_kernel<T, GROUP, ZEROS, 1>), dim3(static_cast<uint32_t>(T16 * a.J)), dim3(256), 0, s, a);
 }
 template <class T, int GROUP>
 void launch_quantize(const PlaneArgs& a, bool zeros, hipStream_t s)
@@ -640,18 +625,16 @@ void launch_quantize(const PlaneArgs& a, int32_t group, bool zeros, hipStream_t 
     group == 128 ? launch_quantize<T, 128>(a, zeros, s) : group == 64 ? launch_quantize<T, 64>(a, zeros, s) : launch_quantize<T, 32>(a, zeros, s);
 }
 
-template <class T, int GROUP>
-void launch_expand(const PlaneArgs& a, hipStream_t s)
-{
-    if (long_runs(a))
-        hipLaunchKernelGGL((w4_expand_kernel<T, GROUP, 4>), plane_grid<4>(a), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((w4_expand_kernel<T, GROUP, 1>), plane_grid<1>(a), dim3(256), 0, s, a);
-}
 template <class T>
 void launch_expand(const PlaneArgs& a, int32_t group, hipStream_t s)
 {
-    group == 128 ? launch_expand<T, 128>(a, s) : group == 64 ? launch_expand<T, 64>(a, s) : launch_expand<T, 32>(a, s);
+    const dim3 grid(static_cast<uint32_t>(tiles16(a.N) * a.J));
+    if (group == 128)
+        hipLaunchKernelGGL((w4_expand_kernel<T, 128>), grid, dim3(256), 0, s, a);
+    else if (group == 64)
+        hipLaunchKernelGGL((w4_expand_kernel<T, 64>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((w4_expand_kernel<T, 32>), grid, dim3(256), 0, s, a);
 }
 
 uw_status product(const uw_w4_args* p, bool up, void* stream)

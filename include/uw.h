@@ -687,7 +687,8 @@ size_t uw_w4_gemm_workspace(int64_t M, int64_t N, int64_t K);
  * ((x - mean) / sqrt(mean (x - mean)^2 + eps) * (w + w_add) + b), weights w and biases b [K] optional (NULL: w + w_add is
  * 1 and b 0). The gate multiplies value by value: row m of y takes row m / gate_rows of d_gate, gate_rows = 0: all rows take
  * the first (NULL: 1). Weights, biases and gate are of w_type. All arithmetic is fp32, sums of a row included; each output
- * is rounded once. A NaN stays in its row; rows whose sum of squares passes fp32's range are not supported.
+ * is rounded once. Results do not depend on the run; the order of a row's sums follows from M and K, so its last bits may be
+ * others in another batch. A NaN stays in its row; rows whose sum of squares passes fp32's range are not supported.
  * d_y NULL: no block (r' = scale_r * r), d_r NULL: no stream (r' = scale_y * gate * v); d_r_out NULL: r' is not
  * stored; d_h NULL: there is no h. At least one of d_y, d_r and one of d_r_out, d_h are given.
  * h is bf16, fp32 or, with h_type UW_E4M3, the codes that uw_fp8_quantize makes of the fp32 h with rows of groups:
@@ -697,7 +698,7 @@ size_t uw_w4_gemm_workspace(int64_t M, int64_t N, int64_t K);
  * neither used nor written.
  * Errors: UW_ESHAPE (M < 0, K < 1), UW_EINVAL (NULL pointers as above; misaligned ones: 16 bytes, scales 4; leading dimensions below
  * K or that do not keep rows 16-byte aligned; an unknown type or norm; gate_rows < 0; eps not a finite number >= 0),
- * UW_EUNSUPPORTED (K > UW_NORM_MAX_K, M >= 2^31), UW_EHIP. M = 0 is a no-op.
+ * UW_EUNSUPPORTED (K > UW_NORM_MAX_K, M >= 2^31, more rows than one launch takes: 2^22 always are), UW_EHIP. M = 0 is a no-op.
  */
 #define UW_NORM_MAX_K 65536
 typedef enum { UW_NORM_NONE = 0, UW_NORM_RMS = 1, UW_NORM_LAYER = 2 } uw_norm;

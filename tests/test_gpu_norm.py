@@ -134,6 +134,12 @@ def test_row_lengths(K):
         case(1, K, K + 1, post=2, pre=2, y_type="bf16", r_type="f32", out="bf16")
 
 
+@pytest.mark.parametrize("K", [2049, 4096, 4097, 6144, 6145, 8192, 8200, 16384, 16399])
+def test_row_lengths_of_many_rows(K):
+    case(515, K, K, out="codes", gate=100)
+    case(512, K, K + 1, post=2, pre=2, y_type="bf16", r_type="f32", w_type="f32", out="bf16", weights=K % 2 == 0)
+
+
 @pytest.mark.parametrize("post", [0, 1, 2])
 @pytest.mark.parametrize("pre", [0, 1, 2])
 @pytest.mark.parametrize("out", ["f32", "bf16", "codes"])
@@ -224,6 +230,6 @@ def test_offsets_past_four_gigabytes():
     y = torch.empty(M, K, device="cuda").normal_()
     h = torch.empty(M, K, device="cuda")
     uw.block_norm(y, None, None, M, K, d_h=h, post=uw.NORM_NONE)
-    few = torch.empty(5, K, device="cuda")
-    uw.block_norm(y[M - 5:], None, None, 5, K, d_h=few, post=uw.NORM_NONE)
-    assert torch.equal(h[M - 5:], few)
+    few = torch.empty(600, K, device="cuda")  # as many rows as are summed up in the same order (512 and more)
+    uw.block_norm(y[M - 600:], None, None, 600, K, d_h=few, post=uw.NORM_NONE)
+    assert torch.equal(h[M - 600:], few)
