@@ -717,8 +717,8 @@ def logprobs(d_logits, M: int, V: int, d_token=None, d_logprob=None, d_rank=None
     """uw_logprobs: per row of logits [M][V] (fp32 or bf16) the log probability (fp32 [M]) and rank (int32 [M]) of d_token
     (int32 [M]), the entropy (fp32 [M]) and the n_top first tokens (int32 [M][n_top]) with their log probabilities (fp32). Each
     output may be None. d_ws: logprobs_workspace(M, V, n_top) bytes. A ValueError for tensors of other types and strided ones."""
-    if n_top == 0:  # empty tensors are no lists
-        d_top_token = d_top_logprob = None
+    if n_top == 0:  # tensors of no elements are no lists
+        d_top_token, d_top_logprob = (None if t is not None and not isinstance(t, int) and t.numel() == 0 else t for t in (d_top_token, d_top_logprob))
     a = _pack_logprobs(M, V, _at(d_logits), V if ld is None else ld, _type(d_logits, type), _elements("d_token", d_token, M, True) or 0,
                        _elements("d_temperature", d_temperature, M) or 0, _elements("d_logprob", d_logprob, M) or 0,
                        _elements("d_rank", d_rank, M, True) or 0, _elements("d_entropy", d_entropy, M) or 0, n_top,

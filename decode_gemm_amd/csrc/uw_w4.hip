@@ -26,7 +26,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int64_t kMostNK = int64_t{1} << 24;
-constexpr int64_t kMostLd = int64_t{1} << 26;  // 16 rows of X within 32-bit byte offsets
+constexpr int64_t kMostLd = int64_t{1} << 25;  // 64 rows of X and K values more lie within 32-bit byte offsets
 
 __host__ __device__ __forceinline__ int64_t tiles16(int64_t n) { return (n + 15) / 16; }
 __host__ __device__ __forceinline__ int64_t tiles128(int64_t k) { return (k + 127) / 128; }
@@ -652,7 +652,7 @@ uw_status product(const uw_w4_args* p, bool up, void* stream)
         return fail(UW_EINVAL, "X, planes and workspace must be 16-byte aligned");
     if (!aligned(p->d_y, p->y_type == UW_BF16 ? 2 : 4)) return fail(UW_EINVAL, "d_y must be aligned to its elements");
     if (p->ldx < p->K || p->ldx % 8) return fail(UW_EINVAL, "ldx must be >= K and a multiple of 8");
-    if (p->ldx > kMostLd) return fail(UW_EUNSUPPORTED, "ldx over 2^26");
+    if (p->ldx > kMostLd) return fail(UW_EUNSUPPORTED, "ldx over 2^25");
     if (p->ldy < p->N) return fail(UW_EINVAL, "ldy must be >= N");
     W4Args a{};
     a.x = p->d_x;

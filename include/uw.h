@@ -637,9 +637,9 @@ size_t uw_sample_workspace(int64_t M, int64_t V);
  * read), Y [M][ldy] fp32 or bf16 (y_type; one rounding), by
  *   Y[m][n] = sum over groups g of  s[n][g] * (sum over k in g of x[m][k] q[n][k]  -  z[n][g] * sum over k in g of x[m][k])
  * with every sum in fp32 and no weight rounded. (The matrix unit takes 1 + q / 16 for q, so that a row's outputs
- * are NaN where it holds an infinity or a NaN.) Made for few rows, where W's bytes bound it; larger M runs in blocks
- * of 64 rows that read W again, right but, from a few hundred rows on, slower than uw_w4_expand and
- * uw_recon_gemm.
+ * are NaN where it holds an infinity or a NaN.) Made for few rows, where W's bytes bound it. Larger M runs in blocks of 64
+ * rows that read W again: from about 512 (a large W) to 1500 rows on, uw_w4_expand and uw_recon_gemm are faster, with weights
+ * rounded to bf16.
  *
  * uw_w4_gate_up (device). h = bf16(silu(X Wg^T) * (X Wu^T)) [M][ldh], both planes N x K with the same group: the
  * two products and the activation of uw_swiglu in one pass over X, the products not rounded on the way.
@@ -651,7 +651,7 @@ size_t uw_sample_workspace(int64_t M, int64_t V);
  * when the call's work is done; calls that overlap need one each.
  * Errors: UW_ESHAPE (M < 0, N or K < 1), UW_EINVAL (NULL or misaligned pointers: 16 bytes; d_y and d_h only that of
  * their elements; a leading dimension too small or not the multiple named; an unknown type or group; zeros not 0 or 1),
- * UW_EUNSUPPORTED (N or K over 2^24, M over 2^31 - 1, ldx over 2^26, more than one launch takes), UW_EHIP. M = 0 is a no-op.
+ * UW_EUNSUPPORTED (N or K over 2^24, M over 2^31 - 1, ldx over 2^25, more than one launch takes), UW_EHIP. M = 0 is a no-op.
  * Buffers must not overlap, but that Wg and Wu may be the same plane.
  */
 size_t uw_w4_plane_bytes(int64_t N, int64_t K, int32_t group); /* 0 for arguments that the calls refuse */

@@ -353,6 +353,22 @@ def test_streams_and_graphs():
             assert torch.equal(h, h0)
 
 
+def test_rows_of_x_far_apart():
+    """64 rows of X at the largest leading dimension: the last one begins 4.2 GB behind the first."""
+    torch, uw = torch_cuda(), _uw()
+    rng = np.random.default_rng(11)
+    N, K, group, ldx = 48, 300, 64, 1 << 25
+    for M in (4, 16, 64):
+        x, q, s, z = _whole(rng, M, N, K, group, True)
+        want = torch.from_numpy(x.astype(np.float64) @ values_of(q, s, z, K).T).float()
+        far = torch.empty((M - 1) * ldx + K, dtype=torch.bfloat16, device="cuda")
+        for m in range(M):
+            far[m * ldx:m * ldx + K] = torch.from_numpy(x[m]).to("cuda")
+        y = torch.zeros(M, N, device="cuda")
+        uw.w4_gemm(far, put_plane(plane_of(q, s, z, N, K, group)), y, M, N, K, group=group, ldx=ldx)
+        assert torch.equal(y.cpu(), want)
+
+
 def test_planes_past_four_gigabytes():
     """The last rows of a plane of 4.4 GB are those of a plane of their own."""
     torch, uw = torch_cuda(), _uw()

@@ -76,6 +76,7 @@ def test_product_refusals(up):
     assert f(**{"ldh" if up else "ldy": 63}) == uw.EINVAL
     assert f(M=1 << 31) == uw.EUNSUPPORTED
     assert f(M=(1 << 31) - 1, N=1 << 20) == uw.EUNSUPPORTED
+    assert f(ldx=(1 << 25) + 8) == uw.EUNSUPPORTED
     assert f(N=1 << 25) == uw.EUNSUPPORTED
     if not up:
         assert f(y_type=uw.E4M3) == uw.EINVAL
@@ -159,6 +160,7 @@ def test_logprobs_refusals():
     assert _lp(d_token=None, d_logprob=None, d_rank=P) == uw.EINVAL
     assert _lp(d_logprob=None) == uw.EINVAL              # no output
     assert _lp(n_top=3) == uw.EINVAL                     # nowhere to put them
+    assert _lp(d_top_token=P) == uw.EINVAL               # a list of nothing
     assert _lp(n_top=3, d_top_token=P + 2) == uw.EINVAL
     need = uw.logprobs_workspace(4, 100000, 3)
     assert need > 0
