@@ -9,7 +9,8 @@
 // reached by at least n tokens and hardly more, and these, found by looking again into the shares of the threads
 // whose maximum reaches it, are sorted in LDS. Where ties make them too many, a search over the digits of
 // (logit, index) finds the n-th token itself.
-// Bound by the row's bytes for many rows; a row alone by its two launches and their chains of barriers.
+// Bound by the row's bytes for many rows (1024 x 131072 fp32 with one first token 102 us, 5.3 TB/s, part of it from the cache behind
+// the L2; bf16 55 us), a row alone by its two launches and their chains of barriers (131072 tokens, 20 first ones: 14 us).
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -93,16 +94,28 @@ struct Words {
         n = (V + skip + VEC - 1) / VEC;
     }
     __device__ __forceinline__ int first(int i) const { return i * VEC - skip; }
-    __device__ __forceinline__ void load(int i, float (&v)[VEC]) const
+    // As it lies in memory: with the conversion apart, the branch has nothing in it that waits.
+    __device__ __forceinline__ u32x4 raw(int i) const
     {
         const int e = first(i);
-        if (e >= 0 && e + VEC <= V) {
-            unpack(*reinterpret_cast<const u32x4*>(x + e), v);
-        } else {
+        if (e >= 0 && e + VEC <= V) return *reinterpret_cast<const u32x4*>(x + e);
+        u32x4 w = nothing();
 #pragma unroll
-            for (int k = 0; k < VEC; k++) v[k] = e + k >= 0 && e + k < V ? value(x, e + k) : -INFINITY;
-        }
+        for (int k = 0; k < VEC; k++)
+            if (e + k >= 0 && e + k < V) put(w, k, x[e + k]);
+        return w;
     }
+    static __device__ __forceinline__ u32x4 nothing()
+    {
+        constexpr uint32_t kNone = VEC == 4 ? 0xFF800000u : 0xFF80FF80u;
+        return u32x4{kNone, kNone, kNone, kNone};
+    }
+    static __device__ __forceinline__ void put(u32x4& w, int k, float v) { w[k] = __float_as_uint(v); }
+    static __device__ __forceinline__ void put(u32x4& w, int k, uint16_t v)
+    {
+        w[k / 2] = k & 1 ? (w[k / 2] & 0xFFFFu) | static_cast<uint32_t>(v) << 16 : (w[k / 2] & 0xFFFF0000u) | v;
+    }
+    __device__ __forceinline__ void load(int i, float (&v)[VEC]) const { unpack(raw(i), v); }
 };
 
 // 2 log2(e) / T, of halved differences, which cannot overflow; 0 where all tokens weigh the same or (T <= 0, NaN)
@@ -303,10 +316,10 @@ __device__ __forceinline__ float threshold(const uint32_t* share, float top, uin
 }
 
 // One slice of a row (all of it with slices = 1) per workgroup; thread t has the words first + t + NT i.
-template <class T, int NT>
+template <class T, int NT, int EL>
 __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
 {
-    constexpr int VEC = Words<T>::VEC, U = 16 / VEC;  // 16 values per thread and step
+    constexpr int VEC = Words<T>::VEC, U = EL / VEC;  // EL values per thread and step
     constexpr int PER = NT / kParts;                  // threads per share
     static_assert(PER == 1 || PER == 2 || PER == 4, "threads per share");
     __shared__ Shared<NT> sh;
@@ -317,6 +330,9 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
     const Words<T> w(x, a.V);
     const int per = (w.n + static_cast<int>(a.slices) - 1) / static_cast<int>(a.slices);
     const int first = per * static_cast<int>(z), end = first + per < w.n ? first + per : w.n;
+    u32x4 next[U];  // the next step's words, on the way
+#pragma unroll
+    for (int u = 0; u < U; u++) next[u] = first + tid + u * NT < end ? w.raw(first + tid + u * NT) : Words<T>::nothing();
     const float temp = a.temperature ? a.temperature[m] : 1.f, c2 = slope(temp);
     const int t = a.token ? a.token[m] : -1;
     const float lt = t >= 0 && t < a.V ? value(x, t) : -INFINITY;
@@ -328,14 +344,10 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
     const bool counts = a.rank || greedy(temp);
     for (int i = first + tid; i < end; i += NT * U) {
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            if (i + u * NT < end) {
-                w.load(i + u * NT, v[u]);
-            } else {
+        for (int u = 0; u < U; u++) unpack(next[u], v[u]);
+        if (i + NT * U < end)
 #pragma unroll
-                for (int k = 0; k < VEC; k++) v[u][k] = -INFINITY;
-            }
-        }
+            for (int u = 0; u < U; u++) next[u] = i + (U + u) * NT < end ? w.raw(i + (U + u) * NT) : Words<T>::nothing();
         float now = top;
 #pragma unroll
         for (int u = 0; u < U; u++)
@@ -559,11 +571,12 @@ __global__ void __launch_bounds__(kJoinThreads) logprobs_join(LogprobArgs a)
     for (int i = C + tid; i < n; i += kJoinThreads) answer_top(a, m, static_cast<uint32_t>(i), kNoKey, p, logS, temp);
 }
 
-// Workgroups of `threads`, `slices` of them per row. A CU takes about 3 us for 32000 tokens, so a row among few is
-// cut into slices until the second launch (3 us) costs more than they save: 1 x 131072 takes 23.6, 19.9, 15.5 and
-// 13.8 us with 1, 2, 4 and 8 slices, 64 x 131072 27.6, 23.6, 19.2 and 19.6. From a CU's worth of rows on slices only add work
-// (256 x 131072: 34.5 us with two, 30.6 with a whole row per 1024 threads), and with many rows small workgroups, whose ends
-// meet others' beginnings, do best (1024 x 131072: 103 us with 256 threads, 121 with 512, 115 with 1024).
+// Workgroups of `threads`, `slices` of them per row. Measured (us, fp32, 20 first tokens):
+//   slices cost a second launch and pay for a few long rows: 1 x 131072 takes 23.6, 19.9, 16.7 and 15.0 with 1, 2, 4 and 8, 64 x
+//   131072 27.6, 23.6, 19.1 and 20.5, 1 x 64000 14.5 with 4 and 13.3 with 8; 1 x 32000 13.4 with one, 13.0 with 4, 64 x 32000
+//   13.7 and 13.8, 200 x 131072 30.4 with one and 32.0 with two;
+//   threads, 256 / 512 / 1024: 1 x 4000 8.4 8.6 11.0, 200 x 32000 18.5 14.9 15.8, 200 x 131072 - 30.4 27.7, 500 x 131072 59.0 55.1
+//   59.5, and with many rows, where ends of small workgroups meet others' beginnings, 1024 x 32000 34.5 38.4 56.9.
 struct Shape {
     int threads;
     uint32_t slices;
@@ -571,9 +584,10 @@ struct Shape {
 
 Shape shape_of(int64_t M, int64_t V)
 {
-    if (V <= 4096 || M >= 512) return {256, 1};
-    if (M >= 128) return {1024, 1};
-    int64_t s = (V + 8191) / 8192;  // a step's tokens at the shortest
+    if (V <= 4096 || M >= 768) return {256, 1};
+    if (M >= 128) return {V >= 100000 && M <= 320 ? 1024 : 512, 1};
+    if (V < 48000) return {512, 1};
+    int64_t s = V / 8192;  // a step's tokens at the shortest
     if (s > 256 / M) s = 256 / M;
     return {512, static_cast<uint32_t>(s < kMostSlices ? s : kMostSlices)};
 }
@@ -617,13 +631,13 @@ uw_status check(const uw_logprobs_args* p)
 template <class T>
 void launch(const LogprobArgs& a, const Shape& h, hipStream_t s)
 {
-    const dim3 grid(static_cast<uint32_t>(a.M * h.slices));
+    const dim3 grid(static_cast<uint32_t>(a.M * h.slices)), block(h.threads);
     if (h.threads == 256)
-        hipLaunchKernelGGL((logprobs_rows<T, 256>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((logprobs_rows<T, 256, 16>), grid, block, 0, s, a);
     else if (h.threads == 512)
-        hipLaunchKernelGGL((logprobs_rows<T, 512>), grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((logprobs_rows<T, 512, 16>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((logprobs_rows<T, 1024>), grid, dim3(1024), 0, s, a);
+        hipLaunchKernelGGL((logprobs_rows<T, 1024, 16>), grid, block, 0, s, a);
     if (h.slices > 1) hipLaunchKernelGGL(logprobs_join<T>, dim3(static_cast<uint32_t>(a.M)), dim3(kJoinThreads), 0, s, a);
 }
 

@@ -90,7 +90,7 @@ def run(x, token, n=0, T=None, bf16=False, pad=0, shift=0):
     need = uw.logprobs_workspace(M, V, n)
     ws = torch.full((max(16, need),), 255, dtype=torch.uint8, device="cuda")
     log(f"  logprobs {M}x{V} top {n} {'bf16' if bf16 else 'f32'} workspace {need}")
-    uw.logprobs(rows, M, V, d_token=t, d_logprob=lp[:M], d_rank=rank[:M], d_entropy=ent[:M], n_top=n, d_top_token=tt[:M], d_top_logprob=tl[:M],
+    uw.logprobs(rows, M, V, d_token=t, d_logprob=lp[:M], d_rank=rank[:M], d_entropy=ent[:M], n_top=n, d_top_token=tt[:M] if n else None, d_top_logprob=tl[:M] if n else None,
                 d_temperature=temp, ld=ld, d_ws=ws, ws_bytes=need)
     lp, ent, rank, tt, tl = (v.cpu().numpy() for v in (lp, ent, rank, tt, tl))
     assert lp[M] == 77 and ent[M] == 77 and rank[M] == 77 and (tt[M] == 77).all() and (tl[M] == 77).all()
@@ -130,6 +130,29 @@ def test_many_rows(M):
     rng = np.random.default_rng(M)
     run(_logits(rng, M, 5003, "peaked"), rng.integers(0, 5003, M), 3, T=rng.choice([0.6, 1.0, 1.3], M), pad=1)
     run(_logits(rng, M, 700, "masked"), rng.integers(0, 700, M), 128, bf16=True)
+
+
+@pytest.mark.parametrize("M,V", [(3, 47999), (3, 48000), (127, 50001), (128, 50001), (320, 100000), (321, 100000), (767, 5000), (768, 5000)])
+def test_where_launch_shapes_change(M, V):
+    """Every number of threads and of slices, a few rows of each checked (the others are copies of them)."""
+    torch, uw = torch_cuda(), _uw()
+    rng = np.random.default_rng(M + V)
+    few = _logits(rng, 3, V, "peaked")
+    tok, n = rng.integers(0, V, 3), 20
+    rows = torch.from_numpy(few).to("cuda").repeat(-(-M // 3), 1)[:M]
+    t = torch.tensor(np.tile(tok, -(-M // 3))[:M].astype(np.int32), device="cuda")
+    lp, ent, rank = torch.zeros(M, device="cuda"), torch.zeros(M, device="cuda"), torch.zeros(M, dtype=torch.int32, device="cuda")
+    tt, tl = torch.zeros(M, n, dtype=torch.int32, device="cuda"), torch.zeros(M, n, device="cuda")
+    need = uw.logprobs_workspace(M, V, n)
+    ws = torch.full((max(16, need),), 255, dtype=torch.uint8, device="cuda")
+    uw.logprobs(rows, M, V, d_token=t, d_logprob=lp, d_rank=rank, d_entropy=ent, n_top=n, d_top_token=tt, d_top_logprob=tl, d_ws=ws, ws_bytes=need)
+    for m in range(min(3, M)):
+        p, tol, k, e, tol_e, wt, wl = reference(few[m], int(tok[m]), 1.0, n)
+        assert (rank[m::3] == k).all() and (tt[m::3].cpu().numpy() == wt).all()
+        near(float(lp[m]), p, tol, "log probability")
+        near(float(ent[m]), e, tol_e, "entropy")
+        # rows that lie elsewhere in memory may begin at another place in a word, and sum up in another order
+        assert (lp[m::3] - lp[m]).abs().max() <= 2 * tol + 2 * U * abs(p) and (tl[m::3] - tl[m]).abs().max() <= 2 * tol + 2 * U * abs(wl[-1])
 
 
 def test_longest_row():

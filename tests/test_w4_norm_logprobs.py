@@ -175,6 +175,8 @@ def test_workspaces():
     assert uw.logprobs_workspace(1 << 22, 1000) == 0
     assert uw.logprobs_workspace(4, 1000, 129) == 0
     assert uw.logprobs_workspace(1, 1000, 20) == 0       # one workgroup has the row
+    assert uw.logprobs_workspace(1024, 131072, 20) == 0
+    assert uw.logprobs_workspace(4, 100000, 20) > uw.logprobs_workspace(4, 100000, 0) > 0
     assert uw.w4_gemm_workspace(0, 16, 128) == 0
     assert uw.w4_gemm_workspace(1, 0, 128) == 0
     assert uw.w4_gemm_workspace(1, 1 << 25, 128) == 0
