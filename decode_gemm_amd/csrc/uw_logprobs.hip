@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kParts = 256;   // shares of a slice whose maxima are compared
 constexpr int kList = 2048;   // tokens that are sorted in LDS
-constexpr int kCounted = 256; // as many are ordered by counting
+constexpr int kCounted = 512;  // as many are ordered by counting
 constexpr int kMostSlices = 8;
 constexpr double kLn2 = 0x1.62e42fefa39efp-1;
 constexpr u64 kNoKey = ~u64{0};
@@ -214,6 +214,18 @@ __device__ __forceinline__ void answer_top(const LogprobArgs& a, int64_t m, uint
     }
 }
 
+__device__ __forceinline__ uint32_t wave_min(uint32_t v)
+{
+    auto less = [](uint32_t a, uint32_t b) { return a < b ? a : b; };
+    v = less(v, static_cast<uint32_t>(rotated<0x128>(static_cast<int>(v))));
+    v = less(v, static_cast<uint32_t>(rotated<0x124>(static_cast<int>(v))));
+    v = less(v, static_cast<uint32_t>(rotated<0x122>(static_cast<int>(v))));
+    v = less(v, static_cast<uint32_t>(rotated<0x121>(static_cast<int>(v))));
+    v = less(v, __shfl_xor(v, 16));
+    v = less(v, __shfl_xor(v, 32));
+    return __builtin_amdgcn_readfirstlane(v);
+}
+
 template <int NT>
 struct Shared {
     u64 list[kList];
@@ -290,16 +302,21 @@ __device__ __noinline__ void search_keys(Shared<NT>& sh, const Words<T>& w, int 
 }
 
 // A number that at least n of the shares' maxima reach, but not many more; -inf where fewer than n have one. By halving, in
-// the order of numbers, each wave for itself: the counts are those of its lanes' comparisons.
+// the order of numbers, between the least and the largest of them, each wave for itself: the counts are those of its lanes'
+// comparisons. A quarter more, or eight, are near enough: a few more candidates cost less than another turn.
 __device__ __forceinline__ float threshold(const uint32_t* share, float top, uint32_t n)
 {
     constexpr uint32_t kNone = 0x007FFFFFu;  // -inf in that order
     const int lane = threadIdx.x & 63;
-    uint32_t v[kParts / 64];
+    uint32_t v[kParts / 64], least;
 #pragma unroll
-    for (int i = 0; i < kParts / 64; i++) v[i] = share[lane + 64 * i];
-    uint32_t lo = kNone, hi = top > -INFINITY ? ~order_bits(top) : kNone;
-    hi = __builtin_amdgcn_readfirstlane(hi);
+    for (int i = 0; i < kParts / 64; i++) {
+        v[i] = share[lane + 64 * i];
+        least = i == 0 || v[i] < least ? v[i] : least;
+    }
+    least = wave_min(least);
+    const uint32_t most = n + (n / 4 > 8 ? n / 4 : 8);
+    uint32_t lo = least > kNone ? least : kNone, hi = __builtin_amdgcn_readfirstlane(top > -INFINITY ? ~order_bits(top) : kNone);
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo + 1) / 2;
         uint32_t c = 0;
@@ -309,10 +326,23 @@ __device__ __forceinline__ float threshold(const uint32_t* share, float top, uin
             hi = mid - 1;
         } else {
             lo = mid;
-            if (c <= n + n / 4) break;
+            if (c <= most) break;
         }
     }
     return lo == kNone ? -INFINITY : order_value(~lo);
+}
+
+// Place of a wave's key among the keys that its first `count` lanes hold.
+__device__ __forceinline__ int place_in_wave(u64 key, int count)
+{
+    const uint32_t lo = static_cast<uint32_t>(key), hi = static_cast<uint32_t>(key >> 32);
+    int place = 0;
+    for (int o = 0; o < count; o++) {
+        const u64 other = static_cast<u64>(static_cast<uint32_t>(__builtin_amdgcn_readlane(hi, o))) << 32 |
+                          static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, o));
+        place += other < key;
+    }
+    return place;
 }
 
 // One slice of a row (all of it with slices = 1) per workgroup; thread t has the words first + t + NT i.
@@ -460,6 +490,22 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
     // Keys are all different, so a key's place is the number of smaller ones; many are sorted instead.
     const int C = static_cast<int>(sh.n_list);
     u64* keys = a.slices > 1 ? a.keys + (m * a.slices + z) * n : nullptr;
+    auto answer = [&](int place, u64 key) {
+        if (keys)
+            keys[place] = key;
+        else
+            answer_top(a, m, static_cast<uint32_t>(place), key, p, logS, temp);
+    };
+    if (C <= 64) {  // a wave has them all; the others fill the places past the last key
+        if (wave == 0) {
+            const u64 key = lane < C ? sh.list[lane] : kNoKey;
+            const int place = lane < C ? place_in_wave(key, C) : n;
+            if (place < n) answer(place, key);
+        } else {
+            for (int c = C + tid - 64; c < n; c += NT - 64) answer(c, kNoKey);
+        }
+        return;
+    }
     if (C > kCounted) {
         int size = 2 * kCounted;
         while (size < C) size *= 2;
@@ -489,11 +535,7 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
                 for (int o = 0; o < C; o++) place += sh.list[o] < key;
             }
         }
-        if (place >= n) continue;
-        if (keys)
-            keys[place] = key;
-        else
-            answer_top(a, m, static_cast<uint32_t>(place), key, p, logS, temp);
+        if (place < n) answer(place, key);
     }
 }
 
