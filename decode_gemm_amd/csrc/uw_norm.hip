@@ -5,8 +5,8 @@
 // are read once and r' and h written once, which is all that the step has to move; the sums that a norm needs
 // are reduced over lanes by rotations, over waves in LDS. A layer norm takes the mean first and then the squares of
 // the differences from it (two reductions): the difference of two sums of squares would lose the variance of a
-// row whose mean is large. HBM-bound for many rows (4096 x 4096 of fp32 y and bf16 r into bf16 r' and h 37.3 us, 168 MB, 4.5 TB/s; into
-// codes 37.4, 151 MB; a large copy reaches 5.1), a launch, the loads and two reductions for few (1 x 4096 4.0 us).
+// row whose mean is large. HBM-bound for many rows (4096 x 4096 of fp32 y and bf16 r into bf16 r' and h 35.5 us, 168 MB, 4.7 TB/s; into
+// codes 35.8, 151 MB; a large copy reaches 5.1), a launch, the loads and two reductions for few (1 x 4096 3.8 us).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -30,8 +30,8 @@ struct NormArgs {
 };
 
 // Eight consecutive values as they lie in memory. Loading is kept apart from reading them, so that the branch on the type
-// has nothing in it that waits, and all of a thread's loads are on the way together (4096 x 4096, 16 values per thread: 37.5 us,
-// 46.0 with the conversion beside each load).
+// has nothing in it that waits, and all of a thread's loads are on the way together (4096 x 4096, 16 values per thread: 37.5 us when this
+// was brought in, 46.0 with the conversion beside each load).
 struct Raw {
     u32x4 a, b;  // bf16: b is unused
 };
@@ -73,19 +73,22 @@ __device__ __forceinline__ void read(const Raw& w, int32_t type, float (&v)[8])
     }
 }
 
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ void store8(void* p, int32_t type, int64_t row, int64_t k, int64_t K, const float (&v)[8])
 {
     if (type == UW_BF16) {
         uint16_t* o = static_cast<uint16_t*>(p) + row + k;
-        if (k + 8 <= K) {
-            u32x4 w;
+        u32x4 w;  // the one rounding, to nearest even
 #pragma unroll
-            for (int i = 0; i < 4; i++) w[i] = f32_to_bf16_rne(v[2 * i]) | (f32_to_bf16_rne(v[2 * i + 1]) << 16);
+        for (int i = 0; i < 4; i++) w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(floatx2{v[2 * i], v[2 * i + 1]}, bf16x2));
+        if (k + 8 <= K) {
             *reinterpret_cast<u32x4*>(o) = w;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; i++)
-                if (k + i < K) o[i] = static_cast<uint16_t>(f32_to_bf16_rne(v[i]));
+                if (k + i < K) o[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
         }
     } else {
         float* o = static_cast<float*>(p) + row + k;
@@ -214,7 +217,9 @@ template <int WAVES, int E>
 __global__ void __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) block_norm_kernel(NormArgs a)
 {
     constexpr int STEP = WAVES * 64 * 8;
-    constexpr bool EARLY = E <= 2;  // vectors are loaded with the row
+    // Vectors are loaded with the row, for the latency, where that leaves registers for other rows (4096 x 4096 of 16 values per thread:
+    // 36.8 us with them late, 40.0 early).
+    constexpr bool EARLY = E == 1;
     __shared__ float red[WAVES > 1 ? 4 : 1][16];
     const int t = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
     const int64_t m = WAVES == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
@@ -301,7 +306,7 @@ uw_status launch(const NormArgs& a, hipStream_t s)
 
 // How many waves share a row: with few rows as many as keep eight values per thread, for the latency; with many rows four, and more
 // values per thread, so that more rows are in a CU at once (us, cold, y fp32, r bf16 and h in codes; few- and many-row shape:
-// 1 x 4096 4.0 and 5.0, 64 x 8192 6.6 and 9.5, 512 x 4096 9.2 and 9.1, 4096 x 4096 40.5 and 37.3, 4096 x 8192 100 and 70). Workgroups
+// 1 x 4096 3.8 and 5.0, 64 x 8192 6.5 and 9.5, 512 x 4096 9.2 and 9.2, 4096 x 4096 40.5 and 35.8, 4096 x 8192 100 and 72). Workgroups
 // that stay, keep the vectors and have the next row on the way took 38.1 and 78 for the last two.
 uw_status launch_shape(const NormArgs& a, hipStream_t s)
 {
