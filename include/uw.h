@@ -747,7 +747,8 @@ uw_status uw_block_norm(const uw_block_norm_args* args, void* stream);
  * lists places past the last token of the order hold -1 and -inf. A row in which no token has a place gets entropy 0.
  * exp and its sums are fp32 within a few hundred values and fp64 from there on: log probabilities and
  * entropies are within about 1e-6 (and 2^-23 of their value). Ranks and top tokens come from comparisons
- * alone and are exact. No result depends on the run.
+ * alone and are exact. No result depends on the run; last bits of the others may be others in another batch or where a row
+ * begins elsewhere.
  * d_ws: uw_logprobs_workspace(M, V, n_top) bytes, 16-byte aligned; free again when the call's work is done; calls
  * that overlap need one each. NULL where that is 0.
  * Errors: UW_ESHAPE (M < 0, V < 1), UW_EINVAL (NULL d_logits; d_logprob or d_rank without d_token; no output; misaligned pointers: that
