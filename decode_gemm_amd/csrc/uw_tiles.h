@@ -18,17 +18,18 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p)
 // Issued from asm so that the compiler's wait counting does not make every later LDS read
 // wait for the newest transfer; the compiler then undercounts outstanding loads, which
 // only ever makes its own waits stricter. Callers order the reads of the target
-// themselves (a wait for a load issued after the transfer).
+// themselves (a wait for a load issued after the transfer). A transfer needs one wait state
+// behind the write of M0, which holds its target; the compiler puts none into an asm block.
 __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t voff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(base)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(base)
                  : "memory");
 }
 
 // The same of 4 bytes per lane, landing at lds + 4 l.
 __device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(base)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(base)
                  : "memory");
 }
 
