@@ -6,6 +6,12 @@
 // shift and an and-or per two codes), and the group's sum of x comes out of the matrix unit too, from a B operand of
 // ones, once for all rows of W: D - (1 + z / 16) S = (sum x q - z sum x) / 16, scaled by s into the fp32
 // accumulator, and by 16 at the end.
+// D and S are rounded apart. For a group whose codes are all its zero point (weights that are 0) what is left between them would be
+// multiplied by a scale that says nothing (1 where the quantizer found only zeros). So a wave that may have met such a group
+// goes through its tiles once more and takes each row's S with an operand of its 1 + z / 16: for such a group the same
+// operations as D, and D - S is 0. (So they are with ones where the zero point is 0.) What it looks for in the first pass is a
+// word of eight like codes, not 0, in each of a row's four lanes. (Rows' own sums in the first pass take 10% longer for M = 1 gate and up and 20% for M = 16, an exact
+// comparison of the codes 8% and 7%.)
 //
 // X is the A operand and W the B operand of v_mfma_f32_16x16x32_bf16: the result's column, a lane's low four bits, is
 // the row n, so a lane needs one scale for all four of its results. A lane's 16 bytes of a 16 x 128 tile of
@@ -249,7 +255,12 @@ struct Codes {
         const u32x4 o = {((w << 3) & mask) | one, ((w >> 1) & mask) | one, ((w >> 5) & mask) | one, ((w >> 9) & mask) | one};
         return __builtin_bit_cast(bf16x8, o);
     }
-    __device__ __forceinline__ bf16x8 ones() const { return __builtin_bit_cast(bf16x8, u32x4{one, one, one, one}); }
+    // an operand all of whose codes are q
+    __device__ __forceinline__ bf16x8 all_of(uint32_t q) const
+    {
+        const uint32_t two = __umul24(q, 0x00080008u) | one;
+        return __builtin_bit_cast(bf16x8, u32x4{two, two, two, two});
+    }
 };
 
 // Eight values of a row of X from k on; what is past K is 0 and not read.
@@ -264,23 +275,27 @@ __device__ __forceinline__ u32x4 load_x(const uint16_t* p, int64_t k, int64_t K)
 }
 
 // Sum over k of a tile's values with the codes, by groups, scaled into the accumulators. x[c][p]: operands of X. RES: results of
-// a lane that count.
-template <int RW, int CT, int PER, int RES>
+// a lane that count. OWN: the sums of x are taken for each row of W, with its 1 + z / 16; else with ones, and multiplied by that.
+template <int RW, int CT, int PER, int RES, bool OWN>
 __device__ __forceinline__ void multiply_tile(const Codes& k, const u32x4 (&x)[CT][4], const u32x4 (&w)[RW], const uint32_t (&meta)[RW][PER], floatx4 (&acc)[RW][CT])
 {
     constexpr int P = 4 / PER;  // operands per group
 #pragma unroll
     for (int g = 0; g < PER; g++) {
         floatx4 sum[CT];
+        auto sums = [&](const bf16x8& b) {
 #pragma unroll
-        for (int c = 0; c < CT; c++) {
-            sum[c] = floatx4{0.f, 0.f, 0.f, 0.f};
+            for (int c = 0; c < CT; c++) {
+                sum[c] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int p = 0; p < P; p++)
-                sum[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[c][g * P + p]), k.ones(), sum[c], 0, 0, 0);
-        }
+                for (int p = 0; p < P; p++)
+                    sum[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[c][g * P + p]), b, sum[c], 0, 0, 0);
+            }
+        };
+        if constexpr (!OWN) sums(k.all_of(0));
 #pragma unroll
         for (int i = 0; i < RW; i++) {
+            if constexpr (OWN) sums(k.all_of(meta[i][g] & 15u));
             floatx4 d[CT];
 #pragma unroll
             for (int c = 0; c < CT; c++) d[c] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -290,7 +305,7 @@ __device__ __forceinline__ void multiply_tile(const Codes& k, const u32x4 (&x)[C
 #pragma unroll
                 for (int c = 0; c < CT; c++) d[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[c][g * P + p]), b, d[c], 0, 0, 0);
             }
-            const float s = __uint_as_float(meta[i][g] & ~15u), z = __uint_as_float(0x3F800000u | (meta[i][g] & 15u) << 19);
+            const float s = __uint_as_float(meta[i][g] & ~15u), z = OWN ? 1.f : __uint_as_float(0x3F800000u | (meta[i][g] & 15u) << 19);
 #pragma unroll
             for (int c = 0; c < CT; c++)
 #pragma unroll
@@ -334,7 +349,8 @@ struct Skinny {
 };
 
 template <int XR, int RT, int U, int NW, int PER, bool UP>
-__global__ void __launch_bounds__(64 * NW) w4_skinny(W4Args a)
+// (16 rows with two groups a tile: held to the registers of two workgroups per CU, which it would miss by two)
+__global__ void __launch_bounds__(64 * NW, (XR == 16 && PER == 2 ? 4 : 1)) w4_skinny(W4Args a)
 {
     typedef Skinny<XR, RT, U, NW, UP> C;
     constexpr int RW = C::RW, CT = C::CT, RES = C::RES, SLOT = C::SLOT;
@@ -374,12 +390,16 @@ __global__ void __launch_bounds__(64 * NW) w4_skinny(W4Args a)
     const uint8_t* mine = lds + wave * U * SLOT;
 
     floatx4 acc[RW][CT];
+    auto clear = [&]() {
 #pragma unroll
-    for (int i = 0; i < RW; i++)
+        for (int i = 0; i < RW; i++)
 #pragma unroll
-        for (int c = 0; c < CT; c++) acc[i][c] = floatx4{0.f, 0.f, 0.f, 0.f};
+            for (int c = 0; c < CT; c++) acc[i][c] = floatx4{0.f, 0.f, 0.f, 0.f};
+    };
+    clear();
     u32x4 wv[U][RW];
     uint32_t sv[U][RW][PER];
+    uint64_t alike = 0;  // lanes that met a word of eight like codes other than 0 (of zero point 0, or of a row past N)
     auto load_w = [&](int u, uint32_t j) {
 #pragma unroll
         for (int i = 0; i < RW; i++) {
@@ -403,13 +423,21 @@ __global__ void __launch_bounds__(64 * NW) w4_skinny(W4Args a)
         for (int c = 0; c < CT; c++)
 #pragma unroll
             for (int p = 0; p < 4; p++) x[c][p] = *reinterpret_cast<const u32x4*>(mine + u * SLOT + c * 4096 + rd[p]);
-        multiply_tile<RW, CT, PER, RES>(k, x, wv[u], sv[u], acc);
+#pragma unroll
+        for (int i = 0; i < RW; i++)
+#pragma unroll
+            for (int g = 0; g < PER; g++) {
+                const uint32_t w = wv[u][i][g * (4 / PER)];
+                alike |= __ballot(w == __builtin_amdgcn_alignbit(w, w, 4)) & __ballot(w != 0);
+            }
+        multiply_tile<RW, CT, PER, RES, false>(k, x, wv[u], sv[u], acc);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     };
     const uint32_t full = static_cast<uint32_t>(a.K / 128);
     // tiles first, first + stride, ...: the waves of all slices take neighbouring ones
     const uint32_t first = blockIdx.z * NW + wave, stride = NW * a.slices;
     const uint32_t count = full > first ? (full - first + stride - 1) / stride : 0;
+    uint32_t slow = count;
     if (count > 0) {
         auto tile = [&](uint32_t i) { return first + stride * (i < count ? i : count - 1); };
 #pragma unroll
@@ -424,18 +452,28 @@ __global__ void __launch_bounds__(64 * NW) w4_skinny(W4Args a)
 #pragma unroll
         for (int u = 0; u < U; u++)
             if (done + u < count) step(u);
+        // A row whose four lanes (r, 16 + r, 32 + r, 48 + r) have all met like codes may have a group of zeros: from the beginning, with sums of
+        // each row's own.
+        const uint64_t half = alike & alike >> 32;
+        if (__builtin_expect((half & half >> 16 & 0xFFFFu) != 0, 0)) {
+            slow = 0;
+            clear();
+        }
     }
-    if (J > full && full % stride == first) {  // the tile that K ends inside
-        load_w(0, full);
+    // What is left: the tile that K ends inside, whose codes past K are 0 whatever the zero point.
+    const uint32_t left = J > full && full % stride == first ? count + 1 : count;
+    for (; slow < left; slow++) {
+        const uint32_t j = first + stride * slow;
+        load_w(0, j);
         u32x4 x[CT][4];
 #pragma unroll
         for (int c = 0; c < CT; c++)
 #pragma unroll
             for (int p = 0; p < 4; p++) {
                 const int row = 16 * c + xrow < rows ? 16 * c + xrow : rows - 1;
-                x[c][p] = load_x(x0 + static_cast<int64_t>(row) * a.ldx, static_cast<int64_t>(full) * 128 + 32 * p + 8 * c4, a.K);
+                x[c][p] = load_x(x0 + static_cast<int64_t>(row) * a.ldx, static_cast<int64_t>(j) * 128 + 32 * p + 8 * c4, a.K);
             }
-        multiply_tile<RW, CT, PER, RES>(k, x, wv[0], sv[0], acc);
+        multiply_tile<RW, CT, PER, RES, true>(k, x, wv[0], sv[0], acc);
     }
     // every transfer has landed before the ring becomes the waves' meeting place
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

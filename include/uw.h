@@ -637,7 +637,7 @@ size_t uw_sample_workspace(int64_t M, int64_t V);
  * read), Y [M][ldy] fp32 or bf16 (y_type; one rounding), by
  *   Y[m][n] = sum over groups g of  s[n][g] * (sum over k in g of x[m][k] q[n][k]  -  z[n][g] * sum over k in g of x[m][k])
  * with every sum in fp32 and no weight rounded. (The matrix unit takes 1 + q / 16 for q, so that a row's outputs
- * are NaN where it holds an infinity or a NaN.) Made for few rows, where W's bytes bound it. Larger M runs in blocks of 64
+ * are NaN where it holds an infinity or a NaN. A group whose codes are all its zero point adds exactly 0 to the others.) Made for few rows, where W's bytes bound it. Larger M runs in blocks of 64
  * rows that read W again: from about 512 (a large W) to 1500 rows on, uw_w4_expand and uw_recon_gemm are faster, with weights
  * rounded to bf16.
  *
