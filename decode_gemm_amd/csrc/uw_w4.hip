@@ -81,19 +81,22 @@ __device__ __forceinline__ V lanes_max(V v)
 }
 
 // a / 7 to 20 significant bits, the nearest, ties to even, for a >= 2^-100: the product with 1 / 7 rounded to 20 bits is at most
-// one step off, and the residual a - 7 c, exact, tells.
+// one step off, and the residual a - 7 c, exact, tells. Below a power of two the step is half as long (with that of the power itself
+// one mantissa in 2^23, 7 - 2^-18, came out one step too large).
 __device__ __forceinline__ float seventh20(float a)
 {
     const uint32_t c = (__float_as_uint(a * (1.0f / 7.0f)) + 8) & ~15u;
-    const float v = __uint_as_float(c), u = __uint_as_float((c & 0x7F800000u) - (19u << 23));  // a step of 20 bits
-    const float e = __builtin_fmaf(-7.0f, v, a), h = 3.5f * u;
+    const float v = __uint_as_float(c), e = __builtin_fmaf(-7.0f, v, a);
+    const float u = __uint_as_float((c & 0x7F800000u) - ((e < 0.f && !(c & 0x7FFFFFu) ? 20u : 19u) << 23)), h = 3.5f * u;  // a step of 20 bits
     return fabsf(e) > h || (fabsf(e) == h && (c & 16)) ? v + __builtin_copysignf(u, e) : v;
 }
 
 // w / s rounded to fp32 and then, by adding 1.5 * 2^23, to the nearest whole number, ties to even, which is left with that
 // number. The quotient is the correctly rounded one (inv = 1 / s is, and one residual step corrects it; s is not so small that the
-// residual underflows). Rounding twice is no loss: s has 20 bits, so T s is exact for a T halfway between two whole numbers
-// up to 15 and lies on w's grid, and a w beside it is a step of w away, more than half a step of the quotient.
+// residual underflows). Rounding twice is no loss, as no quotient but T itself becomes a T = t / 2 halfway between two whole numbers up to
+// 15. s is S 2^a with S < 2^20, so T s is the whole number t S of at most 25 bits times 2^(a-1), and a w beside it lies at least
+// that unit away, or, with fewer than 24 bits in t S, one of w's own steps. Over s that is more than 2^-21 in the first case and more than
+// 2^-24 T in the other: more than half of T's step.
 constexpr float kWhole = 12582912.0f;
 __device__ __forceinline__ float whole_quotient(float w, float s, float inv)
 {
