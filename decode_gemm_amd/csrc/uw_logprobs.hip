@@ -3,8 +3,8 @@
 //
 // Mathematics. With y_i = (l_i - max) log2(e) / T, S = sum 2^y_i and H = sum y_i 2^y_i: log p_t = (l_t - max) / T - log S
 // and the entropy is log S - log(2) H / S. One pass over the row keeps a running maximum with the sums below it: a
-// maximum that grows by d (in units of y) turns S into 2^-d S and H into 2^-d (H - d S). Sums of a thread's values are fp32, sums
-// over threads fp64. The rank counts l_i > l_t, and l_i >= l_t before t, in the same pass.
+// maximum that grows by d (in units of y) turns S into 2^-d S and H into 2^-d (H - d S). Sums of 128 of a thread's values are fp32, sums
+// of these and over threads fp64. The rank counts l_i > l_t, and l_i >= l_t before t, in the same pass.
 // The first n tokens are not sorted out of the row: of the maxima of 256 shares of the row, the n-th largest is
 // reached by at least n tokens and hardly more, and these, found by looking again into the shares of the threads
 // whose maximum reaches it, are sorted in LDS. Where ties make them too many, a search over the digits of
@@ -28,6 +28,7 @@ constexpr int kParts = 256;   // shares of a slice whose maxima are compared
 constexpr int kList = 2048;   // tokens that are sorted in LDS
 constexpr int kCounted = 512;  // as many are ordered by counting
 constexpr int kMostSlices = 8;
+constexpr int kRun = 8;  // steps of a thread whose sums are fp32: equal logits round the same way in every step
 constexpr double kLn2 = 0x1.62e42fefa39efp-1;
 constexpr u64 kNoKey = ~u64{0};
 
@@ -128,12 +129,13 @@ __device__ __forceinline__ float slope(float T)
 
 // Sums below a maximum `from` as sums below `top`, in units of its exponential. An infinite maximum leaves what is
 // finite no mass.
-__device__ __forceinline__ void rebase(float& S, float& H, float from, float top, float c2)
+template <class V>
+__device__ __forceinline__ void rebase(V& S, V& H, float from, float top, float c2)
 {
     if (from == top) return;
     const float y = fmaxf(__builtin_fmaf(from, 0.5f, -0.5f * top) * c2, -200.f);  // NaN too
     const float f = top == INFINITY ? 0.f : __builtin_amdgcn_exp2f(y);
-    H = f * __builtin_fmaf(y, S, H);
+    H = f * (H + y * S);
     S *= f;
 }
 
@@ -370,7 +372,8 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
     const float lt_before = placed ? below(lt) : INFINITY, lt_after = placed ? lt : INFINITY;
 
     float top = -INFINITY, S = 0.f, H = 0.f, v[U][VEC];
-    int before = 0;
+    double dS = 0.0, dH = 0.0;  // of kRun steps and kRun more ...
+    int before = 0, steps = 0;
     const bool counts = a.rank || greedy(temp);
     for (int i = first + tid; i < end; i += NT * U) {
 #pragma unroll
@@ -383,7 +386,17 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
         for (int u = 0; u < U; u++)
 #pragma unroll
             for (int k = 0; k < VEC; k++) now = fmaxf(now, v[u][k]);
-        if (now > top) rebase(S, H, top, now, c2);
+        if (steps == kRun) {
+            steps = 0;
+            dS += S;
+            dH += H;
+            S = H = 0.f;
+        }
+        steps++;
+        if (now > top) {
+            rebase(S, H, top, now, c2);
+            if (i >= first + kRun * NT * U) rebase(dS, dH, top, now, c2);
+        }
         top = now;
         if (top == INFINITY) {
 #pragma unroll
@@ -438,8 +451,11 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
     for (int i = 1; i < NT / 64; i++) p.top = fmaxf(p.top, sh.top[i]);
     p.given = lt;
     // ... and the sums below that maximum.
-    rebase(S, H, top, p.top, c2);
-    const double dS = wave_sum(static_cast<double>(S)), dH = wave_sum(static_cast<double>(H));
+    dS += S;
+    dH += H;
+    rebase(dS, dH, top, p.top, c2);
+    dS = wave_sum(dS);
+    dH = wave_sum(dH);
     before = wave_sum(before);
     if (lane == 0) {
         sh.S[wave] = dS;

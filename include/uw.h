@@ -745,8 +745,9 @@ uw_status uw_block_norm(const uw_block_norm_args* args, void* stream);
  * tokens the same; logits that are NaN or -inf have no mass and no place in the order; where some are +inf they share
  * the mass. A token without a place, or outside 0..V-1 (a padded position), has log probability -inf and rank -1. In the top
  * lists places past the last token of the order hold -1 and -inf. A row in which no token has a place gets entropy 0.
- * exp and its sums are fp32 within a few hundred values and fp64 from there on: log probabilities and
- * entropies are within about 1e-6 (and 2^-23 of their value). Ranks and top tokens come from comparisons
+ * exp and its sums are fp32 within 128 values and fp64 from there on: log probabilities are within about 1e-6
+ * (and 2^-24 of their value), and so are entropies, but for rows where one token stands against very many equal ones far
+ * below it (some 6e-6 in 2^20 tokens). Ranks and top tokens come from comparisons
  * alone and are exact. No result depends on the run; last bits of the others may be others in another batch or where a row
  * begins elsewhere.
  * d_ws: uw_logprobs_workspace(M, V, n_top) bytes, 16-byte aligned; free again when the call's work is done; calls
