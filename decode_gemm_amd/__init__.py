@@ -496,8 +496,7 @@ def _launch(t, stream, call, *args):
     """call(*args, stream) with the device of tensor t current and, without a stream, that device's
     current one. (Two lookups in torch's C layer: at batch size 1 the host's share of a call counts.)"""
     if t is None or isinstance(t, int) or not t.is_cuda:
-        if t is not None and not isinstance(t, int) and not t.is_pinned():
-            raise ValueError("a tensor in host memory that is not pinned: the GPU cannot read it")
+        _reachable(t)
         return _check(call(*args, _stream(stream)))
     global _torch
     if _torch is None:
@@ -512,12 +511,20 @@ def _launch(t, stream, call, *args):
 _torch = None
 
 
+def _reachable(*tensors):
+    """A ValueError for a tensor that the GPU cannot read."""
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and not t.is_cuda and not t.is_pinned():
+            raise ValueError("a tensor in host memory that is not pinned: the GPU cannot read it")
+
+
 def fp8_quantize(d_x, d_q, d_s, M: int, K: int, block_rows: int = 1, x_type: int | None = None, ldx: int | None = None,
                  ldq: int | None = None, lds: int | None = None, stream=None) -> None:
     """uw_fp8_quantize: e4m3 codes and fp32 scales of X [M][K], one scale per 128 values of a row
     (block_rows 1, scales [ceil(K / 128)][lds]) or per 128 x 128 block (block_rows 128, scales
     [ceil(M / 128)][lds]). x_type follows a tensor's dtype unless given."""
     st = lds if lds is not None else M if block_rows == 1 else (K + 127) // 128
+    _reachable(d_q, d_s)
     _launch(d_x, stream, lib.uw_fp8_quantize, _ptr(d_x), _type(d_x, x_type), M, K, K if ldx is None else ldx, block_rows,
             _ptr(d_q), K if ldq is None else ldq, _ptr(d_s), st)
 
@@ -525,6 +532,7 @@ def fp8_quantize(d_x, d_q, d_s, M: int, K: int, block_rows: int = 1, x_type: int
 def fp8_swiglu(d_g, d_u, d_q, d_s, M: int, K: int, ldg: int | None = None, ldu: int | None = None,
                ldq: int | None = None, lds: int | None = None, stream=None) -> None:
     """uw_fp8_swiglu: silu(g) * u of fp32 g and u, as e4m3 codes and row scales."""
+    _reachable(d_u, d_q, d_s)
     _launch(d_g, stream, lib.uw_fp8_swiglu, _ptr(d_g), K if ldg is None else ldg, _ptr(d_u), K if ldu is None else ldu, M, K,
             _ptr(d_q), K if ldq is None else ldq, _ptr(d_s), M if lds is None else lds)
 
@@ -549,6 +557,7 @@ def fp8_gemm(d_x, d_sx, d_w, d_sw, d_y, M: int, N: int, K: int, ldx: int | None 
     a = Fp8GemmArgs(M, N, K, _ptr(d_x), K if ldx is None else ldx, _ptr(d_sx), M if ldsx is None else ldsx, _ptr(d_w),
                     K if ldw is None else ldw, _ptr(d_sw), (K + 127) // 128 if ldsw is None else ldsw, _ptr(d_y),
                     N if ldy is None else ldy, _type(d_y, y_type), _ptr(d_ws), ws_bytes)
+    _reachable(d_sx, d_w, d_sw, d_y, d_ws)
     _launch(d_x, stream, lib.uw_fp8_gemm, ctypes.byref(a))
 
 
@@ -580,6 +589,8 @@ def sample(d_logits, d_u, d_token, M: int, V: int, ld: int | None = None, type: 
                    _elements("d_temperature", d_temperature, M), _elements("d_top_k", d_top_k, M, True),
                    _elements("d_top_p", d_top_p, M), _elements("d_min_p", d_min_p, M), _elements("d_token", d_token, M, True),
                    _elements("d_prob", d_prob, M), _ptr(d_ws), ws_bytes)
+    if not isinstance(d_logits, int):
+        _reachable(d_u, d_token, d_temperature, d_top_k, d_top_p, d_min_p, d_prob, d_ws)
     _launch(d_logits, stream, lib.uw_sample, ctypes.byref(a))
 
 
@@ -611,14 +622,17 @@ def w4_quantize(d_w, d_plane, N: int, K: int, group: int = 128, zeros: bool = Fa
                 w_type: int | None = None, stream=None) -> None:
     """uw_w4_quantize: the plane (w4_plane_bytes bytes) of W [N][K] in 4 bits with a scale, and with zeros a zero
     point, per group of 32, 64 or 128 values of a row."""
-    _launch(d_w, stream, lib.uw_w4_quantize, _ptr(d_w), _type(d_w, w_type), N, K, K if ldw is None else ldw, group, int(zeros),
-            _plane("d_plane", d_plane, N, K, group))
+    plane = _plane("d_plane", d_plane, N, K, group)
+    _reachable(d_plane)
+    _launch(d_w, stream, lib.uw_w4_quantize, _ptr(d_w), _type(d_w, w_type), N, K, K if ldw is None else ldw, group, int(zeros), plane)
 
 
 def w4_expand(d_plane, d_w, N: int, K: int, group: int = 128, ldw: int | None = None, w_type: int | None = None,
               stream=None) -> None:
     """uw_w4_expand: the values of a plane as W [N][K] (fp32, exact, or bf16, by the dtype of d_w unless w_type is given)."""
-    _launch(d_w, stream, lib.uw_w4_expand, _plane("d_plane", d_plane, N, K, group), N, K, group, _ptr(d_w), _type(d_w, w_type),
+    plane = _plane("d_plane", d_plane, N, K, group)
+    _reachable(d_plane)
+    _launch(d_w, stream, lib.uw_w4_expand, plane, N, K, group, _ptr(d_w), _type(d_w, w_type),
             K if ldw is None else ldw)
 
 
@@ -632,6 +646,7 @@ def w4_gemm(d_x, d_plane, d_y, M: int, N: int, K: int, group: int = 128, ldx: in
     of 4-bit weights. d_ws: w4_gemm_workspace(M, N, K) bytes; with fewer K is cut into fewer slices, without it never."""
     a = _pack_w4(M, N, K, group, _bf16("d_x", d_x), K if ldx is None else ldx, _plane("d_plane", d_plane, N, K, group), 0, _at(d_y),
                  N if ldy is None else ldy, _type(d_y, y_type), _at(d_ws), ws_bytes)
+    _reachable(d_plane, d_y, d_ws)
     _launch(d_x, stream, lib.uw_w4_gemm, a)
 
 
@@ -641,6 +656,7 @@ def w4_gate_up(d_x, d_gate, d_up, d_h, M: int, N: int, K: int, group: int = 128,
     w4_gemm_workspace(M, 2 * N, K) bytes, as for w4_gemm."""
     a = _pack_w4(M, N, K, group, _bf16("d_x", d_x), K if ldx is None else ldx, _plane("d_gate", d_gate, N, K, group),
                  _plane("d_up", d_up, N, K, group), _bf16("d_h", d_h), N if ldh is None else ldh, BF16, _at(d_ws), ws_bytes)
+    _reachable(d_gate, d_up, d_h, d_ws)
     _launch(d_x, stream, lib.uw_w4_gate_up, a)
 
 
@@ -704,6 +720,7 @@ def block_norm(d_y, d_r, d_r_out, M: int, K: int, d_h=None, d_q=None, d_s=None, 
         0 if d_pre_w is None else _vector("d_pre_w", d_pre_w), 0 if d_pre_b is None else _vector("d_pre_b", d_pre_b), 0 if d_gate is None else _at(d_gate),
         gate_rows, K if ldgate is None else ldgate, w_type, w_add, scale_y, scale_r, eps, _at(h), K if ldh is None else ldh, h_type,
         _at(d_s), M if lds is None else lds)
+    _reachable(d_r, d_r_out, d_post_w, d_post_b, d_pre_w, d_pre_b, d_gate, h, d_s)
     _launch(d_y if d_y is not None else d_r, stream, lib.uw_block_norm, a)
 
 
@@ -724,6 +741,7 @@ def logprobs(d_logits, M: int, V: int, d_token=None, d_logprob=None, d_rank=None
                        _elements("d_rank", d_rank, M, True) or 0, _elements("d_entropy", d_entropy, M) or 0, n_top,
                        _elements("d_top_token", d_top_token, M * n_top, True) or 0,
                        _elements("d_top_logprob", d_top_logprob, M * n_top) or 0, _at(d_ws), ws_bytes)
+    _reachable(d_token, d_temperature, d_logprob, d_rank, d_entropy, d_top_token, d_top_logprob, d_ws)
     _launch(d_logits, stream, lib.uw_logprobs, a)
 
 
