@@ -119,21 +119,25 @@ struct Words {
     __device__ __forceinline__ void load(int i, float (&v)[VEC]) const { unpack(raw(i), v); }
 };
 
-// 2 log2(e) / T, of halved differences, which cannot overflow; 0 where all tokens weigh the same or (T <= 0, NaN)
-// the sums are not used.
+// log2(e) / T as two factors: y = (unit (l - top)) slope. The unit is 1/2, so that differences cannot overflow; at temperatures below
+// 2^-100, where the slope would, it is 2^23 beside a maximum below 1 (what is then past fp32's range has no mass), and beside a larger one
+// still 1/2, whose product with any difference that is not 0 is past the mass too.
+// The slope is 0 where all tokens weigh the same or (T <= 0, NaN) the sums are not used.
+__device__ __forceinline__ bool tiny(float T) { return T < 0x1p-100f && T > 0.f; }
+__device__ __forceinline__ float unit(float top, bool tiny) { return tiny && fabsf(top) < 1.f ? 0x1p23f : 0.5f; }
 __device__ __forceinline__ float slope(float T)
 {
     if (!(T > 0.f) || T > FLT_MAX) return 0.f;
-    return static_cast<float>(fmin(2.8853900817779268 / static_cast<double>(T), 3.0e38));
+    return static_cast<float>(1.4426950408889634 / static_cast<double>(T) * (tiny(T) ? 0x1p-23 : 2.0));
 }
 
-// Sums below a maximum `from` as sums below `top`, in units of its exponential. An infinite maximum leaves what is
+// Sums below a maximum `from` as sums below `top`, in units of its exponential; h is top's unit. An infinite maximum leaves what is
 // finite no mass.
 template <class V>
-__device__ __forceinline__ void rebase(V& S, V& H, float from, float top, float c2)
+__device__ __forceinline__ void rebase(V& S, V& H, float from, float top, float c, float h)
 {
     if (from == top) return;
-    const float y = fmaxf(__builtin_fmaf(from, 0.5f, -0.5f * top) * c2, -200.f);  // NaN too
+    const float y = fmaxf(__builtin_fmaf(from, h, -h * top) * c, -200.f);  // NaN too
     const float f = top == INFINITY ? 0.f : __builtin_amdgcn_exp2f(y);
     H = f * (H + y * S);
     S *= f;
@@ -366,6 +370,7 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
 #pragma unroll
     for (int u = 0; u < U; u++) next[u] = first + tid + u * NT < end ? w.raw(first + tid + u * NT) : Words<T>::nothing();
     const float temp = a.temperature ? a.temperature[m] : 1.f, c2 = slope(temp);
+    const bool small = tiny(temp);
     const int t = a.token ? a.token[m] : -1;
     const float lt = t >= 0 && t < a.V ? value(x, t) : -INFINITY;
     const bool placed = lt > -INFINITY;
@@ -394,8 +399,8 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
         }
         steps++;
         if (now > top) {
-            rebase(S, H, top, now, c2);
-            if (i >= first + kRun * NT * U) rebase(dS, dH, top, now, c2);
+            rebase(S, H, top, now, c2, unit(now, small));
+            if (i >= first + kRun * NT * U) rebase(dS, dH, top, now, c2, unit(now, small));
         }
         top = now;
         if (top == INFINITY) {
@@ -404,13 +409,13 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
 #pragma unroll
                 for (int k = 0; k < VEC; k++) S += v[u][k] == top ? 1.f : 0.f;
         } else {
-            const float half = 0.5f * top;
+            const float h2 = unit(top, small), scaled = h2 * top;
             float s = 0.f, h = 0.f;
 #pragma unroll
             for (int u = 0; u < U; u++)
 #pragma unroll
                 for (int k = 0; k < VEC; k++) {
-                    const float y = fmaxf(__builtin_fmaf(v[u][k], 0.5f, -half) * c2, -200.f);  // a mask's NaN too
+                    const float y = fmaxf(__builtin_fmaf(v[u][k], h2, -scaled) * c2, -200.f);  // a mask's NaN too
                     const float e = __builtin_amdgcn_exp2f(y);
                     s += e;
                     h = __builtin_fmaf(y, e, h);
@@ -453,7 +458,7 @@ __global__ void __launch_bounds__(NT) logprobs_rows(LogprobArgs a)
     // ... and the sums below that maximum.
     dS += S;
     dH += H;
-    rebase(dS, dH, top, p.top, c2);
+    rebase(dS, dH, top, p.top, c2, unit(p.top, small));
     dS = wave_sum(dS);
     dH = wave_sum(dH);
     before = wave_sum(before);
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(kJoinThreads) logprobs_join(LogprobArgs a)
     if (lane < slices) p = a.part[m * slices + lane];
     const float top = wave_max(p.top);
     if (p.top != top) {
-        const double y = fmax((0.5 * p.top - 0.5 * top) * c2, -1100.0);  // NaN too
+        const double h = unit(top, tiny(temp)), y = fmax((h * p.top - h * top) * c2, -1100.0);  // NaN too
         const double f = top == INFINITY ? 0.0 : exp2(y);
         p.H = f * (p.H + y * p.S);
         p.S *= f;

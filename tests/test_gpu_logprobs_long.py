@@ -100,3 +100,18 @@ def test_slices_with_outputs_left_out():
         alone = torch.zeros_like(whole)
         uw.logprobs(x, M, V, d_token=t if name in ("d_logprob", "d_rank") else None, n_top=n if "top" in name else 0, d_ws=ws, ws_bytes=need, **{name: alone})
         assert torch.equal(alone, whole), name
+
+
+@pytest.mark.parametrize("V", [300, 9000, 60_000])
+def test_temperatures_below_the_normal_numbers(V):
+    """Logits that lie a few such temperatures apart, and others far off, of either sign and up to fp32's ends."""
+    rng = np.random.default_rng(V)
+    T = np.resize(np.array([2.0**-149, 1e-44, 1e-41, 1e-39, 1.17e-38, 1.2e-38, 1e-37], np.float32), 14)
+    x = (rng.standard_normal((14, V)) * 8 * T[:, None]).astype(np.float32)
+    x[:, ::7] = -np.inf
+    x[1, 3], x[2, 5], x[3, 8], x[4, 9] = -3e38, -1.0, 1e-30, 0.75
+    x[5, 4], x[5, 6] = 2.0, 2.0
+    x[6, 10], x[6, 11] = 3e38, np.inf
+    x[7] += np.float32(1.5)
+    x[8, 2], x[8, 1] = 1.0, np.nextafter(np.float32(1), np.float32(0))
+    run(x, np.where(np.arange(14) % 2, rng.integers(0, V, 14), 3), 6, T=T)
