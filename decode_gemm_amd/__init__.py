@@ -712,6 +712,8 @@ def block_norm(d_y, d_r, d_r_out, M: int, K: int, d_h=None, d_q=None, d_s=None, 
         h, h_type = d_q, E4M3
         if not isinstance(d_q, int) and d_q.element_size() != 1:
             raise ValueError(f"d_q must hold bytes, not {d_q.dtype}")
+        if d_s is not None and not isinstance(d_s, int) and str(d_s.dtype) != "torch.float32":
+            raise ValueError(f"d_s must be fp32, not {d_s.dtype}")
     w_type = _same_type("weights, biases and gate", w_type, (d_post_w, d_post_b, d_pre_w, d_pre_b, d_gate))
     a = _pack_block_norm(
         M, K, _at(d_y), K if ldy is None else ldy, _same_type("d_y", y_type, (d_y,)), _at(d_r), K if ldr is None else ldr,

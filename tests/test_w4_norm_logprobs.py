@@ -233,3 +233,10 @@ def test_host_memory_is_refused():
                  lambda: uw.logprobs(w, 4, 256, d_entropy=torch.zeros(4), stream=0)):
         with pytest.raises(ValueError, match="host memory"):
             call()
+
+
+def test_scales_of_codes_are_fp32():
+    f32, q = torch.ones(4), torch.zeros(4, dtype=torch.uint8)
+    for wrong in (torch.ones(4, dtype=torch.bfloat16), torch.ones(4, dtype=torch.float64)):
+        with pytest.raises(ValueError, match="d_s"):
+            uw.block_norm(f32, None, None, 1, 4, d_q=q, d_s=wrong, stream=0)
