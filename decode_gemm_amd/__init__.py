@@ -514,7 +514,7 @@ _torch = None
 def _reachable(*tensors):
     """A ValueError for a tensor that the GPU cannot read."""
     for t in tensors:
-        if t is not None and not isinstance(t, int) and not t.is_cuda and not t.is_pinned():
+        if not getattr(t, "is_cuda", True) and not t.is_pinned():  # (None and raw addresses have no such attribute)
             raise ValueError("a tensor in host memory that is not pinned: the GPU cannot read it")
 
 
@@ -608,13 +608,15 @@ def _at(t) -> int:
 
 
 def _plane(name: str, t, N: int, K: int, group: int) -> int:
-    """Address of a plane, whose tensor must be as large as the sizes say (w4_plane_bytes) and in one piece."""
+    """Address of a plane, whose tensor must be as large as the sizes say (w4_plane_bytes), in one piece and on the GPU."""
     if t is None or isinstance(t, int):
         return t or 0
     if group in (32, 64, 128):  # others are the library's to refuse
         need = (N + 15) // 16 * ((K + 127) // 128) * (1024 + 8192 // group)
         if t.nbytes < need or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous tensor of {need} bytes")
+    if not t.is_cuda:
+        _reachable(t)
     return t.data_ptr()
 
 
@@ -622,17 +624,14 @@ def w4_quantize(d_w, d_plane, N: int, K: int, group: int = 128, zeros: bool = Fa
                 w_type: int | None = None, stream=None) -> None:
     """uw_w4_quantize: the plane (w4_plane_bytes bytes) of W [N][K] in 4 bits with a scale, and with zeros a zero
     point, per group of 32, 64 or 128 values of a row."""
-    plane = _plane("d_plane", d_plane, N, K, group)
-    _reachable(d_plane)
-    _launch(d_w, stream, lib.uw_w4_quantize, _ptr(d_w), _type(d_w, w_type), N, K, K if ldw is None else ldw, group, int(zeros), plane)
+    _launch(d_w, stream, lib.uw_w4_quantize, _ptr(d_w), _type(d_w, w_type), N, K, K if ldw is None else ldw, group, int(zeros),
+            _plane("d_plane", d_plane, N, K, group))
 
 
 def w4_expand(d_plane, d_w, N: int, K: int, group: int = 128, ldw: int | None = None, w_type: int | None = None,
               stream=None) -> None:
     """uw_w4_expand: the values of a plane as W [N][K] (fp32, exact, or bf16, by the dtype of d_w unless w_type is given)."""
-    plane = _plane("d_plane", d_plane, N, K, group)
-    _reachable(d_plane)
-    _launch(d_w, stream, lib.uw_w4_expand, plane, N, K, group, _ptr(d_w), _type(d_w, w_type),
+    _launch(d_w, stream, lib.uw_w4_expand, _plane("d_plane", d_plane, N, K, group), N, K, group, _ptr(d_w), _type(d_w, w_type),
             K if ldw is None else ldw)
 
 
@@ -646,7 +645,7 @@ def w4_gemm(d_x, d_plane, d_y, M: int, N: int, K: int, group: int = 128, ldx: in
     of 4-bit weights. d_ws: w4_gemm_workspace(M, N, K) bytes; with fewer K is cut into fewer slices, without it never."""
     a = _pack_w4(M, N, K, group, _bf16("d_x", d_x), K if ldx is None else ldx, _plane("d_plane", d_plane, N, K, group), 0, _at(d_y),
                  N if ldy is None else ldy, _type(d_y, y_type), _at(d_ws), ws_bytes)
-    _reachable(d_plane, d_y, d_ws)
+    _reachable(d_y, d_ws)
     _launch(d_x, stream, lib.uw_w4_gemm, a)
 
 
@@ -656,7 +655,7 @@ def w4_gate_up(d_x, d_gate, d_up, d_h, M: int, N: int, K: int, group: int = 128,
     w4_gemm_workspace(M, 2 * N, K) bytes, as for w4_gemm."""
     a = _pack_w4(M, N, K, group, _bf16("d_x", d_x), K if ldx is None else ldx, _plane("d_gate", d_gate, N, K, group),
                  _plane("d_up", d_up, N, K, group), _bf16("d_h", d_h), N if ldh is None else ldh, BF16, _at(d_ws), ws_bytes)
-    _reachable(d_gate, d_up, d_h, d_ws)
+    _reachable(d_h, d_ws)
     _launch(d_x, stream, lib.uw_w4_gate_up, a)
 
 
