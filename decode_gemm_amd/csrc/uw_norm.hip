@@ -1,12 +1,12 @@
 // The norm after a block, its gate and scale, the residual stream and the norm before the next block,
 // in one pass: v = post(y), r' = scale_r r + scale_y gate v, h = pre(r').
 //
-// Mathematics. A row lies in the registers of its threads from the first load to the last store, so y and r
-// are read once and r' and h written once, which is all that the step has to move; the sums that a norm needs
+// Mathematics. Up to 16384 values a row lies in the registers of its threads from the first load to the last store, so y and r
+// are read once and r' and h written once, which is all that the step has to move (longer rows: see launch_shape); the sums that a norm needs
 // are reduced over lanes by rotations, over waves in LDS. A layer norm takes the mean first and then the squares of
 // the differences from it (two reductions): the difference of two sums of squares would lose the variance of a
-// row whose mean is large. HBM-bound for many rows (4096 x 4096 of fp32 y and bf16 r into bf16 r' and h 35.5 us, 168 MB, 4.7 TB/s; into
-// codes 35.8, 151 MB; a large copy reaches 5.1), a launch, the loads and two reductions for few (1 x 4096 3.8 us).
+// row whose mean is large. HBM-bound for many rows (4096 x 4096 of fp32 y and bf16 r into bf16 r' and h 34.2 us, 168 MB, 4.9 TB/s; into
+// codes 35.8, 151 MB, with a gate 37.5 to 40.7; a large copy reaches 5.1), a launch, the loads and two reductions for few (1 x 4096 3.8 us).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -308,6 +308,9 @@ uw_status launch(const NormArgs& a, hipStream_t s)
 // values per thread, so that more rows are in a CU at once (us, cold, y fp32, r bf16 and h in codes; few- and many-row shape:
 // 1 x 4096 3.8 and 5.0, 64 x 8192 6.5 and 9.5, 512 x 4096 9.2 and 9.2, 4096 x 4096 40.5 and 35.8, 4096 x 8192 100 and 72). Workgroups
 // that stay, keep the vectors and have the next row on the way took 38.1 and 78 for the last two.
+// Past 16384 values a thread of a workgroup of 1024 has more of them than its 128 registers hold, and part goes through scratch memory (212
+// bytes per thread up to 32768, 848 past that): fp32 y, bf16 r, r' and h, 4096 x 16384 157 us (4.3 TB/s), 2048 x 28672 254 (2.3), 1024 x 65536 865 (0.8),
+// one row of 28672 20.7, of 65536 123.
 uw_status launch_shape(const NormArgs& a, hipStream_t s)
 {
     if (a.K <= 512) return launch<1, 1>(a, s);

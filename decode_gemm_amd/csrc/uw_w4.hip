@@ -341,9 +341,11 @@ __device__ __forceinline__ void store_y(const W4Args& a, int64_t m, int64_t n, f
 // all banks. Transfer q covers rows 4 q .. 4 q + 3, lane l landing at 16 l.
 // Order: a tile's transfers are issued before its load of W, loads and transfers return in order, so a wait for W (an empty
 // asm that uses it) is one for X; reads of a slot are waited for before it is filled again.
-// Measured, W from memory (24 matrices in turn) and from the cache behind the L2: M = 1, N = 14336, K = 4096 8.5 and 6.8 us (31 MB, 3.7 and
-// 4.6 TB/s), gate and up of that with the activation 14.2 and 12.4 (62 MB, 4.4 and 5.0), N = 4096, K = 14336 8.5 and 6.3; M = 16 10.1 and
-// 8.0; M = 64 17.5 and 15.6. W's stream bounds it up to 16 rows, vector operations and matrix cores, one after the other, at 64.
+// Measured, W from memory (24 matrices in turn) and from the cache behind the L2: M = 1, N = 4096, K = 14336 8.7 and 6.6 us (31 MB, 3.6 and 4.7
+// TB/s), gate and up of N = 14336, K = 4096 with the activation 13.6 and 12.5 (62 MB, 4.6 and 5.0); N = 14336, K = 4096 with M = 16 11.3 and 8.6,
+// M = 32 12.7 and 10.6, M = 64 18.5 and 16.4, gate and up of it 22.1 and 20.2 with M = 32, 32.4 and 30.5 with M = 64. W's stream bounds it up to 16
+// rows, vector operations and matrix cores, one after the other, at 64.
+// Planes that have groups of zeros (1% of all, or 48 rows) take the second pass, tile by tile: M = 1 9 -> 10 to 13 us, M = 32 12.7 -> 20, M = 64 18.4 -> 33.
 template <int XR, int RT, int U, int NW, bool UP>
 struct Skinny {
     static constexpr int RW = UP ? 2 * RT : RT, CT = XR >= 16 ? XR / 16 : 1, RES = XR >= 16 ? 4 : 1;
@@ -547,6 +549,7 @@ hipError_t launch_skinny(const W4Args& a, int32_t group, hipStream_t s)
 }
 
 // Row tiles per workgroup and K slices of a product with more than four rows.
+//   (Figures of the kernels before they looked for groups of zeros, which takes 2 to 3% but at M = 32, 7% less.)
 //   Row tiles: more of them read X less often, and leave fewer workgroups. In us, W from memory, at K = 4096 (2000 for N = 5003), N = 4096 /
 //   5003 / 14336 with 1, 2 and 4 row tiles: M = 16 4.9 5.8 7.2 / 5.5 5.0 6.2 / 14.4 10.9 10.1, M = 32 6.0 7.1 9.9 / 7.3 6.3 7.7 /
 //   20.3 14.9 12.9, M = 64 9.6 10.1 13.7 / 14.8 9.4 11.9 / 35.9 23.6 17.9. So four where that leaves 192 workgroups or

@@ -637,9 +637,10 @@ size_t uw_sample_workspace(int64_t M, int64_t V);
  * read), Y [M][ldy] fp32 or bf16 (y_type; one rounding), by
  *   Y[m][n] = sum over groups g of  s[n][g] * (sum over k in g of x[m][k] q[n][k]  -  z[n][g] * sum over k in g of x[m][k])
  * with every sum in fp32 and no weight rounded. (The matrix unit takes 1 + q / 16 for q, so that a row's outputs
- * are NaN where it holds an infinity or a NaN. A group whose codes are all its zero point adds exactly 0 to the others.) Made for few rows, where W's bytes bound it. Larger M runs in blocks of 64
- * rows that read W again: from about 512 (a large W) to 1500 rows on, uw_w4_expand and uw_recon_gemm are faster, with weights
- * rounded to bf16.
+ * are NaN where it holds an infinity or a NaN.) A group whose codes are all its zero point adds exactly 0; planes that
+ * have such groups with a zero point other than 0 take up to 1.8 times as long. Made for few rows, where W's bytes bound
+ * it. Larger M runs in blocks of 64 rows that read W again: from about 512 (a large W) to 1500 rows on, uw_w4_expand and
+ * uw_recon_gemm are faster, with weights rounded to bf16.
  *
  * uw_w4_gate_up (device). h = bf16(silu(X Wg^T) * (X Wu^T)) [M][ldh], both planes N x K with the same group: the
  * two products and the activation of uw_swiglu in one pass over X, the products not rounded on the way.
@@ -698,7 +699,7 @@ size_t uw_w4_gemm_workspace(int64_t M, int64_t N, int64_t K);
  * neither used nor written.
  * Errors: UW_ESHAPE (M < 0, K < 1), UW_EINVAL (NULL pointers as above; misaligned ones: 16 bytes, scales 4; leading dimensions below
  * K or that do not keep rows 16-byte aligned; an unknown type or norm; gate_rows < 0; eps not a finite number >= 0),
- * UW_EUNSUPPORTED (K > UW_NORM_MAX_K, M >= 2^31, more rows than one launch takes: 2^22 always are), UW_EHIP. M = 0 is a no-op.
+ * UW_EUNSUPPORTED (K > UW_NORM_MAX_K, M >= 2^31, more rows than one launch takes: fewer than 2^22 never are), UW_EHIP. M = 0 is a no-op.
  */
 #define UW_NORM_MAX_K 65536
 typedef enum { UW_NORM_NONE = 0, UW_NORM_RMS = 1, UW_NORM_LAYER = 2 } uw_norm;
